@@ -50,6 +50,23 @@ typedef int32_t idx_status;
 /* operation codes for idx_workspace_size */
 #define IDX_OP_BUILD_POOL 1
 #define IDX_OP_TOPK 2
+#define IDX_OP_ATTEND 3   /* nq queries, max_n list slots or positions attended to, k = heads */
+#define IDX_OP_DISTILL 4  /* nq rows of at most max_n scores; any valid k */
+
+/* element types of idx_rope */
+#define IDX_BF16 0
+#define IDX_F32 1
+
+/* pairs of idx_rope: (i, i + rot / 2), or (2i, 2i + 1) */
+#define IDX_ROPE_HALF 0
+#define IDX_ROPE_INTERLEAVED 1
+#define IDX_MAX_ROT 8192
+
+/* frequencies of idx_rope_freqs */
+#define IDX_ROPE_PLAIN 0
+#define IDX_ROPE_LINEAR 1
+#define IDX_ROPE_NTK 2
+#define IDX_ROPE_YARN 3
 
 /* Version of this ABI (IDX_ABI_VERSION). */
 int32_t idx_abi_version(void);
@@ -357,6 +374,152 @@ idx_status idx_quantize_kv(const uint16_t* x_bf16, int64_t rows, uint8_t* codes,
  */
 idx_status idx_gather_kv(const uint8_t* codes, const uint8_t* scales, const int64_t* kv_base, const int32_t* n_vis,
                          int32_t nq, const int32_t* idx, int64_t idx_stride, int32_t k, uint16_t* out, void* stream);
+
+/*
+ * Rotary positions, for the rows that idx_quantize_q, idx_quantize_kv and idx_attend take.
+ *
+ * idx_rope_freqs: the rotation per position of each pair, freq[i] for i < rot / 2, in radians (host
+ * memory, double; the caller copies it to the device once), and the factor on sin and cos that goes with it.
+ * With f_i = base^(-2i / rot):
+ *   IDX_ROPE_PLAIN  : f_i (factor, original, fast and slow are not used);
+ *   IDX_ROPE_LINEAR : f_i / factor (positions squeezed into the trained range);
+ *   IDX_ROPE_NTK    : f_i of the base base * factor^(rot / (rot - 2)): the slowest pair as LINEAR, the
+ *                     fastest unchanged;
+ *   IDX_ROPE_YARN   : by the turns r_i = original * f_i / 2 pi that a pair makes over the trained length:
+ *                     f_i * g + f_i / factor * (1 - g), g = clamp((r_i - slow) / (fast - slow), 0, 1), and
+ *                     mscale = 0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension
+ *                     of Large Language Models", 2023, equations for the interpolation by parts; there
+ *                     fast = 32 and slow = 1).
+ * mscale is 1 for the other three. No HIP call is made.
+ *
+ *   rot    : even, 2 .. 8192 (above 2 for NTK).
+ *   base   : above 1.   factor : at least 1.   original : above 0.   fast > slow.
+ */
+idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double original, double fast,
+                          double slow, double* freq, float* mscale);
+
+/*
+ * idx_rope: rotate the values offset .. offset + rot - 1 of every row by the angles a_i = pos * freq[i]:
+ *
+ *   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a)
+ *
+ * for each pair (x0, x1) of the layout, m = mscale; the row's other values are copied. inverse != 0 turns by
+ * -a: the gradient of the call without it (dx from dy, same mscale), or the way back (mscale = 1 / m).
+ * Angles are reduced in 64 bits, products are fp32, rounded once.
+ *
+ *   x       : device, dtype IDX_BF16 (bit patterns) or IDX_F32, [tokens][heads][dim]; a row's values are
+ *             consecutive, x_token and x_head are the element strides of the other two axes (0 repeats).
+ *   pos     : device int64 [tokens], any order, repeats allowed. Angles are good to 2^-21 rad up to |pos| = 2^31
+ *             (freq at most 1).
+ *   freq    : device double [rot / 2].
+ *   rot     : even, 2 .. 8192; offset >= 0, offset + rot <= dim.
+ *   out     : device, x's dtype; strides out_token, out_head (at least dim where the axis is longer than 1,
+ *             so that rows do not overlap). May be x itself with x's strides: then only the rotated part is
+ *             read and written. Otherwise out may not overlap x.
+ *   tokens  : 0 .. 2^31 - 1 (0 enqueues nothing); heads 1 .. 65535; dim 2 .. 2^20.
+ */
+idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads, int32_t dim, int64_t x_token,
+                    int64_t x_head, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
+                    int32_t layout, float mscale, int32_t inverse, void* out, int64_t out_token, int64_t out_head,
+                    void* stream);
+
+/*
+ * idx_attend: core attention over the FP4 main-KV cache (the layout of idx_quantize_kv); a row of 512 values
+ * is key and value at once, shared by all heads:
+ *
+ *   s_{h,i} = scale * q_h . kv_i,   lse_h = log sum_i exp(s_{h,i}),   out_h = sum_i exp(s_{h,i} - lse_h) kv_i
+ *
+ * over the entries i of the query. The method's core attention reads the selected entries of the cache
+ * ([P1] "the scale format decides precision": the main-KV format is read back before attention); here they
+ * are read back inside the call, which replaces idx_gather_kv and a product over its output.
+ *
+ *   q       : device bf16 [nq][heads][512], 16-byte aligned; heads 1 .. 128, nq 0 .. 65535.
+ *   codes, scales, rows : device main-KV cache, [rows][256] (16-byte aligned) and [rows][32] (2-byte aligned),
+ *             rows 0 .. 2^31 - 1.
+ *   kv_base : device int64 [nq]: position p of query t is row kv_base[t] + p; or NULL with pages.
+ *   pages   : device int32 [nseq][pages_stride], or NULL with kv_base: position p of query t is row
+ *             pages[seq[t]][p / page_size] * page_size + p % page_size. page_size >= 1,
+ *             pages_stride >= ceil(max_n / page_size).
+ *   seq     : device int32 [nq], or NULL (query t is of sequence t, nseq >= nq).
+ *   n_vis   : device int32 [nq]; n_t = min(max(n_vis[t], 0), max_n) positions are visible: for a chunk of new
+ *             tokens, each one's own position + 1. max_n 0 .. 2^30.
+ *   idx     : device int32 [nq][idx_stride] or NULL. Given (idx_topk's output): the entries are the slots
+ *             idx[t][0 .. k - 1], idx_stride >= k, k 0 .. 2^24; a position outside [0, n_t) (the -1 padding) is
+ *             left out, a position given twice counts twice. NULL: the entries are all n_t positions, or the
+ *             last min(window, n_t) with window > 0 (window is 0 with idx).
+ *   scale   : finite.
+ *   out     : device bf16 [nq][heads][512], 16-byte aligned (written).
+ *   lse     : device fp32 [nq][heads] or NULL (written; natural logarithm).
+ *   ws, ws_bytes : at least idx_workspace_size(IDX_OP_ATTEND, nq, entries, heads) bytes, 16-byte aligned, with
+ *             entries = k, or the window where one is given and shorter than max_n, or max_n. It holds nothing
+ *             between calls; calls that may run concurrently need separate workspaces.
+ *
+ * An entry whose row is outside [0, rows), whose page is negative, or whose seq is outside [0, nseq) is left
+ * out; what the cache holds there or at masked entries has no effect. A query without entries gets out = 0 and
+ * lse = -inf. Products are exact in fp16 operands (q scaled by a power of two per row; values below 2^-28 of the
+ * row's largest lose low bits), sums, maximum and normalisation fp32; probabilities are rounded to 11 bits for
+ * the second product. A non-finite value in a q row makes that head's results NaN and no other's.
+ */
+idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes, const uint8_t* scales,
+                      int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,
+                      int32_t page_size, const int32_t* seq, const int32_t* n_vis, int64_t max_n, int64_t window,
+                      const int32_t* idx, int64_t idx_stride, int32_t k, float scale, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * idx_attend_weights: the probability that the attention gives each entry, mean over the heads,
+ *
+ *   w_{t,i} = 1/heads sum_h exp(s_{t,h,i} - lse_{t,h})
+ *
+ * recomputed from lse (idx_attend's, or one that also covers other caches). The indexer is trained towards
+ * it ([P3] Q&A: the divergence of the indexer from the main attention; idx_distill).
+ *
+ *   Arguments as for idx_attend (without a window).
+ *   lse     : device fp32 [nq][heads]; a head with lse = -inf (nothing attended) adds nothing.
+ *   weights : device fp32 [nq][w_stride] (written): with idx, w_stride >= k and slot i holds entry i's weight,
+ *             0 for entries left out; without, w_stride >= max_n and weights[t][p] is written for p < n_t only.
+ */
+idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes,
+                              const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                              int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq,
+                              const int32_t* n_vis, int64_t max_n, const int32_t* idx, int64_t idx_stride, int32_t k,
+                              float scale, const float* lse, float* weights, int64_t w_stride, void* stream);
+
+/*
+ * idx_distill: the divergence of score rows (idx_score_full's) from a teacher that gives its top logits:
+ *
+ *   loss_t = sum_i p_i (log p_i - log q_{x_i}),  p = softmax over the teacher's entries of t_logit * inv_temp,
+ *            q = softmax over the row of scores * inv_temp
+ *
+ * ([P3] Q&A: the indexer learns from the main attention by a KL divergence, first over all positions, then
+ * over the selected ones). A row's positions are those below n_t with a score above -inf (so a row masked by
+ * idx_mask_pool is normalised over its pool). The teacher's entries are the slots x_i = t_idx[t][i] that name
+ * such a position and whose logit is above -inf; the others (the -1 padding) are left out, and a position given
+ * twice counts twice. A row without entries has loss 0.
+ *
+ *   scores  : device fp32 [nq][score_stride], score_stride >= max_n.   n_vis, max_n : as above.
+ *   t_idx   : device int32 [nq][t_stride]; t_logit : device fp32 [nq][t_stride]; k 0 .. 2048 slots, t_stride >= k.
+ *   inv_temp: 1 / T, above 0; scores and logits times it stay in fp32's range.
+ *   loss, lse, t_lse : device fp32 [nq] (written); lse and t_lse are the logarithms of the two sums, for
+ *             idx_distill_bwd (-inf for none).
+ *   ws, ws_bytes : at least idx_workspace_size(IDX_OP_DISTILL, nq, max_n, 1) bytes, 16-byte aligned; as for
+ *             idx_attend.
+ */
+idx_status idx_distill(const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq, int64_t max_n,
+                       const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,
+                       float* loss, float* lse, float* t_lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * idx_distill_bwd: its gradient, dscores[t][s] = dloss[t] * inv_temp * (q_s - sum of p_i over x_i = s).
+ * Written for s < n_t only; 0 where the score is -inf and for a row without entries.
+ *
+ *   lse, t_lse : idx_distill's, of the same arguments.   dloss : device fp32 [nq].
+ *   dscores : device fp32 [nq][d_stride], d_stride >= max_n; may be scores itself (with its stride).
+ */
+idx_status idx_distill_bwd(const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq, int64_t max_n,
+                           const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,
+                           const float* lse, const float* t_lse, const float* dloss, float* dscores, int64_t d_stride,
+                           void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4idx.so")
 
 IDX_OK, IDX_EINVAL, IDX_EALIGN, IDX_EUNSUPPORTED, IDX_EHIP, IDX_EWORKSPACE = 0, -1, -2, -3, -4, -5
-IDX_OP_BUILD_POOL, IDX_OP_TOPK = 1, 2
+IDX_OP_BUILD_POOL, IDX_OP_TOPK, IDX_OP_ATTEND, IDX_OP_DISTILL = 1, 2, 3, 4
 HEADS, DIM, BLOCK = 32, 128, 8
 
 if not os.path.exists(LIB_PATH):
@@ -25,6 +25,7 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); the indexer has no fallback path")
 
 _P, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 lib = ctypes.CDLL(LIB_PATH)
 lib.idx_abi_version.restype = _i32
 lib.idx_last_error.restype = ctypes.c_char_p
@@ -41,15 +42,25 @@ lib.idx_quantize_kv.argtypes = [_P, _i64, _P, _P, _P]
 lib.idx_gather_kv.argtypes = [_P, _P, _P, _P, _i32, _P, _i64, _i32, _P, _P]
 lib.idx_mask_pool.argtypes = [_P, _i64, _P, _i32, _i64, _P, _i64, _P, _i32, _i32, _P]
 lib.idx_topk_pool.argtypes = [_P, _i64, _P, _i32, _i64, _P, _i64, _P, _i32, _i32, _i32, _i32, _P, _i64, _P, _P]
+lib.idx_rope_freqs.argtypes = [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _P, _P]
+lib.idx_rope.argtypes = [_P, _i32, _i64, _i32, _i32, _i64, _i64, _P, _P, _i32, _i32, _i32, _f32, _i32, _P, _i64, _i64, _P]
+lib.idx_attend.argtypes = [_P, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _P, _i64, _i32,
+                           _f32, _P, _P, _P, _sz, _P]
+lib.idx_attend_weights.argtypes = [_P, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _P, _i64, _i32,
+                                   _f32, _P, _P, _i64, _P]
+lib.idx_distill.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, _P, _P, _P, _P, _sz, _P]
+lib.idx_distill_bwd.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, _P, _P, _P, _P, _i64, _P]
 for _f in ("idx_quantize_q", "idx_score_full", "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks",
            "idx_score_pool_gather", "idx_topk",
-           "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool"):
+           "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope",
+           "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd"):
     getattr(lib, _f).restype = _i32
 
 EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quantize_q", "idx_score_full",
            "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks", "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv",
-           "idx_gather_kv", "idx_mask_pool", "idx_topk_pool")
+           "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope", "idx_attend",
+           "idx_attend_weights", "idx_distill", "idx_distill_bwd")
 MKV_DIM = 512
 
 
@@ -294,3 +305,194 @@ def idx_topk_pool(scores, n_vis, max_n: int, pool_blocks, pool_count, max_blocks
           pool_blocks.stride(0), _ptr(pool_count), max_blocks, group, block, k, _ptr(out_idx),
           out_idx.stride(0), _ptr(out_val), _stream(stream))
     return out_idx, out_val
+
+
+def _here(**tensors) -> None:
+    """The arguments given lie on the current device (the library launches there)."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"fp4idx tensors must live on the GPU: {name} is on {t.device}")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must live on the current GPU (cuda:{dev}), got {t.device}")
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original: float = 4096.0,
+               fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Rotation per position of each pair, fp64 [rot / 2] on `device`, and the factor (mscale) that goes with
+    it; scaling stretches a context of `original` positions by `factor` (see idx_rope_freqs in the header)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    freq = torch.empty(max(rot, 0) // 2, dtype=torch.float64)
+    mscale = _f32()
+    _check(lib.idx_rope_freqs(rot, base, ROPE_SCALINGS[scaling], factor, original, fast, slow, freq.data_ptr(),
+                              ctypes.addressof(mscale)))
+    return freq.to(device), mscale.value
+
+
+def idx_rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, offset: int | None = None, layout: str = "half",
+             mscale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None, stream=None):
+    """Rotate the values offset .. offset + 2 * len(freq) - 1 (default: the last ones) of rows x [tokens, heads,
+    dim] (bf16 or fp32, consecutive values, any strides) by pos [tokens] (int64) * freq. out may be x itself;
+    inverse=True is the gradient."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("x must be [tokens, heads, dim] with consecutive values")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    tokens, heads, dim = x.shape
+    _need(pos, torch.int64, "pos")
+    _need(freq, torch.float64, "freq")
+    _need(out, x.dtype, "out")
+    _shape(out, (tokens, heads, dim), "out")
+    _shape(pos, (tokens,), "pos")
+    if out.stride(2) != 1 and dim > 1:
+        raise ValueError("out must have consecutive values")
+    _here(x=x, pos=pos, freq=freq, out=out)
+    rot = 2 * freq.numel()
+    _call(lib.idx_rope, x.data_ptr(), 0 if x.dtype == torch.bfloat16 else 1, tokens, heads, dim, x.stride(0),
+          x.stride(1), _ptr(pos), _ptr(freq), rot, dim - rot if offset is None else offset, ROPE_LAYOUTS[layout],
+          mscale, int(inverse), out.data_ptr(), out.stride(0), out.stride(1), _stream(stream))
+    return out
+
+
+def _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx, extra) -> tuple:
+    """Checks shared by the attention calls; the arguments from q to n_vis, and those of the list."""
+    _need(q, torch.bfloat16, "q")
+    _need(codes, torch.uint8, "codes")
+    _need(scales, torch.uint8, "scales")
+    _need(n_vis, torch.int32, "n_vis")
+    if q.dim() != 3 or q.shape[2] != MKV_DIM:
+        raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(q.shape)}")
+    nq, heads = q.shape[0], q.shape[1]
+    rows = codes.numel() // (MKV_DIM // 2)
+    if codes.numel() != rows * (MKV_DIM // 2) or scales.numel() != rows * (MKV_DIM // 16):
+        raise ValueError("codes and scales must hold 256 and 32 bytes for each cache row")
+    _shape(n_vis, (nq,), "n_vis")
+    nseq = pages_stride = 0
+    if kv_base is not None:
+        _need(kv_base, torch.int64, "kv_base")
+        _shape(kv_base, (nq,), "kv_base")
+    if pages is not None:
+        _need(pages, torch.int32, "pages")
+        pages_ptr = _rows_ptr(pages) or _ptr(n_vis)  # no column: a table all the same, never read
+        nseq = pages.shape[0]
+        if pages.shape[1] * page_size < max_n:
+            raise ValueError(f"pages must cover max_n={max_n} positions: {pages.shape[1]} pages of {page_size}")
+        pages_stride = pages.stride(0) if nseq > 1 else max(pages.shape[1], pages.stride(0))
+    else:
+        pages_ptr = None
+    if seq is not None:
+        _need(seq, torch.int32, "seq")
+        _shape(seq, (nq,), "seq")
+    k = idx_stride = 0
+    idx_ptr = None
+    if idx is not None:
+        _need(idx, torch.int32, "idx")
+        idx_ptr = _rows_ptr(idx) or _ptr(n_vis)  # no slot: a list all the same, never read
+        if idx.shape[0] != nq:
+            raise ValueError(f"idx must have {nq} rows, got {idx.shape[0]}")
+        k = idx.shape[1]
+        idx_stride = idx.stride(0) if nq > 1 else max(k, idx.stride(0))
+    _here(q=q, codes=codes, scales=scales, n_vis=n_vis, kv_base=kv_base, pages=pages, seq=seq, idx=idx, **extra)
+    return ((_ptr(q), nq, heads, _ptr(codes), _ptr(scales), rows, _ptr(kv_base), pages_ptr, pages_stride, nseq,
+             page_size, _ptr(seq), _ptr(n_vis)), (idx_ptr, idx_stride, k))
+
+
+def idx_attend(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=None, window: int = 0, kv_base=None,
+               pages=None, page_size: int = 0, seq=None, idx=None, stream=None):
+    """Core attention of q [nq, heads, 512] over the FP4 main-KV cache: all visible positions (or the last
+    `window`), or those of idx [nq, k]. Rows lie at kv_base [nq] + position, or in pages [nseq, ...] of
+    page_size positions (seq [nq] names each query's page row). ws: workspace(IDX_OP_ATTEND, nq, entries, heads)."""
+    _need(out, torch.bfloat16, "out")
+    _shape(out, tuple(q.shape), "out")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        _shape(lse, tuple(q.shape[:2]), "lse")
+    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx,
+                               dict(out=out, lse=lse, ws=ws))
+    _call(lib.idx_attend, *where, max_n, window, *lst, scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+          _stream(stream))
+    return out, lse
+
+
+def idx_attend_weights(q, codes, scales, n_vis, max_n: int, scale: float, lse, weights, kv_base=None, pages=None,
+                       page_size: int = 0, seq=None, idx=None, stream=None):
+    """The attention's probability of each entry (idx slot, or visible position), mean over the heads, from the
+    saved lse [nq, heads], into weights [nq, >= k] (or [nq, >= max_n])."""
+    _need(lse, torch.float32, "lse")
+    _need(weights, torch.float32, "weights")
+    _shape(lse, tuple(q.shape[:2]), "lse")
+    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx,
+                               dict(lse=lse, weights=weights))
+    if weights.dim() != 2 or weights.shape[0] != q.shape[0] or weights.shape[1] < (max_n if idx is None else lst[2]):
+        raise ValueError("weights must be [nq, >= k] with idx, [nq, >= max_n] without")
+    _call(lib.idx_attend_weights, *where, max_n, *lst, scale, _ptr(lse), _rows_ptr(weights),
+          weights.stride(0) if q.shape[0] > 1 else max(weights.shape[1], weights.stride(0)), _stream(stream))
+    return weights
+
+
+def _distill_rows(scores, n_vis, t_idx, t_logit, per_row: dict, extra: dict) -> tuple:
+    _need(scores, torch.float32, "scores")
+    _need(n_vis, torch.int32, "n_vis")
+    _need(t_idx, torch.int32, "t_idx")
+    _need(t_logit, torch.float32, "t_logit")
+    nq = n_vis.shape[0]
+    _shape(t_logit, tuple(t_idx.shape), "t_logit")
+    if scores.dim() != 2 or scores.shape[0] != nq or t_idx.dim() != 2 or t_idx.shape[0] != nq:
+        raise ValueError("scores and t_idx must have a row for each of n_vis")
+    if nq > 1 and t_idx.stride(0) != t_logit.stride(0):
+        raise ValueError("t_idx and t_logit must have the same row stride")
+    for name, t in per_row.items():
+        _need(t, torch.float32, name)
+        _shape(t, (nq,), name)
+    _here(scores=scores, n_vis=n_vis, t_idx=t_idx, t_logit=t_logit, **per_row, **extra)
+    k = t_idx.shape[1]
+    return nq, (_rows_ptr(t_idx), _rows_ptr(t_logit), t_idx.stride(0) if nq > 1 else max(k, t_idx.stride(0)), k)
+
+
+def _width(t: torch.Tensor, max_n: int, name: str) -> int:
+    """The row stride of a 2-D argument that holds max_n values per row."""
+    if t.shape[1] < max_n:
+        raise ValueError(f"{name} must have at least max_n={max_n} columns, got {t.shape[1]}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+
+
+def idx_distill(scores, n_vis, max_n: int, t_idx, t_logit, loss, lse, t_lse, ws, inv_temp: float = 1.0, stream=None):
+    """KL divergence of score rows [nq, >= max_n] from a teacher's top logits (t_idx, t_logit [nq, k]): writes
+    loss, lse and t_lse [nq]. ws: workspace(IDX_OP_DISTILL, nq, max_n, 1)."""
+    nq, teacher = _distill_rows(scores, n_vis, t_idx, t_logit, dict(loss=loss, lse=lse, t_lse=t_lse), dict(ws=ws))
+    _call(lib.idx_distill, _rows_ptr(scores), _width(scores, max_n, "scores"), _ptr(n_vis), nq, max_n, *teacher,
+          inv_temp, _ptr(loss), _ptr(lse), _ptr(t_lse), _ptr(ws), ws.numel(), _stream(stream))
+    return loss
+
+
+def idx_distill_bwd(scores, n_vis, max_n: int, t_idx, t_logit, lse, t_lse, dloss, dscores, inv_temp: float = 1.0,
+                    stream=None):
+    """Gradient of idx_distill with dloss [nq], from its lse and t_lse, into dscores [nq, >= max_n] (visible
+    positions only; may be scores itself)."""
+    nq, teacher = _distill_rows(scores, n_vis, t_idx, t_logit, dict(lse=lse, t_lse=t_lse, dloss=dloss),
+                                dict(dscores=dscores))
+    _need(dscores, torch.float32, "dscores")
+    if dscores.dim() != 2 or dscores.shape[0] != nq:
+        raise ValueError("dscores must have a row for each of n_vis")
+    _call(lib.idx_distill_bwd, _rows_ptr(scores), _width(scores, max_n, "scores"), _ptr(n_vis), nq, max_n, *teacher,
+          inv_temp, _ptr(lse), _ptr(t_lse), _ptr(dloss), _rows_ptr(dscores), _width(dscores, max_n, "dscores"),
+          _stream(stream))
+    return dscores

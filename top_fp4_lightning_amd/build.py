@@ -7,7 +7,8 @@ import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = ["api.hip", "quantize.hip", "score.hip", "score_multi.hip", "select.hip", "mainkv.hip", "mask.hip"]
+SOURCES = ["api.hip", "quantize.hip", "score.hip", "score_multi.hip", "select.hip", "mainkv.hip", "mask.hip",
+           "rope.hip", "attend.hip", "distill.hip"]
 OUT = os.path.join(HERE, "libfp4idx.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

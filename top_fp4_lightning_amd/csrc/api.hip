@@ -1,12 +1,13 @@
 // C-ABI entry points of libfp4idx: host-side validation, then asynchronous launches.
 // Every check runs before the first HIP call, so argument errors never touch the device.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <mutex>
 #include <string>
 
 #include "../../include/fp4idx.h"
-#include "internal.h"
+#include "operators.h"
 
 using namespace fp4idx;
 
@@ -53,10 +54,14 @@ idx_status hip_status(hipError_t e, const char* what) {
 constexpr int64_t kMaxRows = (int64_t)1 << 36;
 constexpr int64_t kMaxN = (int64_t)1 << 30;
 constexpr int32_t kMaxQueries = 65535;  // grid y dimension
+constexpr int32_t kMaxAttendHeads = 128;
+constexpr int32_t kMaxAttendList = 1 << 24;
 constexpr int64_t kMaxPoolScoreN = (int64_t)1 << 28;  // a score row read through a pool: below 2^30 bytes
 
 size_t ws_bytes_for(int32_t op, int32_t nq, int64_t max_n, int32_t k) {
     if (nq < 0 || max_n < 0 || max_n > kMaxN || k < 1 || k > kMaxK) return 0;
+    if (op == IDX_OP_ATTEND) return k > kMaxAttendHeads ? 0 : attend_workspace_bytes(nq, k, max_n);
+    if (op == IDX_OP_DISTILL) return distill_workspace_bytes(nq, max_n);
     if (op == IDX_OP_BUILD_POOL) return select_workspace_bytes(nq, (max_n + kBlock - 1) / kBlock, k);
     if (op == IDX_OP_TOPK) return select_workspace_bytes(nq, max_n, k);
     return 0;
@@ -95,6 +100,69 @@ idx_status pool_args(const char* fn, const float* block_max, int64_t bm_stride, 
     return ok();
 }
 
+// Validation shared by the attention entry points; fills the arguments common to them.
+idx_status attend_args(const char* fn, const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes,
+                       const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                       int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int32_t* n_vis,
+                       int64_t max_n, int64_t window, const int32_t* idx, int64_t idx_stride, int32_t k, float scale,
+                       AttendArgs& a) {
+    REQUIRE(nq >= 0 && nq <= kMaxQueries, IDX_EUNSUPPORTED, "%s: nq=%d out of [0, 65535]", fn, nq);
+    REQUIRE(heads >= 1 && heads <= kMaxAttendHeads, IDX_EUNSUPPORTED, "%s: heads=%d out of [1, 128]", fn, heads);
+    REQUIRE(max_n >= 0 && max_n <= kMaxN, IDX_EUNSUPPORTED, "%s: max_n=%lld out of [0, 2^30]", fn, (long long)max_n);
+    REQUIRE(rows >= 0 && rows <= INT32_MAX, IDX_EUNSUPPORTED, "%s: rows=%lld out of [0, 2^31 - 1]", fn,
+            (long long)rows);
+    REQUIRE(window >= 0 && !(window && idx), IDX_EINVAL, "%s: window=%lld must be >= 0, and 0 with a list", fn,
+            (long long)window);
+    REQUIRE(isfinite(scale), IDX_EINVAL, "%s: scale is not finite", fn);
+    if (idx) {
+        REQUIRE(k >= 0 && k <= kMaxAttendList, IDX_EUNSUPPORTED, "%s: k=%d out of [0, 2^24]", fn, k);
+        REQUIRE(idx_stride >= k, IDX_EINVAL, "%s: idx_stride=%lld < k=%d", fn, (long long)idx_stride, k);
+    }
+    if (nq == 0) return ok();
+    REQUIRE(q && n_vis && (rows == 0 || (codes && scales)), IDX_EINVAL, "%s: null pointer", fn);
+    REQUIRE((kv_base != nullptr) != (pages != nullptr), IDX_EINVAL, "%s: give either kv_base or pages", fn);
+    if (pages) {
+        REQUIRE(page_size >= 1, IDX_EINVAL, "%s: page_size=%d must be >= 1", fn, page_size);
+        REQUIRE(pages_stride >= (max_n + page_size - 1) / page_size, IDX_EINVAL,
+                "%s: pages_stride=%lld < ceil(max_n / page_size)", fn, (long long)pages_stride);
+        REQUIRE(nseq >= 1 && (seq || nseq >= nq), IDX_EINVAL,
+                "%s: nseq=%d page rows; without seq, query t uses row t of nq=%d", fn, nseq, nq);
+    }
+    REQUIRE(aligned(q, 16) && aligned(codes, 16) && aligned(scales, 2) && aligned(kv_base, 8) && aligned(pages, 4) &&
+                aligned(seq, 4) && aligned(n_vis, 4) && aligned(idx, 4),
+            IDX_EALIGN, "%s: misaligned pointer", fn);
+    a = AttendArgs{q, nq, heads, codes, scales, rows, kv_base, pages, pages_stride, nseq, page_size, seq, n_vis,
+                   max_n, window, idx, idx_stride, idx ? k : 0, scale, nullptr, nullptr, nullptr, nullptr};
+    return ok();
+}
+
+// Validation shared by the two directions of the distillation
+idx_status distill_args(const char* fn, const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq,
+                        int64_t max_n, const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k,
+                        float inv_temp, DistillArgs& a) {
+    REQUIRE(nq >= 0 && nq <= kMaxQueries, IDX_EUNSUPPORTED, "%s: nq=%d out of [0, 65535]", fn, nq);
+    REQUIRE(max_n >= 0 && max_n <= kMaxN, IDX_EUNSUPPORTED, "%s: max_n=%lld out of [0, 2^30]", fn, (long long)max_n);
+    REQUIRE(k >= 0 && k <= kMaxK, IDX_EUNSUPPORTED, "%s: k=%d out of [0, 2048]", fn, k);
+    REQUIRE(isfinite(inv_temp) && inv_temp > 0.0f, IDX_EINVAL, "%s: inv_temp must be finite and above 0", fn);
+    if (nq == 0) return ok();
+    REQUIRE(n_vis && (max_n == 0 || scores) && (k == 0 || (t_idx && t_logit)), IDX_EINVAL, "%s: null pointer", fn);
+    REQUIRE(score_stride >= max_n, IDX_EINVAL, "%s: score_stride=%lld < max_n=%lld", fn, (long long)score_stride,
+            (long long)max_n);
+    REQUIRE(t_stride >= k, IDX_EINVAL, "%s: t_stride=%lld < k=%d", fn, (long long)t_stride, k);
+    REQUIRE(aligned(scores, 4) && aligned(n_vis, 4) && aligned(t_idx, 4) && aligned(t_logit, 4), IDX_EALIGN,
+            "%s: misaligned pointer", fn);
+    a.scores = scores;
+    a.score_stride = score_stride;
+    a.n_vis = n_vis;
+    a.nq = nq;
+    a.max_n = max_n;
+    a.t_idx = t_idx;
+    a.t_logit = t_logit;
+    a.t_stride = t_stride;
+    a.k = k;
+    a.inv_temp = inv_temp;
+    return ok();
+}
 
 constexpr int kMaxDevices = 64;
 struct DeviceScratch {
@@ -390,6 +458,141 @@ idx_status idx_mask_pool(float* scores, int64_t score_stride, const int32_t* n_v
     return hip_status(launch_mask_pool(scores, score_stride, n_vis, nq, max_n, pool_blocks, pool_stride, pool_count,
                                        group, (hipStream_t)stream),
                       "idx_mask_pool");
+}
+
+idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double original, double fast,
+                          double slow, double* freq, float* mscale) {
+    REQUIRE(rot >= 2 && rot <= IDX_MAX_ROT && rot % 2 == 0, IDX_EINVAL,
+            "idx_rope_freqs: rot=%d must be even, 2 .. 8192", rot);
+    REQUIRE(freq && mscale, IDX_EINVAL, "idx_rope_freqs: null pointer");
+    REQUIRE(isfinite(base) && base > 1.0, IDX_EINVAL, "idx_rope_freqs: base must be finite and above 1");
+    REQUIRE(scaling >= IDX_ROPE_PLAIN && scaling <= IDX_ROPE_YARN, IDX_EUNSUPPORTED, "idx_rope_freqs: scaling=%d",
+            scaling);
+    REQUIRE(scaling == IDX_ROPE_PLAIN || (isfinite(factor) && factor >= 1.0), IDX_EINVAL,
+            "idx_rope_freqs: factor must be finite and at least 1");
+    REQUIRE(scaling != IDX_ROPE_NTK || rot > 2, IDX_EINVAL, "idx_rope_freqs: the changed base needs rot > 2");
+    REQUIRE(scaling != IDX_ROPE_YARN || (isfinite(original) && original > 0.0 && isfinite(fast) && isfinite(slow) &&
+                                         fast > slow),
+            IDX_EINVAL, "idx_rope_freqs: needs original > 0 and fast > slow");
+    if (scaling == IDX_ROPE_NTK) base *= pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        if (scaling == IDX_ROPE_LINEAR) f /= factor;
+        if (scaling == IDX_ROPE_YARN) {
+            const double turns = original * f / (2.0 * M_PI);
+            const double keep = fmin(fmax((turns - slow) / (fast - slow), 0.0), 1.0);
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        freq[i] = f;
+    }
+    *mscale = scaling == IDX_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    return ok();
+}
+
+idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads, int32_t dim, int64_t x_token,
+                    int64_t x_head, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
+                    int32_t layout, float mscale, int32_t inverse, void* out, int64_t out_token, int64_t out_head,
+                    void* stream) {
+    REQUIRE(dtype == IDX_BF16 || dtype == IDX_F32, IDX_EUNSUPPORTED, "idx_rope: dtype=%d", dtype);
+    REQUIRE(layout == IDX_ROPE_HALF || layout == IDX_ROPE_INTERLEAVED, IDX_EUNSUPPORTED, "idx_rope: layout=%d",
+            layout);
+    REQUIRE(tokens >= 0 && tokens <= INT32_MAX, IDX_EUNSUPPORTED, "idx_rope: tokens=%lld out of [0, 2^31 - 1]",
+            (long long)tokens);
+    REQUIRE(heads >= 1 && heads <= 65535, IDX_EUNSUPPORTED, "idx_rope: heads=%d out of [1, 65535]", heads);
+    REQUIRE(dim >= 2 && dim <= (1 << 20), IDX_EUNSUPPORTED, "idx_rope: dim=%d out of [2, 2^20]", dim);
+    REQUIRE(rot >= 2 && rot <= IDX_MAX_ROT && rot % 2 == 0 && offset >= 0 && offset <= dim - rot, IDX_EINVAL,
+            "idx_rope: rot=%d must be even, 2 .. 8192, and lie in the row: offset=%d, dim=%d", rot, offset, dim);
+    REQUIRE(isfinite(mscale), IDX_EINVAL, "idx_rope: mscale is not finite");
+    if (tokens == 0) return ok();
+    REQUIRE(x && pos && freq && out, IDX_EINVAL, "idx_rope: null pointer");
+    REQUIRE(x_token >= 0 && x_head >= 0 && (tokens == 1 || out_token >= dim) && (heads == 1 || out_head >= dim),
+            IDX_EINVAL, "idx_rope: strides must be >= 0, and out's at least dim (rows may not overlap)");
+    REQUIRE(out != x || ((tokens == 1 || x_token == out_token) && (heads == 1 || x_head == out_head)), IDX_EINVAL,
+            "idx_rope: in place, the strides must agree");
+    const size_t size = dtype == IDX_BF16 ? 2 : 4;
+    REQUIRE(aligned(x, size) && aligned(out, size) && aligned(pos, 8) && aligned(freq, 8), IDX_EALIGN,
+            "idx_rope: misaligned pointer");
+    const RopeArgs a{x, dtype == IDX_F32, tokens, heads, dim, x_token, x_head, pos, freq, rot, offset,
+                     layout == IDX_ROPE_HALF, inverse != 0, mscale, out, out_token, out_head};
+    return hip_status(launch_rope(a, (hipStream_t)stream), "idx_rope");
+}
+
+idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes, const uint8_t* scales,
+                      int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,
+                      int32_t page_size, const int32_t* seq, const int32_t* n_vis, int64_t max_n, int64_t window,
+                      const int32_t* idx, int64_t idx_stride, int32_t k, float scale, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+    AttendArgs a{};
+    const idx_status st = attend_args("idx_attend", q, nq, heads, codes, scales, rows, kv_base, pages, pages_stride,
+                                      nseq, page_size, seq, n_vis, max_n, window, idx, idx_stride, k, scale, a);
+    if (st != IDX_OK || nq == 0) return st;
+    REQUIRE(out, IDX_EINVAL, "idx_attend: null pointer");
+    REQUIRE(aligned(out, 16) && aligned(lse, 4), IDX_EALIGN, "idx_attend: misaligned pointer");
+    const int64_t entries = idx ? k : (window > 0 && window < max_n ? window : max_n);
+    const size_t need = attend_workspace_bytes(nq, heads, entries);
+    REQUIRE(ws && ws_bytes >= need, IDX_EWORKSPACE, "idx_attend: workspace %zu bytes, need %zu", ws_bytes, need);
+    REQUIRE(aligned(ws, 16), IDX_EALIGN, "idx_attend: misaligned workspace");
+    a.out = out;
+    a.lse = lse;
+    return hip_status(launch_attend(a, ws, (hipStream_t)stream), "idx_attend");
+}
+
+idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes,
+                              const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                              int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq,
+                              const int32_t* n_vis, int64_t max_n, const int32_t* idx, int64_t idx_stride, int32_t k,
+                              float scale, const float* lse, float* weights, int64_t w_stride, void* stream) {
+    AttendArgs a{};
+    const idx_status st = attend_args("idx_attend_weights", q, nq, heads, codes, scales, rows, kv_base, pages,
+                                      pages_stride, nseq, page_size, seq, n_vis, max_n, 0, idx, idx_stride, k, scale, a);
+    if (st != IDX_OK || nq == 0) return st;
+    const int64_t width = idx ? k : max_n;
+    if (width == 0) return ok();
+    REQUIRE(lse && weights, IDX_EINVAL, "idx_attend_weights: null pointer");
+    REQUIRE(w_stride >= width, IDX_EINVAL, "idx_attend_weights: w_stride=%lld < %lld", (long long)w_stride,
+            (long long)width);
+    REQUIRE(aligned(lse, 4) && aligned(weights, 4), IDX_EALIGN, "idx_attend_weights: misaligned pointer");
+    return hip_status(launch_attend_weights(a, lse, weights, w_stride, (hipStream_t)stream), "idx_attend_weights");
+}
+
+idx_status idx_distill(const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq, int64_t max_n,
+                       const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,
+                       float* loss, float* lse, float* t_lse, void* ws, size_t ws_bytes, void* stream) {
+    DistillArgs a{};
+    const idx_status st = distill_args("idx_distill", scores, score_stride, n_vis, nq, max_n, t_idx, t_logit, t_stride,
+                                       k, inv_temp, a);
+    if (st != IDX_OK || nq == 0) return st;
+    REQUIRE(loss && lse && t_lse, IDX_EINVAL, "idx_distill: null pointer");
+    REQUIRE(aligned(loss, 4) && aligned(lse, 4) && aligned(t_lse, 4), IDX_EALIGN, "idx_distill: misaligned pointer");
+    const size_t need = distill_workspace_bytes(nq, max_n);
+    REQUIRE(ws && ws_bytes >= need, IDX_EWORKSPACE, "idx_distill: workspace %zu bytes, need %zu", ws_bytes, need);
+    REQUIRE(aligned(ws, 16), IDX_EALIGN, "idx_distill: misaligned workspace");
+    a.loss = loss;
+    a.lse = lse;
+    a.t_lse = t_lse;
+    a.ws = ws;
+    return hip_status(launch_distill(a, (hipStream_t)stream), "idx_distill");
+}
+
+idx_status idx_distill_bwd(const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq, int64_t max_n,
+                           const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,
+                           const float* lse, const float* t_lse, const float* dloss, float* dscores, int64_t d_stride,
+                           void* stream) {
+    DistillArgs a{};
+    const idx_status st = distill_args("idx_distill_bwd", scores, score_stride, n_vis, nq, max_n, t_idx, t_logit,
+                                       t_stride, k, inv_temp, a);
+    if (st != IDX_OK || nq == 0 || max_n == 0) return st;
+    REQUIRE(lse && t_lse && dloss && dscores, IDX_EINVAL, "idx_distill_bwd: null pointer");
+    REQUIRE(d_stride >= max_n, IDX_EINVAL, "idx_distill_bwd: d_stride=%lld < max_n", (long long)d_stride);
+    REQUIRE(dscores != scores || d_stride == score_stride, IDX_EINVAL, "idx_distill_bwd: in place, the strides must agree");
+    REQUIRE(aligned(lse, 4) && aligned(t_lse, 4) && aligned(dloss, 4) && aligned(dscores, 4), IDX_EALIGN,
+            "idx_distill_bwd: misaligned pointer");
+    a.lse = const_cast<float*>(lse);
+    a.t_lse = const_cast<float*>(t_lse);
+    a.dloss = dloss;
+    a.dscores = dscores;
+    a.d_stride = d_stride;
+    return hip_status(launch_distill_bwd(a, (hipStream_t)stream), "idx_distill_bwd");
 }
 
 }  // extern "C"

@@ -1,0 +1,254 @@
+// Distillation of score rows from a teacher's top logits: the divergence
+//   L = sum_i p_i (log p_i - log q_{x_i}),  p = softmax(t / T) over the teacher's entries,
+//   q = softmax(s / T) over the row's visible positions with a score above -inf,
+// and its gradient dL/ds = (q - p) / T.
+//
+// Both directions are one pass over the row: the forward reads it (running maximum and sum per
+// thread, base 2), the gradient reads it and writes as much, with the teacher's probabilities of a piece
+// of the row laid out in LDS before the piece is streamed. They are bound by HBM.
+#include "operators.h"
+
+namespace fp4idx {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kThreads = 256;
+constexpr int kPiece = 4096;       // values whose teacher probabilities are in LDS at a time
+constexpr int kPerThread = kMaxK / kThreads;
+
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));  // rows start at any fp32 address
+
+__device__ __forceinline__ float ninf() { return -__builtin_inff(); }
+
+// sum = l * exp(m / T). m is a value of the row itself and differences are taken before the factor
+// c = log2(e) / T: values near the type's lowest would overflow with it.
+struct MaxSum {
+    float m, l;
+};
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    const float r = m == ninf() ? 0.0f : m;
+    return MaxSum{m, a.l * __builtin_amdgcn_exp2f((a.m - r) * c) + b.l * __builtin_amdgcn_exp2f((b.m - r) * c)};
+}
+__device__ __forceinline__ MaxSum block_join(MaxSum v, float c, MaxSum* lds) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v = join(v, MaxSum{__shfl_xor(v.m, d), __shfl_xor(v.l, d)}, c);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return join(join(lds[0], lds[1], c), join(lds[2], lds[3], c), c);
+}
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__device__ __forceinline__ int32_t visible(const DistillArgs& a, int64_t t) {
+    const int32_t n = a.n_vis[t];
+    return n < 0 ? 0 : (n > a.max_n ? (int32_t)a.max_n : n);
+}
+
+// natural log of a sum
+__device__ __forceinline__ double log_of(MaxSum v, float inv_temp) {
+    return v.l == 0.0f ? -__builtin_inf() : (double)v.m * inv_temp + log((double)v.l);
+}
+
+// the sum over s[i0 .. i1), this thread's share
+__device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t i0, int32_t i1, float c) {
+    MaxSum v{ninf(), 0.0f};
+    int32_t i = i0 + (int32_t)threadIdx.x * 4;
+    for (; i + 3 * kThreads * 4 + 4 <= i1; i += 4 * kThreads * 4) {
+        f4u x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * kThreads * 4);
+        float top = ninf();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3])));
+        const float m = fmaxf(v.m, top);
+        const float r = m == ninf() ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += __builtin_amdgcn_exp2f((x[k][j] - r) * c);
+        v.l = v.l * __builtin_amdgcn_exp2f((v.m - r) * c) + sum;
+        v.m = m;
+    }
+    for (; i < i1; i += kThreads * 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < i1) {
+                const float x = s[i + j];
+                v = join(v, MaxSum{x, x == ninf() ? 0.0f : 1.0f}, c);
+            }
+    }
+    return v;
+}
+
+// the row's end: the teacher's sum and the loss. Whole block.
+__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, MaxSum row, MaxSum* lds_ms, double* lds_d) {
+    const float* s = a.scores + t * a.score_stride;
+    const int32_t n = visible(a, t);
+    const float c = a.inv_temp * kLog2e;
+    float tl[kPerThread], sl[kPerThread];
+    MaxSum v{ninf(), 0.0f};
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        tl[k] = ninf();
+        sl[k] = 0.0f;
+        const int i = k * kThreads + (int)threadIdx.x;
+        if (i < a.k) {
+            const int32_t p = a.t_idx[t * a.t_stride + i];
+            if (p >= 0 && p < n) {
+                sl[k] = s[p];
+                if (sl[k] != ninf()) tl[k] = a.t_logit[t * a.t_stride + i];
+            }
+        }
+        if (tl[k] != ninf()) v = join(v, MaxSum{tl[k], 1.0f}, c);
+    }
+    v = block_join(v, c, lds_ms);
+    const double tlse = log_of(v, a.inv_temp), lse = log_of(row, a.inv_temp);
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (tl[k] != ninf()) {
+            const double d = (double)tl[k] * a.inv_temp - tlse;
+            sum += (double)expf((float)d) * (d - ((double)sl[k] * a.inv_temp - lse));
+        }
+    sum = block_sum(sum, lds_d);
+    if (threadIdx.x == 0) {
+        a.loss[t] = (float)sum;
+        a.lse[t] = (float)lse;
+        a.t_lse[t] = (float)tlse;
+    }
+}
+
+// one block per row (pieces == 1), or per piece of a row: then only (max, sum) of the piece is written
+__global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a, int pieces) {
+    __shared__ MaxSum s_ms[4];
+    __shared__ double s_d[4];
+    const int64_t t = blockIdx.x / pieces;
+    const int piece = (int)(blockIdx.x % pieces);
+    const int32_t n = visible(a, t);
+    const int32_t per = ((n + pieces - 1) / pieces + 3) & ~3;
+    const int32_t i0 = (int32_t)min((int64_t)piece * per, (int64_t)n);
+    const int32_t i1 = (int32_t)min((int64_t)i0 + per, (int64_t)n);
+    const float c = a.inv_temp * kLog2e;
+    const MaxSum v = block_join(row_part(a.scores + t * a.score_stride, i0, i1, c), c, s_ms);
+    if (pieces == 1)
+        finish_row(a, t, v, s_ms, s_d);
+    else if (threadIdx.x == 0)
+        reinterpret_cast<MaxSum*>(a.ws)[blockIdx.x] = v;
+}
+
+__global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArgs a, int pieces) {
+    __shared__ MaxSum s_ms[4];
+    __shared__ double s_d[4];
+    const int64_t t = blockIdx.x;
+    const float c = a.inv_temp * kLog2e;
+    MaxSum v{ninf(), 0.0f};
+    for (int i = threadIdx.x; i < pieces; i += kThreads)
+        v = join(v, reinterpret_cast<const MaxSum*>(a.ws)[t * pieces + i], c);
+    v = block_join(v, c, s_ms);
+    finish_row(a, t, v, s_ms, s_d);
+}
+
+__device__ __forceinline__ float softmax_of(float x, float inv_temp, float lse) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, inv_temp, -lse) * kLog2e);
+}
+
+// gradient: a block takes a range of whole pieces of one row
+__global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs a, int blocks_per_row) {
+    __shared__ float s_p[kPiece];
+    const int64_t t = blockIdx.x / blocks_per_row;
+    const int part = (int)(blockIdx.x % blocks_per_row);
+    const int32_t n = visible(a, t);
+    const int32_t pieces = (n + kPiece - 1) / kPiece;
+    const int32_t per = (pieces + blocks_per_row - 1) / blocks_per_row;
+    const int32_t p0 = min(part * per, pieces), p1 = min(p0 + per, pieces);
+    if (p0 >= p1) return;
+    const float* s = a.scores + t * a.score_stride;
+    float* d = a.dscores + t * a.d_stride;
+    const float tlse = a.t_lse[t];
+    const float lse = a.lse[t];
+    const float gain = tlse == ninf() ? 0.0f : a.dloss[t] * a.inv_temp;
+    if (tlse == ninf()) {  // no teacher entry: no gradient
+        for (int32_t i = p0 * kPiece + (int32_t)threadIdx.x; i < min(p1 * kPiece, n); i += kThreads) d[i] = 0.0f;
+        return;
+    }
+    int32_t at[kPerThread];
+    float p[kPerThread];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int i = k * kThreads + (int)threadIdx.x;
+        at[k] = -1;
+        p[k] = 0.0f;
+        if (i < a.k) {
+            at[k] = a.t_idx[t * a.t_stride + i];
+            const float x = a.t_logit[t * a.t_stride + i];
+            p[k] = x == ninf() ? 0.0f : softmax_of(x, a.inv_temp, tlse);
+        }
+    }
+    for (int32_t pc = p0; pc < p1; ++pc) {
+        const int32_t i0 = pc * kPiece, i1 = min(i0 + kPiece, n);
+        for (int i = threadIdx.x * 4; i < kPiece; i += kThreads * 4) *reinterpret_cast<v4f*>(s_p + i) = v4f{};
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k)
+            if (at[k] >= i0 && at[k] < i1) atomicAdd(s_p + (at[k] - i0), p[k]);
+        __syncthreads();
+        for (int32_t i = i0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
+            const v4f pv = *reinterpret_cast<const v4f*>(s_p + (i - i0));
+            if (i + 4 <= i1) {
+                const f4u x = *reinterpret_cast<const f4u*>(s + i);
+                f4u y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = x[j] == ninf() ? 0.0f : gain * (softmax_of(x[j], a.inv_temp, lse) - pv[j]);
+                *reinterpret_cast<f4u*>(d + i) = y;
+            } else {
+                for (int j = 0; i + j < i1; ++j) {
+                    const float x = s[i + j];
+                    d[i + j] = x == ninf() ? 0.0f : gain * (softmax_of(x, a.inv_temp, lse) - pv[j]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+// Blocks per row: one while the rows alone give every compute unit four blocks, else enough for that
+// with at least 4096 values each.
+int distill_pieces(int32_t nq, int64_t max_n) {
+    if (nq <= 0 || nq >= 1024) return 1;
+    const int64_t want = (1024 + nq - 1) / nq, most = (max_n + kPiece - 1) / kPiece;
+    return (int)(want < most ? want : (most < 1 ? 1 : most));
+}
+
+size_t distill_workspace_bytes(int32_t nq, int64_t max_n) {
+    const int pieces = distill_pieces(nq, max_n);
+    return pieces == 1 ? 16 : (size_t)nq * pieces * sizeof(MaxSum);
+}
+
+hipError_t launch_distill(const DistillArgs& a, hipStream_t stream) {
+    const int pieces = distill_pieces(a.nq, a.max_n);
+    hipLaunchKernelGGL(distill_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || pieces == 1) return err;
+    hipLaunchKernelGGL(distill_join_kernel, dim3((unsigned)a.nq), dim3(kThreads), 0, stream, a, pieces);
+    return hipGetLastError();
+}
+
+hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t stream) {
+    const int pieces = distill_pieces(a.nq, a.max_n);
+    hipLaunchKernelGGL(distill_bwd_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
+    return hipGetLastError();
+}
+
+}  // namespace fp4idx

@@ -1,0 +1,159 @@
+// Rotary positions: pair i of a row's rotated part turns by the angle pos * freq_i,
+//   y0 = m (x0 cos - x1 sin),  y1 = m (x1 cos + x0 sin);  inverse (the gradient): the angle negated.
+// Pairs are (i, i + rot/2) ("half") or (2i, 2i + 1) ("interleaved").
+//
+// Angles of far positions need more than 32 bits (at position 2^20 an fp32 product is off by up to
+// 0.06 rad): turns = pos * freq / 2 pi in fp64, its whole part taken off exactly, then sin and cos of
+// the remainder in fp32. They are computed once per token, in LDS, and used by all heads.
+//
+// The kernel is a copy: one read and one write of every value (the rotated part only, in place). A
+// lane moves 16 bytes at a time where sizes and addresses allow it, else one value or pair.
+#include "operators.h"
+
+namespace fp4idx {
+namespace {
+
+constexpr int kRopeLds = 4096;  // (cos, sin) pairs per block: 32 KB
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+template <> __device__ __forceinline__ float to_f(float v) { return v; }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ uint16_t from_f(float v) { return (uint16_t)bf16_pair(v, 0.0f); }
+template <> __device__ __forceinline__ float from_f(float v) { return v; }
+
+// V values moved as one access
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T v[V];
+};
+
+// A block takes `tokens_per_block` tokens; a row (token, head) takes `lanes` lanes (a power of two).
+// items of a row: first the rotated ones (a vector of each half of a pair, or a vector of whole pairs),
+// then the vectors that pass through (none in place).
+template <typename T, int V, bool HALF>
+__global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a, int tokens_per_block, int lanes_log2,
+                                                   int rot_items, int items) {
+    __shared__ float2 s_cs[kRopeLds];
+    const int64_t tok0 = (int64_t)blockIdx.x * tokens_per_block;
+    const int toks = (int)min((int64_t)tokens_per_block, a.tokens - tok0);
+    const int pairs = a.rot / 2;
+    for (int i = threadIdx.x; i < toks * pairs; i += 256) {
+        const int tk = i / pairs, pr = i - tk * pairs;
+        double turns = (double)a.pos[tok0 + tk] * (a.freq[pr] * 0.15915494309189533577);
+        turns -= rint(turns);
+        float s, c;
+        sincospif(2.0f * (float)turns, &s, &c);
+        s_cs[i] = float2{c * a.mscale, (a.inverse ? -s : s) * a.mscale};
+    }
+    __syncthreads();
+
+    const int lanes = 1 << lanes_log2;
+    const int at = threadIdx.x & (lanes - 1);
+    const int step = 256 >> lanes_log2;  // rows per pass of the block
+    const int step_tok = step / a.heads, step_head = step - step_tok * a.heads;
+    int tk = (int)(threadIdx.x >> lanes_log2) / a.heads;
+    int h = (int)(threadIdx.x >> lanes_log2) - tk * a.heads;
+    const T* xs = (const T*)a.x;
+    T* ys = (T*)a.out;
+    typedef Vec<T, V> W;
+    while (tk < toks) {
+        const T* x = xs + (tok0 + tk) * a.x_token + h * a.x_head;
+        T* y = ys + (tok0 + tk) * a.out_token + h * a.out_head;
+        const float2* cs = s_cs + tk * pairs;
+        for (int it = at; it < items; it += lanes) {
+            if (it < rot_items) {
+                if constexpr (HALF) {
+                    const int i = it * V;
+                    const W v0 = *reinterpret_cast<const W*>(x + a.offset + i);
+                    const W v1 = *reinterpret_cast<const W*>(x + a.offset + pairs + i);
+                    W o0, o1;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const float2 z = cs[i + k];
+                        const float x0 = to_f<T>(v0.v[k]), x1 = to_f<T>(v1.v[k]);
+                        o0.v[k] = from_f<T>(x0 * z.x - x1 * z.y);
+                        o1.v[k] = from_f<T>(x1 * z.x + x0 * z.y);
+                    }
+                    *reinterpret_cast<W*>(y + a.offset + i) = o0;
+                    *reinterpret_cast<W*>(y + a.offset + pairs + i) = o1;
+                } else {
+                    constexpr int P = V > 1 ? V / 2 : 1;  // pairs of an item
+                    constexpr int N = V > 1 ? 1 : 2;      // accesses of an item
+                    W v[N];
+                    T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) v[n] = reinterpret_cast<const W*>(x + a.offset + it * 2 * P)[n];
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const float2 z = cs[it * P + k];
+                        const float x0 = to_f<T>(e[2 * k]), x1 = to_f<T>(e[2 * k + 1]);
+                        e[2 * k] = from_f<T>(x0 * z.x - x1 * z.y);
+                        e[2 * k + 1] = from_f<T>(x1 * z.x + x0 * z.y);
+                    }
+#pragma unroll
+                    for (int n = 0; n < N; ++n) reinterpret_cast<W*>(y + a.offset + it * 2 * P)[n] = v[n];
+                }
+            } else {
+                int i = (it - rot_items) * V;
+                if (i >= a.offset) i += a.rot;
+                *reinterpret_cast<W*>(y + i) = *reinterpret_cast<const W*>(x + i);
+            }
+        }
+        tk += step_tok;
+        h += step_head;
+        if (h >= a.heads) {
+            h -= a.heads;
+            ++tk;
+        }
+    }
+}
+
+template <typename T, int V>
+void launch_rope_as(const RopeArgs& a, hipStream_t stream) {
+    const bool in_place = a.out == a.x;
+    const int rot_items = a.rot / 2 / (a.half ? V : (V > 1 ? V / 2 : 1));
+    const int items = rot_items + (in_place ? 0 : (a.dim - a.rot) / V);
+    int lanes_log2 = 0;
+    while (lanes_log2 < 6 && (1 << lanes_log2) < items) ++lanes_log2;
+    // about 16 passes of the block over its rows (64 KB of bf16), fewer while that leaves the 256
+    // compute units short of blocks; what the table of angles holds at most
+    const int64_t rows_per_block = 16 * (256 >> lanes_log2);
+    int64_t tpb = rows_per_block / a.heads;
+    const int64_t most = kRopeLds / (a.rot / 2);
+    const int64_t spread = (a.tokens + 1023) / 1024;
+    tpb = tpb < spread ? tpb : spread;
+    tpb = tpb < most ? tpb : most;
+    tpb = tpb < 1 ? 1 : tpb;
+    const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb));
+    if (a.half)
+        hipLaunchKernelGGL((rope_kernel<T, V, true>), grid, dim3(256), 0, stream, a, (int)tpb, lanes_log2, rot_items,
+                           items);
+    else
+        hipLaunchKernelGGL((rope_kernel<T, V, false>), grid, dim3(256), 0, stream, a, (int)tpb, lanes_log2, rot_items,
+                           items);
+}
+
+template <typename T>
+void launch_rope_of(const RopeArgs& a, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    const int64_t strides = a.x_token | a.x_head | a.out_token | a.out_head | a.dim | a.offset |
+                            (a.half ? a.rot / 2 : a.rot);
+    const bool wide = strides % V == 0 && ((uintptr_t)a.x | (uintptr_t)a.out) % 16 == 0;
+    if (wide)
+        launch_rope_as<T, V>(a, stream);
+    else
+        launch_rope_as<T, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
+    if (a.f32)
+        launch_rope_of<float>(a, stream);
+    else
+        launch_rope_of<uint16_t>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace fp4idx
