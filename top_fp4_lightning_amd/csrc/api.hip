@@ -132,7 +132,7 @@ idx_status attend_args(const char* fn, const uint16_t* q, int32_t nq, int32_t he
                 aligned(seq, 4) && aligned(n_vis, 4) && aligned(idx, 4),
             IDX_EALIGN, "%s: misaligned pointer", fn);
     a = AttendArgs{q, nq, heads, codes, scales, rows, kv_base, pages, pages_stride, nseq, page_size, seq, n_vis,
-                   max_n, window, idx, idx_stride, idx ? k : 0, scale, nullptr, nullptr, nullptr, nullptr};
+                   max_n, window, idx, idx_stride, idx ? k : 0, scale, nullptr, nullptr, 0, 0, nullptr, nullptr};
     return ok();
 }
 

@@ -5,16 +5,20 @@
 //   s_{h,i} = scale * q_h . kv_i,  p = softmax_i(s_h),  o_h = sum_i p_{h,i} kv_i   (one row is key and value)
 //
 // One pass over the entries with a running maximum M and sum l per head (base 2: s2 = s * log2 e).
-// A block of four wavefronts takes 32 heads of one query and 64 entries at a time: wavefront w
-// multiplies entries 16w .. 16w+15 with all 32 heads, then values 128w .. 128w+127 of all 64 entries
-// with the probabilities.
+// A block of four wavefronts takes 16, 32 or 64 heads of one query and 64 entries per step. Wavefront w
+// reads the rows of entries 16w .. 16w+15 straight into registers, widens them to fp16 there, multiplies
+// them with all heads of the block and leaves them in LDS; after a barrier it multiplies values
+// 128w .. 128w+127 of all 64 entries with the probabilities. So every row is widened once, and read from
+// LDS once (transposed). Queries and outputs stay in registers: at 64 heads 256 + 128 of a lane's 512.
 //
 // Arithmetic. An E2M1 code times an E4M3 scale has at most 6 significant bits and lies in
 // [2^-10, 2688]: exact in fp16. A query row is multiplied by the power of two that brings its largest
 // value to [2^14, 2^15); its bf16 values are then exact in fp16 down to 2^-28 of the row's largest
 // (below that they lose bits worth less than 2^-39 of it). Products and sums are fp32 in the matrix
-// units. Probabilities enter the second product as fp16 values in (0, 2^14] (11 bits; the offset keeps
-// them normal numbers down to 2^-28 of the largest).
+// units. Probabilities enter the second product as fp16 values (11 bits) up to 2^15, the largest so far of a
+// head above 2^9: values down to 2^-23 of it are normal numbers, and what rounds to zero is below 2^-34 of it.
+#include <type_traits>
+
 #include "operators.h"
 
 namespace fp4idx {
@@ -22,10 +26,12 @@ namespace {
 
 constexpr int kD = 512;
 constexpr int kTile = 64;        // entries per step
-constexpr int kHeadTile = 32;    // heads per block
 constexpr int kRow = kD + 16;    // LDS row of a tile in fp16 values (the pad spreads rows over the banks)
 constexpr int kPRow = kTile + 8;
-constexpr float kPBits = 14.0f;
+constexpr int kQRow = 32;
+constexpr float kNone = -3.0e38f;  // reference of a head that has met no entry
+constexpr float kRoom = 10.0f;   // the reference lies this far below the largest logit (base 2) when it is set
+constexpr float kMost = 15.0f;   // and a logit at most this far above it: probabilities up to 2^15
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -72,50 +78,43 @@ __device__ __forceinline__ Entries entries_of(const AttendArgs& a, int64_t t) {
     return e;
 }
 
-// cache row of entry i, or -1 (past the end, a position that is not visible, a row outside the cache)
-__device__ __forceinline__ int32_t row_of(const AttendArgs& a, const Entries& e, int i) {
-    if (i >= e.count) return -1;
-    const int32_t p = e.list ? e.list[i] : e.first + i;
-    if (p < 0 || p >= e.n) return -1;
-    int64_t r;
-    if (e.pages) {
-        const uint32_t pg = (uint32_t)p / (uint32_t)a.page_size;
-        const int64_t page = e.pages[pg];
-        if (page < 0) return -1;
-        r = page * a.page_size + (p - (int32_t)(pg * (uint32_t)a.page_size));
-    } else {
-        r = e.base + p;
-    }
-    return (r >= 0 && r < a.rows) ? (int32_t)r : -1;
+// An entry's row is found in three stages, so that a kernel can keep the loads of each in flight:
+// its position, its page, its row. -1: past the end, not visible, or outside the cache.
+__device__ __forceinline__ uint32_t page_index(const AttendArgs& a, int32_t p) {
+    return a.page_size == 1 ? (uint32_t)p : __umulhi((uint32_t)p, a.page_mul) >> a.page_shift;
+}
+__device__ __forceinline__ int32_t position_of(const Entries& e, int i, int end) {
+    if (i >= end) return -1;
+    return e.list ? e.list[i] : e.first + i;
+}
+__device__ __forceinline__ int32_t page_of(const AttendArgs& a, const Entries& e, int32_t p) {
+    if (!e.pages || (uint32_t)p >= (uint32_t)e.n) return 0;
+    return e.pages[page_index(a, p)];
+}
+__device__ __forceinline__ int32_t row_of(const AttendArgs& a, const Entries& e, int32_t p, int32_t page) {
+    int64_t r = e.base + p;
+    if (e.pages) r = (int64_t)page * a.page_size + (p - (int32_t)page_index(a, p) * a.page_size);
+    return ((uint32_t)p < (uint32_t)e.n && page >= 0 && r >= 0 && r < a.rows) ? (int32_t)r : -1;
 }
 
 // One lane's share of a cache row: lane group g (of 4) holds, for j = 0 .. 3, values 128j + 32g ..
 // 128j + 32g + 31: sixteen code bytes and two scales. The four groups read 64 consecutive bytes.
 struct RowPart {
     uint4 code[4];
-    uint32_t scale[4];
+    uint32_t scale[4];  // four scales; the lane's two are the low or (odd g) the high half
 };
 
-__device__ __forceinline__ void load_row(const AttendArgs& a, int32_t row, int g, RowPart& r) {
+// chunk j of a row; a row that is not there counts as zeros (codes are always finite)
+__device__ __forceinline__ void load_chunk(const AttendArgs& a, int32_t row, int g, int j, RowPart& r) {
     const int64_t at = row < 0 ? 0 : row;
-    const uint8_t* c = a.codes + at * 256 + g * 16;
-    const uint8_t* s = a.scales + at * 32 + g * 2;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        r.code[j] = *reinterpret_cast<const uint4*>(c + 64 * j);
-        r.scale[j] = *reinterpret_cast<const uint16_t*>(s + 8 * j);
-    }
-    // a row that is not there counts as zeros (codes are always finite)
-    if (row < 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r.scale[j] = 0;
-    }
+    r.code[j] = *reinterpret_cast<const uint4*>(a.codes + at * 256 + g * 16 + 64 * j);
+    r.scale[j] = *reinterpret_cast<const uint32_t*>(a.scales + at * 32 + (g >> 1) * 4 + 8 * j);
 }
 
-// values 8u .. 8u+7 of chunk j as fp16 (exact)
-__device__ __forceinline__ h8 values8(const RowPart& r, int j, int u) {
+// values 8u .. 8u+7 of chunk j as fp16 (exact); there: the row is in the cache
+__device__ __forceinline__ h8 values8(const RowPart& r, int j, int u, int g, bool there) {
     const uint32_t w = u == 0 ? r.code[j].x : u == 1 ? r.code[j].y : u == 2 ? r.code[j].z : r.code[j].w;
-    const h2 sp = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.scale[j], 1.0f, false);
+    const h2 sp = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(there ? (int)(r.scale[j] >> (16 * (g & 1))) : 0, 1.0f, false);
     const _Float16 s1 = u < 2 ? sp[0] : sp[1];
     const h2 s = {s1, s1};
     const h2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s;
@@ -125,20 +124,21 @@ __device__ __forceinline__ h8 values8(const RowPart& r, int j, int u) {
     return h8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
-// 32 query rows (heads h0 .. h0+31, rows past the last head as zeros) into LDS as scaled fp16, and
-// per head the factor that turns a dot product of theirs into s2: 8 rows per wavefront, a row per
-// step, 8 values per lane.
-__device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int h0, _Float16* lds, float* factor) {
+// ROWS query rows (heads h0 .. , rows past the last head as zeros) into LDS as scaled fp16, and per head
+// the factor that turns a dot product of theirs into s2: a row per wavefront and step, 8 values per lane.
+template <int ROWS>
+__device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int h0, _Float16* lds, float2* factor) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint4 raw[8];
+    constexpr int PER = ROWS / 4;
+    uint4 raw[PER];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int h = h0 + w * 8 + i;
+    for (int i = 0; i < PER; ++i) {
+        const int h = h0 + w * PER + i;
         raw[i] = uint4{0, 0, 0, 0};
         if (h < a.heads) raw[i] = *reinterpret_cast<const uint4*>(a.q + (t * a.heads + h) * kD + lane * 8);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         uint32_t m = 0;
 #pragma unroll
@@ -158,9 +158,23 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
             o[2 * c] = (_Float16)(__uint_as_float(v[c] << 16) * mul);
             o[2 * c + 1] = (_Float16)(__uint_as_float(v[c] & 0xffff0000u) * mul);
         }
-        *reinterpret_cast<h8*>(lds + (w * 8 + i) * kRow + lane * 8) = o;
-        if (lane == 0) factor[w * 8 + i] = a.scale * kLog2e * __uint_as_float((uint32_t)(e - 14) << 23);
+        *reinterpret_cast<h8*>(lds + (w * PER + i) * kRow + lane * 8) = o;
+        if (lane == 0) {
+            // (above zero or below it: a masked entry's product is an infinity of the other sign)
+            const float f = a.scale * kLog2e * __uint_as_float((uint32_t)(e - 14) << 23);
+            factor[w * PER + i] = float2{fabsf(f) < 0x1p-126f ? 0x1p-126f : f, -kNone};
+        }
     }
+}
+
+// the value of the lane 16 or 32 away (the four lane groups of one column)
+__device__ __forceinline__ float xor16(float v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float((threadIdx.x & 16) ? s[0] : s[1]);
+}
+__device__ __forceinline__ float xor32(float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? s[0] : s[1]);
 }
 
 // block -> (query and part, head tile): the head tiles of one query run on one XCD (blocks b and
@@ -172,178 +186,280 @@ __device__ __forceinline__ bool unit_of(uint32_t b, uint32_t units, uint32_t til
     return unit < units;
 }
 
-// Registers per lane: 128 of the queries, 64 of the outputs.
-__global__ __launch_bounds__(256, 2) void attend_kernel(const AttendArgs a, int splits) {
-    __shared__ __align__(16) _Float16 s_kv[kTile * kRow];
-    __shared__ __align__(16) _Float16 s_p[kHeadTile * kPRow];
-    __shared__ __align__(16) float s_m[kHeadTile][4];
-    __shared__ __align__(16) float s_l[kHeadTile][4];
-    __shared__ float s_factor[kHeadTile];
+// NH: heads of a block in sixteens
+template <int NH>
+struct Shared {
+    _Float16 kv[2][kTile * kRow];
+    _Float16 p[2][NH * 16 * kPRow];
+    float m[NH * 16][4];
+    float l[NH * 16][4];
+    int over[2][4];
+    float2 fr[NH * 16];                // per head: the factor of stage_query, and minus R
+    _Float16 q[NH * 16 * kQRow];       // the queries' last fragment (the registers hold 15 of 16)
+};
 
+// What a wavefront holds of the step at hand and of the next ones. Loads in flight: the rows of step + 1,
+// the page of step + 2, the position of step + 3.
+struct Feed {
+    RowPart kv;
+    int32_t row;             // of the step whose rows kv holds
+    int32_t pos1, page1;     // step + 1
+    int32_t pos2, page2;     // step + 2 (page2: still travelling)
+    int32_t pos3;            // step + 3 (still travelling)
+};
+
+template <int NH>
+__global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int splits) {
+    __shared__ __align__(16) Shared<NH> sh;
+    constexpr int kHeads = NH * 16;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int g = lane >> 4, c = lane & 15;
-    const uint32_t head_tiles = (a.heads + kHeadTile - 1) / kHeadTile;
+    const uint32_t head_tiles = (a.heads + kHeads - 1) / kHeads;
     uint32_t unit, tile;
     if (!unit_of(blockIdx.x, (uint32_t)a.nq * splits, head_tiles, unit, tile)) return;
     const int64_t t = unit / splits;
     const int part = (int)(unit % splits);
-    const int h0 = (int)tile * kHeadTile;
+    const int h0 = (int)tile * kHeads;
     const Entries e = entries_of(a, t);
     const int steps_all = (e.count + kTile - 1) / kTile;
     const int per = (steps_all + splits - 1) / splits;
     const int step0 = part * per;
-    const int step1 = min(step0 + per, steps_all);
+    const int steps = min(per, steps_all - step0);  // may be 0 or less
+    const int end = steps > 0 ? min((step0 + steps) * kTile, e.count) : 0;
+    const int i0 = step0 * kTile + w * 16 + c;      // this lane's entry of the first step
 
-    RowPart kv;
-    int32_t row = -1, row_next = -1;
-    if (step0 < step1) {
-        row = row_of(a, e, step0 * kTile + w * 16 + c);
-        load_row(a, row, g, kv);
-        row_next = row_of(a, e, (step0 + 1) * kTile + w * 16 + c);
+    Feed fd;
+    {
+        const int32_t p0 = position_of(e, i0, end);
+        fd.pos1 = position_of(e, i0 + kTile, end);
+        fd.pos2 = position_of(e, i0 + 2 * kTile, end);
+        const int32_t page0 = page_of(a, e, p0);
+        fd.page1 = page_of(a, e, fd.pos1);
+        fd.row = row_of(a, e, p0, page0);
+        if (steps > 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
+        }
     }
-
-    stage_query(a, t, h0, s_kv, s_factor);
+    stage_query<kHeads>(a, t, h0, sh.kv[1], sh.fr);
     __syncthreads();
-    h8 q[2][16];
-    float f[2];
+    h8 q[NH][15];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        f[hf] = s_factor[hf * 16 + c];
+    for (int n = 0; n < NH; ++n) {
+        if (w == 0)
+            *reinterpret_cast<h8*>(sh.q + (n * 16 + c) * kQRow + g * 8) =
+                *reinterpret_cast<const h8*>(sh.kv[1] + (n * 16 + c) * kRow + 3 * 128 + g * 32 + 3 * 8);
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-            q[hf][x] = *reinterpret_cast<const h8*>(s_kv + (hf * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
+        for (int x = 0; x < 15; ++x) {
+            q[n][x] = *reinterpret_cast<const h8*>(sh.kv[1] + (n * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
+            asm volatile("" : "+a"(q[n][x]));  // in the accumulation half of the register file: matrix operands only
+        }
     }
-    v4f o[2][8] = {};
-    float M[2] = {ninf(), ninf()};   // maximum (an integer) that all four wavefronts know
-    float m[2] = {ninf(), ninf()};   // reference of this wavefront's sum
-    float l[2] = {0.0f, 0.0f};       // this lane's part of it
+    __syncthreads();  // before kv[1] takes rows
+    v4f o[NH][8] = {};
+    v4f s[NH];
+    float l[NH];         // this lane's part of the sum of 2^(s2 - R)
+#pragma unroll
+    for (int n = 0; n < NH; ++n) l[n] = 0.0f;
 
-    for (int step = step0; step < step1; ++step) {
-        __syncthreads();  // the last step's reads of s_kv, s_p and s_m are done
-        v4f s[2] = {};
+    // One turn of the pipe: the first product of step `next` (into s, its rows into kv[buf ^ 1]) and the second
+    // product of the step before it (its probabilities and rows in p[buf] and kv[buf]), interleaved so that
+    // widening, LDS and loads run under the matrix instructions.
+    const auto turn = [&](auto first, auto last, int buf, int next) {
+        constexpr bool kPv = !decltype(first)::value, kQk = !decltype(last)::value;
+        _Float16* in = sh.kv[buf ^ 1] + (w * 16 + c) * kRow + g * 32;
+        const _Float16* out = sh.kv[buf] + (g * 8 + (c >> 2)) * kRow + w * 128 + (c & 3) * 4;
+        const _Float16* prob = sh.p[buf] + c * kPRow + g * 8;
+        // a transposed read: lane group g gets entries 32 (x / 8) + 8 g .. + 7 of value 16 (x % 8) + c
+        const auto rows8 = [&](int x) {
+            const _Float16* at = out + (x >> 3) * 32 * kRow + (x & 7) * 16;
+            const hv4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
+            const hv4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 4 * kRow));
+            h8 v;
+            __builtin_memcpy(&v, &lo, 8);
+            __builtin_memcpy((char*)&v + 8, &hi, 8);
+            return v;
+        };
+        const bool there = fd.row >= 0;
+        int32_t row1 = -1;
+        h8 k, v[3], p[NH], ql[NH];
+        if constexpr (kPv) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const h8 v = values8(kv, j, u);
-                s[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, q[0][j * 4 + u], s[0], 0, 0, 0);
-                s[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, q[1][j * 4 + u], s[1], 0, 0, 0);
-                *reinterpret_cast<h8*>(s_kv + (w * 16 + c) * kRow + j * 128 + g * 32 + u * 8) = v;
-            }
+            for (int n = 0; n < NH; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow);
+            v[0] = rows8(0);
+            v[1] = rows8(1);
         }
-        const uint32_t seen = (uint32_t)__ballot(row >= 0) >> (g * 4);
-        // the next step's rows travel while this one is finished
-        row = row_next;
-        if (step + 1 < step1) {
-            load_row(a, row, g, kv);
-            row_next = row_of(a, e, (step + 2) * kTile + w * 16 + c);
+        if constexpr (kQk) {
+            row1 = row_of(a, e, fd.pos1, fd.page1);
+            fd.page2 = page_of(a, e, fd.pos2);
+            fd.pos3 = position_of(e, i0 + (next + 3) * kTile, end);
+            k = values8(fd.kv, 0, 0, g, there);
+#pragma unroll
+            for (int n = 0; n < NH; ++n) s[n] = v4f{};
         }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float x[4];
-            float top = ninf();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = (seen >> i) & 1 ? s[hf][i] * f[hf] : ninf();
-                top = fmaxf(top, x[i]);
+        for (int x = 0; x < 16; ++x) {
+            if constexpr (kPv) {
+                if (x < 14) v[(x + 2) % 3] = rows8(x + 2);
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float mn = fmaxf(M[hf], ceilf(top));
-            const float ref = mn == ninf() ? 0.0f : mn - kPBits;
-            float sum = 0.0f;
-            h4 p;
+            if constexpr (kQk) {
+                const h8 kx = k;
+                *reinterpret_cast<h8*>(in + (x >> 2) * 128 + (x & 3) * 8) = kx;
+                if (x < 15) k = values8(fd.kv, (x + 1) >> 2, (x + 1) & 3, g, there);
+                if ((x & 3) == 3) load_chunk(a, row1, g, x >> 2, fd.kv);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ex = __builtin_amdgcn_exp2f(x[i] - ref);
-                sum += ex;
-                p[i] = (_Float16)ex;
+                for (int n = 0; n < NH; ++n) {
+                    if (x == 14) ql[n] = *reinterpret_cast<const h8*>(sh.q + (n * 16 + c) * kQRow + g * 8);
+                    s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, x < 15 ? q[n][x < 15 ? x : 0] : ql[n], s[n], 0, 0, 0);
+                }
             }
-            l[hf] = l[hf] * (m[hf] == ninf() ? 0.0f : __builtin_amdgcn_exp2f(m[hf] - mn)) + sum;
-            m[hf] = mn;
-            *reinterpret_cast<h4*>(s_p + (hf * 16 + c) * kPRow + w * 16 + g * 4) = p;
-            if (g == 0) s_m[hf * 16 + c][w] = mn;
+            if constexpr (kPv) {
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    o[n][x & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x % 3], p[n], o[n][x & 7], 0, 0, 0);
+                    if (x == 7) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow + 32);
+                }
+            }
+            // a matrix instruction takes 16 cycles, four times another: one of those into each gap
+#pragma unroll
+            for (int i = 0; i < NH * (kQk + kPv); ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (kQk) {
+            const uint64_t all = __ballot(there);
+            if (all != ~0ull) {
+                const uint32_t seen = (uint32_t)all >> (g * 4);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    const float hole = sh.fr[n * 16 + c].x < 0.0f ? __builtin_inff() : ninf();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[n][i] = (seen >> i) & 1 ? s[n][i] : hole;
+                }
+            }
+            fd.row = row1;
+            fd.pos1 = fd.pos2;
+            fd.page1 = fd.page2;
+            fd.pos2 = fd.pos3;
+        }
+    };
+
+    // The products s of a step to probabilities 2^(s2 - R) in p[buf]. R is set kRoom below the largest logit at
+    // hand. Where one comes to lie more than kMost above R (seldom after the first step), the four wavefronts
+    // agree on new references and bring outputs and sums to them (powers of two, exact), and the step is done again.
+    const auto softmax = [&](int buf) {
+        float sum[NH];
+        const auto store = [&]() {
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                const float2 fr = sh.fr[n * 16 + c];
+                const float f = fr.x, minus = fr.y;
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s[n][i], f, minus);
+                over |= fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kMost;
+                h4 x;
+                sum[n] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float ex = __builtin_amdgcn_exp2f(y[i]);
+                    sum[n] += ex;
+                    x[i] = (_Float16)ex;
+                }
+                *reinterpret_cast<h4*>(sh.p[buf] + (n * 16 + c) * kPRow + w * 16 + g * 4) = x;
+            }
+            return over;
+        };
+        const int over = __any(store());
+        if (lane == 0) sh.over[buf][w] = over;
         __syncthreads();
-        // bring the four wavefronts' probabilities to one maximum: powers of two, exact
-        h8 p[2][2];
+        const int4 ov = *reinterpret_cast<const int4*>(sh.over[buf]);
+        if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const v4f mv = *reinterpret_cast<const v4f*>(s_m[hf * 16 + c]);
-            const float mx = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
-            const float shift = mx == ninf() ? 0.0f : mx;
-            const float alpha = __builtin_amdgcn_exp2f(M[hf] - shift);  // 0 before the first maximum (o is 0 then)
-            M[hf] = mx;
+            for (int n = 0; n < NH; ++n) {
+                const float2 fr = sh.fr[n * 16 + c];
+                const float f = fr.x;
+                float top = ninf();
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const float mw = g < 2 ? mv[2 * ks] : mv[2 * ks + 1];
-                const _Float16 r = (_Float16)__builtin_amdgcn_exp2f(mw - shift);
-                p[hf][ks] = *reinterpret_cast<const h8*>(s_p + (hf * 16 + c) * kPRow + ks * 32 + g * 8) * r;
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][i] * f);
+                top = fmaxf(top, xor16(top));
+                top = fmaxf(top, xor32(top));
+                if (g == 0) sh.m[n * 16 + c][w] = top + fr.y > kMost ? ceilf(top) - kRoom : -fr.y;
             }
-            if (__any(alpha != 1.0f)) {
+            __syncthreads();
+            float s_r[NH];
 #pragma unroll
-                for (int d = 0; d < 8; ++d) o[hf][d] *= alpha;
+            for (int n = 0; n < NH; ++n) {
+                const v4f mv = *reinterpret_cast<const v4f*>(sh.m[n * 16 + c]);
+                const float r = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
+                const float alpha = __builtin_amdgcn_exp2f(-sh.fr[n * 16 + c].y - r);  // 0 at a head's first entry (o is 0 then)
+#pragma unroll
+                for (int d = 0; d < 8; ++d) o[n][d] *= alpha;
+                l[n] *= alpha;
+                s_r[n] = r;
             }
+            __syncthreads();  // every wavefront has read the old references
+            if (w == 0 && g == 0) {
+#pragma unroll
+                for (int n = 0; n < NH; ++n) sh.fr[n * 16 + c].y = -s_r[n];
+            }
+            __syncthreads();
+            store();
+            __syncthreads();
         }
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                // a transposed read: lane group g gets entries 32 ks + 8 g .. + 7 of value 16 d + c
-                _Float16* at = s_kv + (ks * 32 + g * 8 + (c >> 2)) * kRow + w * 128 + d * 16 + (c & 3) * 4;
-                const hv4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
-                const hv4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 4 * kRow));
-                h8 v;
-                __builtin_memcpy(&v, &lo, 8);
-                __builtin_memcpy((char*)&v + 8, &hi, 8);
-                o[0][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[0][ks], o[0][d], 0, 0, 0);
-                o[1][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[1][ks], o[1][d], 0, 0, 0);
-            }
+        for (int n = 0; n < NH; ++n) l[n] += sum[n];
+    };
+
+    if (steps > 0) {
+        turn(std::true_type{}, std::false_type{}, 1, 0);
+        for (int step = 0; step + 1 < steps; ++step) {
+            softmax(step & 1);
+            turn(std::false_type{}, std::false_type{}, step & 1, step + 1);
         }
+        softmax((steps - 1) & 1);
+        turn(std::false_type{}, std::true_type{}, (steps - 1) & 1, steps);
     }
 
-    // the sum over the four lane groups and the four wavefronts, each relative to its own maximum
-    __syncthreads();
+    // the sum over the four lane groups and the four wavefronts
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        float x = l[hf];
-        x += __shfl_xor(x, 16);
-        x += __shfl_xor(x, 32);
-        if (g == 0) {
-            s_l[hf * 16 + c][w] = x;
-            s_m[hf * 16 + c][w] = m[hf];
-        }
+    for (int n = 0; n < NH; ++n) {
+        float x = l[n];
+        x += xor16(x);
+        x += xor32(x);
+        if (g == 0) sh.l[n * 16 + c][w] = x;
     }
     __syncthreads();
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        const int hl = hf * 16 + c;
-        const v4f mv = *reinterpret_cast<const v4f*>(s_m[hl]);
-        const v4f lv = *reinterpret_cast<const v4f*>(s_l[hl]);
-        float L = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) L += mv[i] == ninf() ? 0.0f : lv[i] * __builtin_amdgcn_exp2f(mv[i] - M[hf]);
+    for (int n = 0; n < NH; ++n) {
+        const int hl = n * 16 + c;
+        const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
+        const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]);
         const int h = h0 + hl;
+        if (h >= a.heads) continue;
         if (splits > 1) {
-            const int64_t r = (int64_t)(unit * head_tiles + tile) * kHeadTile + hl;
+            const int64_t r = (int64_t)unit * a.heads + h;
             float* po = a.part_o + r * kD + w * 128 + g * 4;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) *reinterpret_cast<v4f*>(po + d * 16) = o[hf][d];
+            for (int d = 0; d < 8; ++d) *reinterpret_cast<v4f*>(po + d * 16) = o[n][d];
             if (w == 0 && g == 0) {
-                a.part_ml[2 * r] = M[hf];
+                a.part_ml[2 * r] = -sh.fr[hl].y;
                 a.part_ml[2 * r + 1] = L;
             }
-        } else if (h < a.heads) {
+        } else {
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             uint16_t* po = a.out + (t * a.heads + h) * kD + w * 128 + g * 4;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
-                const v4f y = o[hf][d] * inv;
+                const v4f y = o[n][d] * inv;
                 *reinterpret_cast<uint2*>(po + d * 16) = uint2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
             }
             if (a.lse && w == 0 && g == 0)
-                a.lse[t * a.heads + h] = L == 0.0f ? ninf() : (M[hf] + __builtin_amdgcn_logf(L) - kPBits) * kLn2;
+                a.lse[t * a.heads + h] = L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) - sh.fr[hl].y) * kLn2;
         }
     }
 }
@@ -352,17 +468,15 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(const AttendArgs a, int 
 __global__ __launch_bounds__(128) void attend_join_kernel(const AttendArgs a, int splits) {
     const int64_t t = blockIdx.x / a.heads;
     const int h = (int)(blockIdx.x % a.heads);
-    const int head_tiles = (a.heads + kHeadTile - 1) / kHeadTile;
-    const int64_t first = ((t * splits) * head_tiles + h / kHeadTile) * kHeadTile + h % kHeadTile;
-    const int64_t step = (int64_t)head_tiles * kHeadTile;
-    float M = ninf();
+    const int64_t first = t * splits * a.heads + h;
+    const int64_t step = a.heads;
+    float M = kNone;
     for (int i = 0; i < splits; ++i) M = fmaxf(M, a.part_ml[2 * (first + i * step)]);
-    const float ref = M == ninf() ? 0.0f : M;
     float L = 0.0f;
     v4f o = {};
     for (int i = 0; i < splits; ++i) {
         const int64_t r = first + i * step;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * r] - ref);
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * r] - M);
         L += f * a.part_ml[2 * r + 1];
         o += f * *reinterpret_cast<const v4f*>(a.part_o + r * kD + threadIdx.x * 4);
     }
@@ -371,8 +485,10 @@ __global__ __launch_bounds__(128) void attend_join_kernel(const AttendArgs a, in
     *reinterpret_cast<uint2*>(a.out + (int64_t)blockIdx.x * kD + threadIdx.x * 4) =
         uint2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
     if (a.lse && threadIdx.x == 0)
-        a.lse[blockIdx.x] = L == 0.0f ? ninf() : (M + __builtin_amdgcn_logf(L) - kPBits) * kLn2;
+        a.lse[blockIdx.x] = L == 0.0f ? ninf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
+
+constexpr int kWeightHeads = 32;
 
 // The attention's probability of every entry, mean over the heads, from the saved lse:
 //   w_i = 1/H sum_h exp(s_{h,i} - lse_h).
@@ -381,8 +497,8 @@ __global__ __launch_bounds__(128) void attend_join_kernel(const AttendArgs a, in
 __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,
                                                                 float* __restrict__ weights, int64_t w_stride,
                                                                 int splits) {
-    __shared__ __align__(16) _Float16 s_q[kHeadTile * kRow];
-    __shared__ float s_factor[kHeadTile];
+    __shared__ __align__(16) _Float16 s_q[kWeightHeads * kRow];
+    __shared__ float2 s_factor[kWeightHeads];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int g = lane >> 4, c = lane & 15;
@@ -403,9 +519,9 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
     }
     const float mean = 1.0f / (float)a.heads;
 
-    for (int h0 = 0; h0 < a.heads; h0 += kHeadTile) {
+    for (int h0 = 0; h0 < a.heads; h0 += kWeightHeads) {
         __syncthreads();
-        stage_query(a, t, h0, s_q, s_factor);
+        stage_query<kWeightHeads>(a, t, h0, s_q, s_factor);
         __syncthreads();
         h8 q[2][16];
         float f[2][4], off[2][4];
@@ -414,7 +530,7 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int hl = hf * 16 + g * 4 + i;
-                f[hf][i] = s_factor[hl];
+                f[hf][i] = s_factor[hl].x;
                 // a head that is not there, or that saw nothing, adds nothing
                 float y = h0 + hl < a.heads ? lse[t * a.heads + h0 + hl] : ninf();
                 off[hf][i] = y == ninf() ? __builtin_inff() : y * kLog2e;
@@ -426,15 +542,17 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
         }
         for (int step = step0; step < step1; ++step) {
             const int i = step * kTile + w * 16 + c;
-            const int32_t row = row_of(a, e, i);
+            const int32_t pos = position_of(e, i, e.count);
+            const int32_t row = row_of(a, e, pos, page_of(a, e, pos));
             RowPart kv;
-            load_row(a, row, g, kv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_chunk(a, row, g, j, kv);
             v4f s[2] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const h8 v = values8(kv, j, u);
+                    const h8 v = values8(kv, j, u, g, row >= 0);
                     s[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[0][j * 4 + u], v, s[0], 0, 0, 0);
                     s[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[1][j * 4 + u], v, s[1], 0, 0, 0);
                 }
@@ -457,45 +575,76 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
 
 }  // namespace
 
-// Parts per query: enough blocks for two on each of the 256 compute units, at least one step of 64
-// entries each.
-int attend_splits(int32_t nq, int32_t heads, int64_t entries) {
-    if (nq <= 0 || heads <= 0 || entries <= 0) return 1;
-    const int64_t blocks = (int64_t)nq * ((heads + kHeadTile - 1) / kHeadTile);
+namespace {
+
+// How a call is cut: head sixteens of a block and parts of a query's entries. Large head tiles widen a row
+// for more heads, small ones and parts give blocks: the largest tile that leaves a block for each of the 256
+// compute units, else the smallest, and then as many parts as fill them (at least one step each).
+struct Cut {
+    int nh, splits;
+};
+Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
+    const auto blocks = [&](int nh) { return (int64_t)nq * ((heads + 16 * nh - 1) / (16 * nh)); };
+    int nh = heads > 32 ? 4 : heads > 16 ? 2 : 1;
+    while (nh > 1 && blocks(nh) < 256) nh /= 2;
     const int64_t steps = (entries + kTile - 1) / kTile;
-    const int64_t want = (512 + blocks - 1) / blocks;
-    return (int)(want < steps ? want : steps);
+    const int64_t want = (256 + blocks(nh) - 1) / blocks(nh);
+    return Cut{nh, (int)(want < steps ? want : (steps < 1 ? 1 : steps))};
 }
 
+// p / page_size for 0 <= p < 2^30 as a product: with 2^(b-1) < d <= 2^b, mul = floor(2^(31+b) / d) + 1 (below 2^32
+// for d > 1) exceeds 2^(31+b) / d by at most 1, so p * mul / 2^(31+b) exceeds p / d by at most p / 2^(31+b) < 1 / (2 d):
+// the floors agree.
+void set_page_division(AttendArgs& a) {
+    if (!a.pages || a.page_size == 1) return;
+    int b = 1;
+    while (((int64_t)1 << b) < a.page_size) ++b;
+    a.page_mul = (uint32_t)(((uint64_t)1 << (31 + b)) / (uint64_t)a.page_size + 1);
+    a.page_shift = b - 1;
+}
+
+template <int NH>
+void launch_attend_as(const AttendArgs& a, int splits, hipStream_t stream) {
+    const uint32_t units = (uint32_t)a.nq * splits, head_tiles = (a.heads + 16 * NH - 1) / (16 * NH);
+    hipLaunchKernelGGL(attend_kernel<NH>, dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, splits);
+}
+
+}  // namespace
+
 size_t attend_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
-    const int64_t splits = attend_splits(nq, heads, entries);
-    if (splits <= 1) return 16;
-    const size_t rows = (size_t)nq * splits * ((heads + kHeadTile - 1) / kHeadTile) * kHeadTile;
-    return rows * (kD + 2) * sizeof(float);
+    if (nq <= 0 || entries <= 0) return 16;
+    const int splits = cut_of(nq, heads, entries).splits;
+    return splits <= 1 ? 16 : (size_t)nq * splits * heads * (kD + 2) * sizeof(float);
 }
 
 hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream) {
     const int64_t entries = a.idx ? a.k : (a.window > 0 && a.window < a.max_n ? a.window : a.max_n);
-    const int splits = attend_splits(a.nq, a.heads, entries);
-    const uint32_t head_tiles = (a.heads + kHeadTile - 1) / kHeadTile;
-    if (splits > 1) {
-        const size_t rows = (size_t)a.nq * splits * head_tiles * kHeadTile;
+    const Cut cut = cut_of(a.nq, a.heads, entries);
+    set_page_division(a);
+    if (cut.splits > 1) {
         a.part_o = (float*)ws;
-        a.part_ml = a.part_o + rows * kD;
+        a.part_ml = a.part_o + (size_t)a.nq * cut.splits * a.heads * kD;
     }
-    const uint32_t units = (uint32_t)a.nq * splits;
-    hipLaunchKernelGGL(attend_kernel, dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, splits);
+    if (cut.nh == 4)
+        launch_attend_as<4>(a, cut.splits, stream);
+    else if (cut.nh == 2)
+        launch_attend_as<2>(a, cut.splits, stream);
+    else
+        launch_attend_as<1>(a, cut.splits, stream);
     hipError_t err = hipGetLastError();
-    if (err != hipSuccess || splits <= 1) return err;
-    hipLaunchKernelGGL(attend_join_kernel, dim3((uint32_t)a.nq * a.heads), dim3(128), 0, stream, a, splits);
+    if (err != hipSuccess || cut.splits <= 1) return err;
+    hipLaunchKernelGGL(attend_join_kernel, dim3((uint32_t)a.nq * a.heads), dim3(128), 0, stream, a, cut.splits);
     return hipGetLastError();
 }
 
-hipError_t launch_attend_weights(const AttendArgs& a, const float* lse, float* weights, int64_t w_stride,
+hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights, int64_t w_stride,
                                  hipStream_t stream) {
     const int64_t entries = a.idx ? a.k : a.max_n;
     if (entries == 0) return hipSuccess;
-    const int splits = attend_splits(a.nq, kHeadTile, entries);
+    set_page_division(a);
+    // two blocks for each compute unit, at least one step of 64 entries each
+    const int64_t steps = (entries + kTile - 1) / kTile, want = (512 + a.nq - 1) / a.nq;
+    const int splits = (int)(want < steps ? want : steps);
     hipLaunchKernelGGL(attend_weights_kernel, dim3((uint32_t)a.nq * splits), dim3(256), 0, stream, a, lse, weights,
                        w_stride, splits);
     return hipGetLastError();

@@ -38,13 +38,15 @@ struct AttendArgs {
     float scale;
     uint16_t* out;          // bf16 [nq][heads][512]
     float* lse;             // [nq][heads] or null
-    float* part_o;          // set by the launch
+    uint32_t page_mul;      // set by the launch: p / page_size = (p * page_mul >> 32) >> page_shift
+    int32_t page_shift;
+    float* part_o;
     float* part_ml;
 };
 // entries: list slots, or the most positions a query attends to
 size_t attend_workspace_bytes(int32_t nq, int32_t heads, int64_t entries);
 hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream);
-hipError_t launch_attend_weights(const AttendArgs& a, const float* lse, float* weights, int64_t w_stride,
+hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights, int64_t w_stride,
                                  hipStream_t stream);
 
 // rotary positions
