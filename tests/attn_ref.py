@@ -63,11 +63,11 @@ def out_tolerance(r, n):
     """bf16 result, half a step: 2^-8 |o|. Probabilities in 11 bits: 2^-11 A. Logits: 512 fp32 additions in any
     order, 2^-24 each, of terms that sum to B, and the product with scale: 513 * 2^-24 B, in the probability and
     in the sum; their exponential, 2^-22 relative and |s| 2^-23 of the base-2 logit. n fp32 additions of p kv and
-    of the sum. A probability below 2^-23 of the largest is off by
-    up to half a step of fp16's smallest numbers, 2^-25 where the largest is above 2^9: 2^-34 of it, n times."""
+    of the sum. A probability below 2^-20 of the largest is off by
+    up to half a step of fp16's smallest numbers, 2^-25 where the largest is above 2^6: 2^-31 of it, n times."""
     big = np.abs(r["s"]).max(initial=0.0)
     rel = 2.0 ** -11 + 2 * (513 * 2.0 ** -24 * r["B"] + 2.0 ** -22 + big * 2.0 ** -22) + 2 * n * 2.0 ** -24
-    return 2.0 ** -8 * np.abs(r["out"]) + r["A"] * rel + n * 2.0 ** -34 * 2688
+    return 2.0 ** -8 * np.abs(r["out"]) + r["A"] * rel + n * 2.0 ** -31 * 2688
 
 
 def lse_tolerance(r, n):

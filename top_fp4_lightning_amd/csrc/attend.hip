@@ -16,7 +16,7 @@
 // value to [2^14, 2^15); its bf16 values are then exact in fp16 down to 2^-28 of the row's largest
 // (below that they lose bits worth less than 2^-39 of it). Products and sums are fp32 in the matrix
 // units. Probabilities enter the second product as fp16 values (11 bits) up to 2^15, the largest so far of a
-// head above 2^9: values down to 2^-23 of it are normal numbers, and what rounds to zero is below 2^-34 of it.
+// head above 2^6: values down to 2^-20 of it are normal numbers, and what rounds to zero is below 2^-31 of it.
 #include <type_traits>
 
 #include "operators.h"
@@ -30,7 +30,7 @@ constexpr int kRow = kD + 16;    // LDS row of a tile in fp16 values (the pad sp
 constexpr int kPRow = kTile + 8;
 constexpr int kQRow = 32;
 constexpr float kNone = -3.0e38f;  // reference of a head that has met no entry
-constexpr float kRoom = 10.0f;   // the reference lies this far below the largest logit (base 2) when it is set
+constexpr float kRoom = 7.0f;   // the reference lies this far below the largest logit (base 2) when it is set
 constexpr float kMost = 15.0f;   // and a logit at most this far above it: probabilities up to 2^15
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -124,6 +124,34 @@ __device__ __forceinline__ h8 values8(const RowPart& r, int j, int u, int g, boo
     return h8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
+// exchanges inside a wavefront without LDS: a value moved by a data-parallel-primitive pattern, and the two lanes
+// that lie 16 or 32 apart joined
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max(s[0], s[1]);
+}
+__device__ __forceinline__ uint32_t max32(uint32_t v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(s[0], s[1]);
+}
+// over the four lane groups of a column
+__device__ __forceinline__ float group_max(float v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // ROWS query rows (heads h0 .. , rows past the last head as zeros) into LDS as scaled fp16, and per head
 // the factor that turns a dot product of theirs into s2: a row per wavefront and step, 8 values per lane.
 template <int ROWS>
@@ -133,9 +161,9 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
     uint4 raw[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int h = h0 + w * PER + i;
-        raw[i] = uint4{0, 0, 0, 0};
-        if (h < a.heads) raw[i] = *reinterpret_cast<const uint4*>(a.q + (t * a.heads + h) * kD + lane * 8);
+        const int h = h0 + w * PER + i, hc = h < a.heads ? h : a.heads - 1;
+        raw[i] = *reinterpret_cast<const uint4*>(a.q + (t * a.heads + hc) * kD + lane * 8);
+        if (h != hc) raw[i] = uint4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -146,8 +174,12 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
             const uint32_t hi = v[c] & 0x7fff0000u, lo = (v[c] << 16) & 0x7fff0000u;
             m = max(m, max(hi, lo));
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        m = max(m, dpp<0xB1>(m));   // quad_perm [1,0,3,2]
+        m = max(m, dpp<0x4E>(m));   // quad_perm [2,3,0,1]
+        m = max(m, dpp<0x141>(m));  // row_half_mirror
+        m = max(m, dpp<0x140>(m));  // row_mirror
+        m = max16(m);
+        m = max32(m);
         // 2^(14 - exponent of the largest), a power of two kept inside the normal range
         int e = (int)(m >> 23);
         e = e < 15 ? 15 : (e > 254 ? 254 : e);
@@ -165,16 +197,6 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
             factor[w * PER + i] = float2{fabsf(f) < 0x1p-126f ? 0x1p-126f : f, -kNone};
         }
     }
-}
-
-// the value of the lane 16 or 32 away (the four lane groups of one column)
-__device__ __forceinline__ float xor16(float v) {
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float((threadIdx.x & 16) ? s[0] : s[1]);
-}
-__device__ __forceinline__ float xor32(float v) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float((threadIdx.x & 32) ? s[0] : s[1]);
 }
 
 // block -> (query and part, head tile): the head tiles of one query run on one XCD (blocks b and
@@ -198,14 +220,13 @@ struct Shared {
     _Float16 q[NH * 16 * kQRow];       // the queries' last fragment (the registers hold 15 of 16)
 };
 
-// What a wavefront holds of the step at hand and of the next ones. Loads in flight: the rows of step + 1,
-// the page of step + 2, the position of step + 3.
+// What a wavefront holds of the next steps: rows are found for four steps at a time (lane group g: the g-th), and
+// travel one step ahead.
 struct Feed {
     RowPart kv;
-    int32_t row;             // of the step whose rows kv holds
-    int32_t pos1, page1;     // step + 1
-    int32_t pos2, page2;     // step + 2 (page2: still travelling)
-    int32_t pos3;            // step + 3 (still travelling)
+    int32_t row;          // of the step whose rows kv holds
+    int32_t rows4;        // of the four steps at hand
+    int32_t pos, page;    // of the next four
 };
 
 template <int NH>
@@ -227,16 +248,16 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     const int step0 = part * per;
     const int steps = min(per, steps_all - step0);  // may be 0 or less
     const int end = steps > 0 ? min((step0 + steps) * kTile, e.count) : 0;
-    const int i0 = step0 * kTile + w * 16 + c;      // this lane's entry of the first step
+    const int i0 = (step0 + g) * kTile + w * 16 + c;  // this lane's entry of the first four steps
 
     Feed fd;
+    const auto row_of_step = [&](int i) { return __builtin_amdgcn_ds_bpermute(((i & 3) * 16 + c) * 4, fd.rows4); };
     {
-        const int32_t p0 = position_of(e, i0, end);
-        fd.pos1 = position_of(e, i0 + kTile, end);
-        fd.pos2 = position_of(e, i0 + 2 * kTile, end);
-        const int32_t page0 = page_of(a, e, p0);
-        fd.page1 = page_of(a, e, fd.pos1);
-        fd.row = row_of(a, e, p0, page0);
+        const int32_t p = position_of(e, i0, end);
+        fd.pos = position_of(e, i0 + 4 * kTile, end);
+        fd.page = 0;
+        fd.rows4 = row_of(a, e, p, page_of(a, e, p));
+        fd.row = row_of_step(0);
         if (steps > 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
@@ -247,33 +268,86 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     h8 q[NH][15];
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-        if (w == 0)
-            *reinterpret_cast<h8*>(sh.q + (n * 16 + c) * kQRow + g * 8) =
-                *reinterpret_cast<const h8*>(sh.kv[1] + (n * 16 + c) * kRow + 3 * 128 + g * 32 + 3 * 8);
+        const _Float16* at = sh.kv[1] + (n * 16 + c) * kRow + g * 32;
 #pragma unroll
-        for (int x = 0; x < 15; ++x) {
-            q[n][x] = *reinterpret_cast<const h8*>(sh.kv[1] + (n * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
-            asm volatile("" : "+a"(q[n][x]));  // in the accumulation half of the register file: matrix operands only
-        }
+        for (int x = 0; x < 15; ++x) q[n][x] = *reinterpret_cast<const h8*>(at + (x >> 2) * 128 + (x & 3) * 8);
+        const h8 ql = *reinterpret_cast<const h8*>(at + 3 * 128 + 3 * 8);
+        if (w == 0) *reinterpret_cast<h8*>(sh.q + (n * 16 + c) * kQRow + g * 8) = ql;
+        // in the accumulation half of the register file: matrix operands only
+#pragma unroll
+        for (int x = 0; x < 15; ++x) asm volatile("" : "+a"(q[n][x]));
     }
     __syncthreads();  // before kv[1] takes rows
     v4f o[NH][8] = {};
     v4f s[NH];
     float l[NH];         // this lane's part of the sum of 2^(s2 - R)
+    float sum[NH];       // and of the step whose probabilities were formed last
 #pragma unroll
     for (int n = 0; n < NH; ++n) l[n] = 0.0f;
 
-    // One turn of the pipe: the first product of step `next` (into s, its rows into kv[buf ^ 1]) and the second
-    // product of the step before it (its probabilities and rows in p[buf] and kv[buf]), interleaved so that
-    // widening, LDS and loads run under the matrix instructions.
-    const auto turn = [&](auto first, auto last, int buf, int next) {
-        constexpr bool kPv = !decltype(first)::value, kQk = !decltype(last)::value;
+    // Probabilities 2^(s2 - R) of sixteen heads' products s into p[step & 1]; true if a logit lies too far above R.
+    const auto probabilities = [&](int n, float2 fr, int step) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s[n][i], fr.x, fr.y);
+        h4 x;
+        sum[n] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float ex = __builtin_amdgcn_exp2f(y[i]);
+            sum[n] += ex;
+            x[i] = (_Float16)ex;
+        }
+        *reinterpret_cast<h4*>(sh.p[step & 1] + (n * 16 + c) * kPRow + w * 16 + g * 4) = x;
+        return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kMost;
+    };
+    // R is set kRoom below the largest logit at hand. Where one comes to lie more than kMost above R (seldom after the
+    // first step), the four wavefronts agree on a new R and bring outputs and sums to it (powers of two, exact), and
+    // the step's probabilities are formed again.
+    const auto rebase = [&](int step) {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const float2 fr = sh.fr[n * 16 + c];
+            float top = ninf();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][i] * fr.x);
+            top = group_max(top);
+            if (g == 0) sh.m[n * 16 + c][w] = top + fr.y > kMost ? ceilf(top) - kRoom : -fr.y;
+        }
+        __syncthreads();
+        float r[NH];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const v4f mv = *reinterpret_cast<const v4f*>(sh.m[n * 16 + c]);
+            r[n] = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
+            const float alpha = __builtin_amdgcn_exp2f(-sh.fr[n * 16 + c].y - r[n]);  // 0 at a head's first entry (o is 0 then)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[n][d] *= alpha;
+            l[n] *= alpha;
+        }
+        __syncthreads();  // every wavefront has read the old references
+        if (w == 0 && g == 0) {
+#pragma unroll
+            for (int n = 0; n < NH; ++n) sh.fr[n * 16 + c].y = -r[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NH; ++n) probabilities(n, sh.fr[n * 16 + c], step);
+        __syncthreads();
+    };
+
+    // Turn i of the pipe, after a barrier: the first product of step i + 1 and the second product of step i, then the
+    // probabilities of step i + 1 under the rest of the second product. Widening, exponentials, LDS and loads run
+    // under the matrix instructions: one takes 16 cycles, four times another instruction.
+    const auto turn = [&](auto pv, auto qk, int i) {
+        constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value;
+        const int buf = i & 1;
         _Float16* in = sh.kv[buf ^ 1] + (w * 16 + c) * kRow + g * 32;
         const _Float16* out = sh.kv[buf] + (g * 8 + (c >> 2)) * kRow + w * 128 + (c & 3) * 4;
         const _Float16* prob = sh.p[buf] + c * kPRow + g * 8;
-        // a transposed read: lane group g gets entries 32 (x / 8) + 8 g .. + 7 of value 16 (x % 8) + c
-        const auto rows8 = [&](int x) {
-            const _Float16* at = out + (x >> 3) * 32 * kRow + (x & 7) * 16;
+        // a transposed read: lane group g gets entries 32 (y / 8) + 8 g .. + 7 of value 16 (y % 8) + c
+        const auto rows8 = [&](int y) {
+            const _Float16* at = out + (y >> 3) * 32 * kRow + (y & 7) * 16;
             const hv4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
             const hv4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 4 * kRow));
             h8 v;
@@ -281,28 +355,54 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             __builtin_memcpy((char*)&v + 8, &hi, 8);
             return v;
         };
-        const bool there = fd.row >= 0;
-        int32_t row1 = -1;
-        h8 k, v[3], p[NH], ql[NH];
+        h8 k, v[4], p[NH], ql[NH];
+        int4 ov{0, 0, 0, 0};
         if constexpr (kPv) {
+            ov = *reinterpret_cast<const int4*>(sh.over[buf]);
 #pragma unroll
             for (int n = 0; n < NH; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow);
             v[0] = rows8(0);
-            v[1] = rows8(1);
         }
+        const bool there = fd.row >= 0;
+        int32_t row1 = -1;
         if constexpr (kQk) {
-            row1 = row_of(a, e, fd.pos1, fd.page1);
-            fd.page2 = page_of(a, e, fd.pos2);
-            fd.pos3 = position_of(e, i0 + (next + 3) * kTile, end);
+            const int ahead = i + 2;
+            if ((ahead & 3) == 2) fd.page = page_of(a, e, fd.pos);
+            if ((ahead & 3) == 0) {
+                fd.rows4 = row_of(a, e, fd.pos, fd.page);
+                fd.pos = position_of(e, i0 + (ahead + 4) * kTile, end);
+            }
+            row1 = row_of_step(ahead);
             k = values8(fd.kv, 0, 0, g, there);
+        }
+        if constexpr (kPv) {
+            if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
+                rebase(i);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow);
+            }
+#pragma unroll
+            for (int n = 0; n < NH; ++n) l[n] += sum[n];
+        }
+        // y-th unit of the second product: entries 32 (y / 8) .. + 31 of values 16 (y % 8) .. + 15
+        const auto unit = [&](int y) {
+            // operands are read one unit ahead, three where units follow each other closely
+            const auto ahead = [](int u) { return u < 0 ? 0 : u + 1 + (u >= 4) + (u >= 6); };
+#pragma unroll
+            for (int r = 1; r < 16; ++r)
+                if (r > ahead(y - 1) && r <= ahead(y)) v[r & 3] = rows8(r);
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                o[n][y & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y & 3], p[n], o[n][y & 7], 0, 0, 0);
+                if (y == 7) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow + 32);
+            }
+        };
+        if constexpr (kQk) {
 #pragma unroll
             for (int n = 0; n < NH; ++n) s[n] = v4f{};
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-            if constexpr (kPv) {
-                if (x < 14) v[(x + 2) % 3] = rows8(x + 2);
-            }
             if constexpr (kQk) {
                 const h8 kx = k;
                 *reinterpret_cast<h8*>(in + (x >> 2) * 128 + (x & 3) * 8) = kx;
@@ -315,122 +415,65 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
                 }
             }
             if constexpr (kPv) {
-#pragma unroll
-                for (int n = 0; n < NH; ++n) {
-                    o[n][x & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x % 3], p[n], o[n][x & 7], 0, 0, 0);
-                    if (x == 7) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow + 32);
-                }
+                if (!kQk || (x & 1)) unit(kQk ? x >> 1 : x);
             }
-            // a matrix instruction takes 16 cycles, four times another: one of those into each gap
 #pragma unroll
-            for (int i = 0; i < NH * (kQk + kPv); ++i) {
+            for (int y = 0; y < NH * (kQk + (kPv && (x & 1))); ++y) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x2, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (kQk) {
             const uint64_t all = __ballot(there);
+            float2 fr[NH];
+#pragma unroll
+            for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
             if (all != ~0ull) {
                 const uint32_t seen = (uint32_t)all >> (g * 4);
 #pragma unroll
                 for (int n = 0; n < NH; ++n) {
-                    const float hole = sh.fr[n * 16 + c].x < 0.0f ? __builtin_inff() : ninf();
+                    const float hole = fr[n].x < 0.0f ? __builtin_inff() : ninf();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[n][i] = (seen >> i) & 1 ? s[n][i] : hole;
+                    for (int y = 0; y < 4; ++y) s[n][y] = (seen >> y) & 1 ? s[n][y] : hole;
                 }
             }
             fd.row = row1;
-            fd.pos1 = fd.pos2;
-            fd.page1 = fd.page2;
-            fd.pos2 = fd.pos3;
-        }
-    };
-
-    // The products s of a step to probabilities 2^(s2 - R) in p[buf]. R is set kRoom below the largest logit at
-    // hand. Where one comes to lie more than kMost above R (seldom after the first step), the four wavefronts
-    // agree on new references and bring outputs and sums to them (powers of two, exact), and the step is done again.
-    const auto softmax = [&](int buf) {
-        float sum[NH];
-        const auto store = [&]() {
             bool over = false;
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
-                const float2 fr = sh.fr[n * 16 + c];
-                const float f = fr.x, minus = fr.y;
-                float y[4];
+                if constexpr (kPv) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(s[n][i], f, minus);
-                over |= fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kMost;
-                h4 x;
-                sum[n] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float ex = __builtin_amdgcn_exp2f(y[i]);
-                    sum[n] += ex;
-                    x[i] = (_Float16)ex;
+                    for (int y = 8 + n * 8 / NH; y < 8 + (n + 1) * 8 / NH; ++y) unit(y);
                 }
-                *reinterpret_cast<h4*>(sh.p[buf] + (n * 16 + c) * kPRow + w * 16 + g * 4) = x;
+                over |= probabilities(n, fr[n], i + 1);
+                if constexpr (kPv) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            return over;
-        };
-        const int over = __any(store());
-        if (lane == 0) sh.over[buf][w] = over;
-        __syncthreads();
-        const int4 ov = *reinterpret_cast<const int4*>(sh.over[buf]);
-        if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                const float2 fr = sh.fr[n * 16 + c];
-                const float f = fr.x;
-                float top = ninf();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][i] * f);
-                top = fmaxf(top, xor16(top));
-                top = fmaxf(top, xor32(top));
-                if (g == 0) sh.m[n * 16 + c][w] = top + fr.y > kMost ? ceilf(top) - kRoom : -fr.y;
-            }
-            __syncthreads();
-            float s_r[NH];
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                const v4f mv = *reinterpret_cast<const v4f*>(sh.m[n * 16 + c]);
-                const float r = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
-                const float alpha = __builtin_amdgcn_exp2f(-sh.fr[n * 16 + c].y - r);  // 0 at a head's first entry (o is 0 then)
-#pragma unroll
-                for (int d = 0; d < 8; ++d) o[n][d] *= alpha;
-                l[n] *= alpha;
-                s_r[n] = r;
-            }
-            __syncthreads();  // every wavefront has read the old references
-            if (w == 0 && g == 0) {
-#pragma unroll
-                for (int n = 0; n < NH; ++n) sh.fr[n * 16 + c].y = -s_r[n];
-            }
-            __syncthreads();
-            store();
+            const int mine = __any(over);
+            sh.over[buf ^ 1][w] = mine;
             __syncthreads();
         }
-#pragma unroll
-        for (int n = 0; n < NH; ++n) l[n] += sum[n];
     };
 
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     if (steps > 0) {
-        turn(std::true_type{}, std::false_type{}, 1, 0);
-        for (int step = 0; step + 1 < steps; ++step) {
-            softmax(step & 1);
-            turn(std::false_type{}, std::false_type{}, step & 1, step + 1);
-        }
-        softmax((steps - 1) & 1);
-        turn(std::false_type{}, std::true_type{}, (steps - 1) & 1, steps);
+        turn(no, yes, -1);
+        for (int i = 0; i + 1 < steps; ++i) turn(yes, yes, i);
+        turn(yes, no, steps - 1);
     }
 
     // the sum over the four lane groups and the four wavefronts
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-        float x = l[n];
-        x += xor16(x);
-        x += xor32(x);
+        const float x = group_sum(l[n]);
         if (g == 0) sh.l[n * 16 + c][w] = x;
     }
     __syncthreads();
@@ -563,8 +606,7 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[hf][k], f[hf][k], -off[hf][k]));
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
+            sum = group_sum(sum);
             if (g == 0 && i < slots) {
                 const float x = row >= 0 ? sum * mean : 0.0f;
                 out[i] = h0 ? out[i] + x : x;
