@@ -78,23 +78,37 @@ __device__ __forceinline__ Entries entries_of(const AttendArgs& a, int64_t t) {
     return e;
 }
 
-// An entry's row is found in three stages, so that a kernel can keep the loads of each in flight:
-// its position, its page, its row. -1: past the end, not visible, or outside the cache.
-__device__ __forceinline__ uint32_t page_index(const AttendArgs& a, int32_t p) {
-    return a.page_size == 1 ? (uint32_t)p : __umulhi((uint32_t)p, a.page_mul) >> a.page_shift;
-}
+// An entry's row is found in three stages, so that a kernel can keep the loads of each in flight: its position, its
+// page, its row. No branches: an entry that is not there (past the end, not visible, outside the cache) reads
+// a place that is and becomes row -1. Only for queries with entries.
+template <bool LIST>
 __device__ __forceinline__ int32_t position_of(const Entries& e, int i, int end) {
-    if (i >= end) return -1;
-    return e.list ? e.list[i] : e.first + i;
+    const int32_t p = LIST ? e.list[min(i, end - 1)] : e.first + i;
+    return i < end ? p : -1;
 }
+__device__ __forceinline__ uint32_t page_index(const AttendArgs& a, uint32_t p) {
+    return __umulhi(2 * p, a.page_mul) >> a.page_shift;
+}
+template <bool PAGED>
 __device__ __forceinline__ int32_t page_of(const AttendArgs& a, const Entries& e, int32_t p) {
-    if (!e.pages || (uint32_t)p >= (uint32_t)e.n) return 0;
-    return e.pages[page_index(a, p)];
+    if (!PAGED) return 0;
+    return e.pages[page_index(a, (uint32_t)p < (uint32_t)e.n ? (uint32_t)p : 0u)];
 }
+template <bool PAGED>
 __device__ __forceinline__ int32_t row_of(const AttendArgs& a, const Entries& e, int32_t p, int32_t page) {
-    int64_t r = e.base + p;
-    if (e.pages) r = (int64_t)page * a.page_size + (p - (int32_t)page_index(a, p) * a.page_size);
-    return ((uint32_t)p < (uint32_t)e.n && page >= 0 && r >= 0 && r < a.rows) ? (int32_t)r : -1;
+    bool there = (uint32_t)p < (uint32_t)e.n;
+    uint32_t r;
+    if (PAGED) {
+        const uint32_t in_page = (uint32_t)p - page_index(a, (uint32_t)p) * (uint32_t)a.page_size;
+        const uint64_t at = (uint64_t)(uint32_t)page * (uint32_t)a.page_size + in_page;
+        there &= page >= 0 && at < (uint64_t)a.rows;
+        r = (uint32_t)at;
+    } else {
+        // the base lies in (-2^30, rows) and p in [0, 2^30): a sum below zero wraps above any row
+        r = (uint32_t)e.base + (uint32_t)p;
+        there &= r < (uint32_t)a.rows;
+    }
+    return there ? (int32_t)r : -1;
 }
 
 // One lane's share of a cache row: lane group g (of 4) holds, for j = 0 .. 3, values 128j + 32g ..
@@ -220,16 +234,16 @@ struct Shared {
     _Float16 q[NH * 16 * kQRow];       // the queries' last fragment (the registers hold 15 of 16)
 };
 
-// What a wavefront holds of the next steps: rows are found for four steps at a time (lane group g: the g-th), and
-// travel one step ahead.
+// What a wavefront holds of the next steps. Loads in flight: the rows of the next step, the page of the one after,
+// the position of the one after that.
 struct Feed {
     RowPart kv;
-    int32_t row;          // of the step whose rows kv holds
-    int32_t rows4;        // of the four steps at hand
-    int32_t pos, page;    // of the next four
+    int32_t row;             // of the step whose rows kv holds
+    int32_t pos1, page1;     // one step on
+    int32_t pos2;            // two steps on
 };
 
-template <int NH>
+template <int NH, bool LIST, bool PAGED>
 __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int splits) {
     __shared__ __align__(16) Shared<NH> sh;
     constexpr int kHeads = NH * 16;
@@ -248,20 +262,18 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     const int step0 = part * per;
     const int steps = min(per, steps_all - step0);  // may be 0 or less
     const int end = steps > 0 ? min((step0 + steps) * kTile, e.count) : 0;
-    const int i0 = (step0 + g) * kTile + w * 16 + c;  // this lane's entry of the first four steps
+    const int i0 = step0 * kTile + w * 16 + c;      // this lane's entry of the first step
 
     Feed fd;
-    const auto row_of_step = [&](int i) { return __builtin_amdgcn_ds_bpermute(((i & 3) * 16 + c) * 4, fd.rows4); };
-    {
-        const int32_t p = position_of(e, i0, end);
-        fd.pos = position_of(e, i0 + 4 * kTile, end);
-        fd.page = 0;
-        fd.rows4 = row_of(a, e, p, page_of(a, e, p));
-        fd.row = row_of_step(0);
-        if (steps > 0) {
+    if (steps > 0) {
+        const int32_t p = position_of<LIST>(e, i0, end);
+        fd.pos1 = position_of<LIST>(e, i0 + kTile, end);
+        fd.pos2 = position_of<LIST>(e, i0 + 2 * kTile, end);
+        const int32_t page = page_of<PAGED>(a, e, p);
+        fd.page1 = page_of<PAGED>(a, e, fd.pos1);
+        fd.row = row_of<PAGED>(a, e, p, page);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
-        }
+        for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
     }
     stage_query<kHeads>(a, t, h0, sh.kv[1], sh.fr);
     __syncthreads();
@@ -366,13 +378,10 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         const bool there = fd.row >= 0;
         int32_t row1 = -1;
         if constexpr (kQk) {
-            const int ahead = i + 2;
-            if ((ahead & 3) == 2) fd.page = page_of(a, e, fd.pos);
-            if ((ahead & 3) == 0) {
-                fd.rows4 = row_of(a, e, fd.pos, fd.page);
-                fd.pos = position_of(e, i0 + (ahead + 4) * kTile, end);
-            }
-            row1 = row_of_step(ahead);
+            row1 = row_of<PAGED>(a, e, fd.pos1, fd.page1);
+            fd.pos1 = fd.pos2;
+            fd.page1 = page_of<PAGED>(a, e, fd.pos2);
+            fd.pos2 = position_of<LIST>(e, i0 + (i + 4) * kTile, end);
             k = values8(fd.kv, 0, 0, g, there);
         }
         if constexpr (kPv) {
@@ -537,6 +546,7 @@ constexpr int kWeightHeads = 32;
 //   w_i = 1/H sum_h exp(s_{h,i} - lse_h).
 // The first product alone; entries are independent, so a query's entries spread over blocks freely.
 // Heads beyond 32 are further rounds over the same entries, added by the lane that wrote them.
+template <bool LIST, bool PAGED>
 __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,
                                                                 float* __restrict__ weights, int64_t w_stride,
                                                                 int splits) {
@@ -585,8 +595,8 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
         }
         for (int step = step0; step < step1; ++step) {
             const int i = step * kTile + w * 16 + c;
-            const int32_t pos = position_of(e, i, e.count);
-            const int32_t row = row_of(a, e, pos, page_of(a, e, pos));
+            const int32_t pos = position_of<LIST>(e, i, e.count);
+            const int32_t row = row_of<PAGED>(a, e, pos, page_of<PAGED>(a, e, pos));
             RowPart kv;
 #pragma unroll
             for (int j = 0; j < 4; ++j) load_chunk(a, row, g, j, kv);
@@ -651,21 +661,34 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
     return best;
 }
 
-// p / page_size for 0 <= p < 2^30 as a product: with 2^(b-1) < d <= 2^b, mul = floor(2^(31+b) / d) + 1 (below 2^32
-// for d > 1) exceeds 2^(31+b) / d by at most 1, so p * mul / 2^(31+b) exceeds p / d by at most p / 2^(31+b) < 1 / (2 d):
-// the floors agree.
+// p / page_size for 0 <= p < 2^30 as a product: with d <= 2^b < 2 d, mul = floor(2^(31+b) / d) + 1 is below 2^32 and exceeds
+// 2^(31+b) / d by at most 1, so 2 p mul / 2^(32+b) exceeds p / d by at most p / 2^(31+b) < 1 / (2 d): the floors agree.
 void set_page_division(AttendArgs& a) {
-    if (!a.pages || a.page_size == 1) return;
-    int b = 1;
+    if (!a.pages) return;
+    int b = 0;
     while (((int64_t)1 << b) < a.page_size) ++b;
     a.page_mul = (uint32_t)(((uint64_t)1 << (31 + b)) / (uint64_t)a.page_size + 1);
-    a.page_shift = b - 1;
+    a.page_shift = b;
+}
+
+// the kernel of the call's entries: listed or a range, paged or contiguous
+template <typename F>
+void by_entries(const AttendArgs& a, F&& launch) {
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (a.idx)
+        a.pages ? launch(yes, yes) : launch(yes, no);
+    else
+        a.pages ? launch(no, yes) : launch(no, no);
 }
 
 template <int NH>
 void launch_attend_as(const AttendArgs& a, int splits, hipStream_t stream) {
     const uint32_t units = (uint32_t)a.nq * splits, head_tiles = (a.heads + 16 * NH - 1) / (16 * NH);
-    hipLaunchKernelGGL(attend_kernel<NH>, dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, splits);
+    by_entries(a, [&](auto list, auto paged) {
+        hipLaunchKernelGGL((attend_kernel<NH, decltype(list)::value, decltype(paged)::value>),
+                           dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, splits);
+    });
 }
 
 }  // namespace
@@ -704,8 +727,10 @@ hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights,
     // two blocks for each compute unit, at least one step of 64 entries each
     const int64_t steps = (entries + kTile - 1) / kTile, want = (512 + a.nq - 1) / a.nq;
     const int splits = (int)(want < steps ? want : steps);
-    hipLaunchKernelGGL(attend_weights_kernel, dim3((uint32_t)a.nq * splits), dim3(256), 0, stream, a, lse, weights,
-                       w_stride, splits);
+    by_entries(a, [&](auto list, auto paged) {
+        hipLaunchKernelGGL((attend_weights_kernel<decltype(list)::value, decltype(paged)::value>),
+                           dim3((uint32_t)a.nq * splits), dim3(256), 0, stream, a, lse, weights, w_stride, splits);
+    });
     return hipGetLastError();
 }
 
