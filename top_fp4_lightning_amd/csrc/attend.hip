@@ -166,28 +166,35 @@ __device__ __forceinline__ float group_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// ROWS query rows (heads h0 .. , rows past the last head as zeros) into LDS as scaled fp16, and per head
-// the factor that turns a dot product of theirs into s2: a row per wavefront and step, 8 values per lane.
+// ROWS query rows (heads h0 .. , rows past the last head as zeros): read, a row per wavefront and step, 8 values per
+// lane; then into LDS as scaled fp16, and per head the factor that turns a dot product of theirs into s2.
 template <int ROWS>
-__device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int h0, _Float16* lds, float2* factor) {
+struct QueryRows {
+    uint4 raw[ROWS / 4];
+};
+template <int ROWS>
+__device__ __forceinline__ void load_query(const AttendArgs& a, int64_t t, int h0, QueryRows<ROWS>& q) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    constexpr int PER = ROWS / 4;
-    uint4 raw[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int h = h0 + w * PER + i, hc = h < a.heads ? h : a.heads - 1;
-        raw[i] = *reinterpret_cast<const uint4*>(a.q + (t * a.heads + hc) * kD + lane * 8);
-        if (h != hc) raw[i] = uint4{0, 0, 0, 0};
+    for (int i = 0; i < ROWS / 4; ++i) {
+        const int h = h0 + w * (ROWS / 4) + i, hc = h < a.heads ? h : a.heads - 1;
+        q.raw[i] = *reinterpret_cast<const uint4*>(a.q + (t * a.heads + hc) * kD + lane * 8);
     }
+}
+template <int ROWS>
+__device__ __forceinline__ void stage_query(const AttendArgs& a, int h0, QueryRows<ROWS>& q, _Float16* lds,
+                                            float2* factor) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t m = 0;
+    for (int i = 0; i < ROWS / 4; ++i) {
+        const int row = w * (ROWS / 4) + i;
+        const uint32_t keep = h0 + row < a.heads ? 0xffffffffu : 0u;
+        const uint32_t v[4] = {q.raw[i].x & keep, q.raw[i].y & keep, q.raw[i].z & keep, q.raw[i].w & keep};
+        us2 two = {0, 0};  // the largest magnitude of each half
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t hi = v[c] & 0x7fff0000u, lo = (v[c] << 16) & 0x7fff0000u;
-            m = max(m, max(hi, lo));
-        }
+        for (int c = 0; c < 4; ++c) two = __builtin_elementwise_max(two, __builtin_bit_cast(us2, v[c] & 0x7fff7fffu));
+        uint32_t m = max((uint32_t)two[0], (uint32_t)two[1]);
         m = max(m, dpp<0xB1>(m));   // quad_perm [1,0,3,2]
         m = max(m, dpp<0x4E>(m));   // quad_perm [2,3,0,1]
         m = max(m, dpp<0x141>(m));  // row_half_mirror
@@ -195,7 +202,7 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
         m = max16(m);
         m = max32(m);
         // 2^(14 - exponent of the largest), a power of two kept inside the normal range
-        int e = (int)(m >> 23);
+        int e = (int)(m >> 7);
         e = e < 15 ? 15 : (e > 254 ? 254 : e);
         const float mul = __uint_as_float((uint32_t)(127 + 141 - e) << 23);
         h8 o;
@@ -204,12 +211,10 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int64_t t, int 
             o[2 * c] = (_Float16)(__uint_as_float(v[c] << 16) * mul);
             o[2 * c + 1] = (_Float16)(__uint_as_float(v[c] & 0xffff0000u) * mul);
         }
-        *reinterpret_cast<h8*>(lds + (w * PER + i) * kRow + lane * 8) = o;
-        if (lane == 0) {
-            // (above zero or below it: a masked entry's product is an infinity of the other sign)
-            const float f = a.scale * kLog2e * __uint_as_float((uint32_t)(e - 14) << 23);
-            factor[w * PER + i] = float2{fabsf(f) < 0x1p-126f ? 0x1p-126f : f, -kNone};
-        }
+        *reinterpret_cast<h8*>(lds + row * kRow + lane * 8) = o;
+        // (above zero or below it: a masked entry's product is an infinity of the other sign)
+        const float f = a.scale * kLog2e * __uint_as_float((uint32_t)(e - 14) << 23);
+        factor[row] = float2{fabsf(f) < 0x1p-126f ? 0x1p-126f : f, -kNone};
     }
 }
 
@@ -264,6 +269,8 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     const int end = steps > 0 ? min((step0 + steps) * kTile, e.count) : 0;
     const int i0 = step0 * kTile + w * 16 + c;      // this lane's entry of the first step
 
+    QueryRows<kHeads> qr;
+    load_query<kHeads>(a, t, h0, qr);
     Feed fd;
     if (steps > 0) {
         const int32_t p = position_of<LIST>(e, i0, end);
@@ -275,7 +282,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
     }
-    stage_query<kHeads>(a, t, h0, sh.kv[1], sh.fr);
+    stage_query<kHeads>(a, h0, qr, sh.kv[1], sh.fr);
     __syncthreads();
     h8 q[NH][15];
 #pragma unroll
@@ -316,35 +323,41 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     // R is set kRoom below the largest logit at hand. Where one comes to lie more than kMost above R (seldom after the
     // first step), the four wavefronts agree on a new R and bring outputs and sums to it (powers of two, exact), and
     // the step's probabilities are formed again.
-    const auto rebase = [&](int step) {
+    const auto new_reference = [&](const float2 (&fr)[NH], float (&r)[NH]) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const float2 fr = sh.fr[n * 16 + c];
             float top = ninf();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][i] * fr.x);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[n][i] * fr[n].x);
             top = group_max(top);
-            if (g == 0) sh.m[n * 16 + c][w] = top + fr.y > kMost ? ceilf(top) - kRoom : -fr.y;
+            if (g == 0) sh.m[n * 16 + c][w] = top + fr[n].y > kMost ? ceilf(top) - kRoom : -fr[n].y;
         }
         __syncthreads();
-        float r[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             const v4f mv = *reinterpret_cast<const v4f*>(sh.m[n * 16 + c]);
             r[n] = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
-            const float alpha = __builtin_amdgcn_exp2f(-sh.fr[n * 16 + c].y - r[n]);  // 0 at a head's first entry (o is 0 then)
+        }
+    };
+    const auto rebase = [&](int step) {
+        float2 fr[NH];
+        float r[NH];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
+        new_reference(fr, r);
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const float alpha = __builtin_amdgcn_exp2f(-fr[n].y - r[n]);  // 0 at a head's first entry (o is 0 then)
 #pragma unroll
             for (int d = 0; d < 8; ++d) o[n][d] *= alpha;
             l[n] *= alpha;
         }
-        __syncthreads();  // every wavefront has read the old references
-        if (w == 0 && g == 0) {
+        if (w == 0 && g == 0) {  // (every wavefront has read the old ones)
 #pragma unroll
             for (int n = 0; n < NH; ++n) sh.fr[n * 16 + c].y = -r[n];
         }
-        __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NH; ++n) probabilities(n, sh.fr[n * 16 + c], step);
+        for (int n = 0; n < NH; ++n) probabilities(n, float2{fr[n].x, -r[n]}, step);
         __syncthreads();
     };
 
@@ -449,6 +462,16 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             }
             fd.row = row1;
             bool over = false;
+            if constexpr (!kPv) {
+                // the first step sets R
+                float r[NH];
+                new_reference(fr, r);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    fr[n].y = -r[n];
+                    if (w == 0 && g == 0) sh.fr[n * 16 + c].y = -r[n];
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
                 if constexpr (kPv) {
@@ -486,14 +509,15 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         if (g == 0) sh.l[n * 16 + c][w] = x;
     }
     __syncthreads();
+    _Float16* rows = sh.kv[0];  // (bf16) the block's output rows, to be written whole
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
         const int hl = n * 16 + c;
         const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
         const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]);
         const int h = h0 + hl;
-        if (h >= a.heads) continue;
         if (splits > 1) {
+            if (h >= a.heads) continue;
             const int64_t r = (int64_t)unit * a.heads + h;
             float* po = a.part_o + r * kD + w * 128 + g * 4;
 #pragma unroll
@@ -504,15 +528,24 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             }
         } else {
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            uint16_t* po = a.out + (t * a.heads + h) * kD + w * 128 + g * 4;
+            _Float16* po = rows + hl * kRow + w * 128 + g * 4;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 const v4f y = o[n][d] * inv;
                 *reinterpret_cast<uint2*>(po + d * 16) = uint2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
             }
-            if (a.lse && w == 0 && g == 0)
+            if (a.lse && h < a.heads && w == 0 && g == 0)
                 a.lse[t * a.heads + h] = L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) - sh.fr[hl].y) * kLn2;
         }
+    }
+    if (splits > 1) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NH * 4; ++i) {
+        const int hl = w * NH * 4 + i;
+        if (h0 + hl < a.heads)
+            *reinterpret_cast<uint4*>(a.out + (t * a.heads + h0 + hl) * kD + lane * 8) =
+                *reinterpret_cast<const uint4*>(rows + hl * kRow + lane * 8);
     }
 }
 
@@ -574,7 +607,9 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
 
     for (int h0 = 0; h0 < a.heads; h0 += kWeightHeads) {
         __syncthreads();
-        stage_query<kWeightHeads>(a, t, h0, s_q, s_factor);
+        QueryRows<kWeightHeads> qr;
+        load_query<kWeightHeads>(a, t, h0, qr);
+        stage_query<kWeightHeads>(a, h0, qr, s_q, s_factor);
         __syncthreads();
         h8 q[2][16];
         float f[2][4], off[2][4];
