@@ -139,7 +139,8 @@ def _rows_ptr(t: torch.Tensor | None) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object in between (2.7 us of a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -307,23 +308,37 @@ def idx_topk_pool(scores, n_vis, max_n: int, pool_blocks, pool_count, max_blocks
     return out_idx, out_val
 
 
-def _here(**tensors) -> None:
-    """The arguments given lie on the current device (the library launches there)."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"fp4idx tensors must live on the GPU: {name} is on {t.device}")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must live on the current GPU (cuda:{dev}), got {t.device}")
+def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
+    """Address of a contiguous argument of this type and shape (its place is checked by _same_gpu)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _rows_arg(t: torch.Tensor, dtype: torch.dtype, rows: int, width: int, name: str) -> tuple:
+    """(address, row stride) of a 2-D argument of at least `width` columns, each row contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < width:
+        raise ValueError(f"{name} must be [{rows}, >= {width}], got {tuple(t.shape)}")
+    stride, one = t.stride()
+    if one != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), stride if rows > 1 else max(stride, t.shape[1])
+
+
+def _same_gpu(*tensors) -> None:
+    """The arguments lie together on the current device (the library launches there)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError(f"fp4idx tensors must live on one GPU, got {tensors[0].device} and {t.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"fp4idx tensors must live on the current GPU, got {tensors[0].device}")
 
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -348,71 +363,62 @@ def idx_rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, offset: int
     """Rotate the values offset .. offset + 2 * len(freq) - 1 (default: the last ones) of rows x [tokens, heads,
     dim] (bf16 or fp32, consecutive values, any strides) by pos [tokens] (int64) * freq. out may be x itself;
     inverse=True is the gradient."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {dtype}")
     if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
         raise ValueError("x must be [tokens, heads, dim] with consecutive values")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype is not dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    elif out.shape != x.shape or (out.shape[2] > 1 and out.stride(2) != 1):
+        raise ValueError("out must have x's shape and consecutive values")
     tokens, heads, dim = x.shape
-    _need(pos, torch.int64, "pos")
-    _need(freq, torch.float64, "freq")
-    _need(out, x.dtype, "out")
-    _shape(out, (tokens, heads, dim), "out")
-    _shape(pos, (tokens,), "pos")
-    if out.stride(2) != 1 and dim > 1:
-        raise ValueError("out must have consecutive values")
-    _here(x=x, pos=pos, freq=freq, out=out)
-    rot = 2 * freq.numel()
-    _call(lib.idx_rope, x.data_ptr(), 0 if x.dtype == torch.bfloat16 else 1, tokens, heads, dim, x.stride(0),
-          x.stride(1), _ptr(pos), _ptr(freq), rot, dim - rot if offset is None else offset, ROPE_LAYOUTS[layout],
-          mscale, int(inverse), out.data_ptr(), out.stride(0), out.stride(1), _stream(stream))
+    half = freq.numel()
+    pos_ptr = _arg(pos, torch.int64, (tokens,), "pos")
+    freq_ptr = _arg(freq, torch.float64, (half,), "freq")
+    _same_gpu(x, pos, freq, out)
+    x_token, x_head, _ = x.stride()
+    out_token, out_head, _ = out.stride()
+    _call(lib.idx_rope, x.data_ptr(), 0 if dtype is torch.bfloat16 else 1, tokens, heads, dim, x_token, x_head, pos_ptr,
+          freq_ptr, 2 * half, dim - 2 * half if offset is None else offset, ROPE_LAYOUTS[layout], mscale, int(inverse),
+          out.data_ptr(), out_token, out_head, _stream(stream))
     return out
 
 
-def _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx, extra) -> tuple:
-    """Checks shared by the attention calls; the arguments from q to n_vis, and those of the list."""
-    _need(q, torch.bfloat16, "q")
-    _need(codes, torch.uint8, "codes")
-    _need(scales, torch.uint8, "scales")
-    _need(n_vis, torch.int32, "n_vis")
+def _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx) -> tuple:
+    """Checks shared by the attention calls: the arguments from q to n_vis, and those of the list."""
     if q.dim() != 3 or q.shape[2] != MKV_DIM:
         raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(q.shape)}")
-    nq, heads = q.shape[0], q.shape[1]
+    nq, heads, _ = q.shape
     rows = codes.numel() // (MKV_DIM // 2)
     if codes.numel() != rows * (MKV_DIM // 2) or scales.numel() != rows * (MKV_DIM // 16):
         raise ValueError("codes and scales must hold 256 and 32 bytes for each cache row")
-    _shape(n_vis, (nq,), "n_vis")
-    nseq = pages_stride = 0
+    q_ptr = _arg(q, torch.bfloat16, q.shape, "q")
+    codes_ptr = _arg(codes, torch.uint8, codes.shape, "codes")
+    scales_ptr = _arg(scales, torch.uint8, scales.shape, "scales")
+    nv_ptr = _arg(n_vis, torch.int32, (nq,), "n_vis")
+    base_ptr = pages_ptr = seq_ptr = idx_ptr = None
+    pages_stride = nseq = idx_stride = k = 0
     if kv_base is not None:
-        _need(kv_base, torch.int64, "kv_base")
-        _shape(kv_base, (nq,), "kv_base")
+        base_ptr = _arg(kv_base, torch.int64, (nq,), "kv_base")
     if pages is not None:
-        _need(pages, torch.int32, "pages")
-        pages_ptr = _rows_ptr(pages) or _ptr(n_vis)  # no column: a table all the same, never read
         nseq = pages.shape[0]
+        pages_ptr, pages_stride = _rows_arg(pages, torch.int32, nseq, 0, "pages")
         if pages.shape[1] * page_size < max_n:
             raise ValueError(f"pages must cover max_n={max_n} positions: {pages.shape[1]} pages of {page_size}")
-        pages_stride = pages.stride(0) if nseq > 1 else max(pages.shape[1], pages.stride(0))
-    else:
-        pages_ptr = None
+        pages_ptr = pages_ptr or nv_ptr  # no column: a table all the same, never read
     if seq is not None:
-        _need(seq, torch.int32, "seq")
-        _shape(seq, (nq,), "seq")
-    k = idx_stride = 0
-    idx_ptr = None
+        seq_ptr = _arg(seq, torch.int32, (nq,), "seq")
     if idx is not None:
-        _need(idx, torch.int32, "idx")
-        idx_ptr = _rows_ptr(idx) or _ptr(n_vis)  # no slot: a list all the same, never read
-        if idx.shape[0] != nq:
-            raise ValueError(f"idx must have {nq} rows, got {idx.shape[0]}")
+        idx_ptr, idx_stride = _rows_arg(idx, torch.int32, nq, 0, "idx")
+        idx_ptr = idx_ptr or nv_ptr  # no slot: a list all the same, never read
         k = idx.shape[1]
-        idx_stride = idx.stride(0) if nq > 1 else max(k, idx.stride(0))
-    _here(q=q, codes=codes, scales=scales, n_vis=n_vis, kv_base=kv_base, pages=pages, seq=seq, idx=idx, **extra)
-    return ((_ptr(q), nq, heads, _ptr(codes), _ptr(scales), rows, _ptr(kv_base), pages_ptr, pages_stride, nseq,
-             page_size, _ptr(seq), _ptr(n_vis)), (idx_ptr, idx_stride, k))
+    return ((q_ptr, nq, heads, codes_ptr, scales_ptr, rows, base_ptr, pages_ptr, pages_stride, nseq, page_size, seq_ptr,
+             nv_ptr), (idx_ptr, idx_stride, k))
 
 
 def idx_attend(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=None, window: int = 0, kv_base=None,
@@ -420,15 +426,12 @@ def idx_attend(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=N
     """Core attention of q [nq, heads, 512] over the FP4 main-KV cache: all visible positions (or the last
     `window`), or those of idx [nq, k]. Rows lie at kv_base [nq] + position, or in pages [nseq, ...] of
     page_size positions (seq [nq] names each query's page row). ws: workspace(IDX_OP_ATTEND, nq, entries, heads)."""
-    _need(out, torch.bfloat16, "out")
-    _shape(out, tuple(q.shape), "out")
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        _shape(lse, tuple(q.shape[:2]), "lse")
-    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx,
-                               dict(out=out, lse=lse, ws=ws))
-    _call(lib.idx_attend, *where, max_n, window, *lst, scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-          _stream(stream))
+    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx)
+    out_ptr = _arg(out, torch.bfloat16, q.shape, "out")
+    lse_ptr = None if lse is None else _arg(lse, torch.float32, q.shape[:2], "lse")
+    ws_ptr = _arg(ws, torch.uint8, ws.shape, "ws")
+    _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, idx, out, lse, ws)
+    _call(lib.idx_attend, *where, max_n, window, *lst, scale, out_ptr, lse_ptr, ws_ptr, ws.numel(), _stream(stream))
     return out, lse
 
 
@@ -436,50 +439,38 @@ def idx_attend_weights(q, codes, scales, n_vis, max_n: int, scale: float, lse, w
                        page_size: int = 0, seq=None, idx=None, stream=None):
     """The attention's probability of each entry (idx slot, or visible position), mean over the heads, from the
     saved lse [nq, heads], into weights [nq, >= k] (or [nq, >= max_n])."""
-    _need(lse, torch.float32, "lse")
-    _need(weights, torch.float32, "weights")
-    _shape(lse, tuple(q.shape[:2]), "lse")
-    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx,
-                               dict(lse=lse, weights=weights))
-    if weights.dim() != 2 or weights.shape[0] != q.shape[0] or weights.shape[1] < (max_n if idx is None else lst[2]):
-        raise ValueError("weights must be [nq, >= k] with idx, [nq, >= max_n] without")
-    _call(lib.idx_attend_weights, *where, max_n, *lst, scale, _ptr(lse), _rows_ptr(weights),
-          weights.stride(0) if q.shape[0] > 1 else max(weights.shape[1], weights.stride(0)), _stream(stream))
+    where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx)
+    lse_ptr = _arg(lse, torch.float32, q.shape[:2], "lse")
+    w_ptr, w_stride = _rows_arg(weights, torch.float32, q.shape[0], max_n if idx is None else lst[2], "weights")
+    _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, idx, lse, weights)
+    _call(lib.idx_attend_weights, *where, max_n, *lst, scale, lse_ptr, w_ptr, w_stride, _stream(stream))
     return weights
 
 
-def _distill_rows(scores, n_vis, t_idx, t_logit, per_row: dict, extra: dict) -> tuple:
-    _need(scores, torch.float32, "scores")
-    _need(n_vis, torch.int32, "n_vis")
-    _need(t_idx, torch.int32, "t_idx")
-    _need(t_logit, torch.float32, "t_logit")
+def _distill_rows(scores, n_vis, max_n, t_idx, t_logit) -> tuple:
+    """Checks shared by the two directions: the arguments from scores to k."""
     nq = n_vis.shape[0]
-    _shape(t_logit, tuple(t_idx.shape), "t_logit")
-    if scores.dim() != 2 or scores.shape[0] != nq or t_idx.dim() != 2 or t_idx.shape[0] != nq:
-        raise ValueError("scores and t_idx must have a row for each of n_vis")
-    if nq > 1 and t_idx.stride(0) != t_logit.stride(0):
-        raise ValueError("t_idx and t_logit must have the same row stride")
-    for name, t in per_row.items():
-        _need(t, torch.float32, name)
-        _shape(t, (nq,), name)
-    _here(scores=scores, n_vis=n_vis, t_idx=t_idx, t_logit=t_logit, **per_row, **extra)
+    s_ptr, s_stride = _rows_arg(scores, torch.float32, nq, max_n, "scores")
+    nv_ptr = _arg(n_vis, torch.int32, (nq,), "n_vis")
+    i_ptr, i_stride = _rows_arg(t_idx, torch.int32, nq, 0, "t_idx")
+    if t_logit.shape != t_idx.shape:
+        raise ValueError(f"t_logit must have t_idx's shape {tuple(t_idx.shape)}, got {tuple(t_logit.shape)}")
+    l_ptr, l_stride = _rows_arg(t_logit, torch.float32, nq, 0, "t_logit")
     k = t_idx.shape[1]
-    return nq, (_rows_ptr(t_idx), _rows_ptr(t_logit), t_idx.stride(0) if nq > 1 else max(k, t_idx.stride(0)), k)
-
-
-def _width(t: torch.Tensor, max_n: int, name: str) -> int:
-    """The row stride of a 2-D argument that holds max_n values per row."""
-    if t.shape[1] < max_n:
-        raise ValueError(f"{name} must have at least max_n={max_n} columns, got {t.shape[1]}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    if nq > 1 and i_stride != l_stride:
+        raise ValueError("t_idx and t_logit must have the same row stride")
+    return s_ptr, s_stride, nv_ptr, nq, max_n, i_ptr, l_ptr, i_stride if nq > 1 else k, k
 
 
 def idx_distill(scores, n_vis, max_n: int, t_idx, t_logit, loss, lse, t_lse, ws, inv_temp: float = 1.0, stream=None):
     """KL divergence of score rows [nq, >= max_n] from a teacher's top logits (t_idx, t_logit [nq, k]): writes
     loss, lse and t_lse [nq]. ws: workspace(IDX_OP_DISTILL, nq, max_n, 1)."""
-    nq, teacher = _distill_rows(scores, n_vis, t_idx, t_logit, dict(loss=loss, lse=lse, t_lse=t_lse), dict(ws=ws))
-    _call(lib.idx_distill, _rows_ptr(scores), _width(scores, max_n, "scores"), _ptr(n_vis), nq, max_n, *teacher,
-          inv_temp, _ptr(loss), _ptr(lse), _ptr(t_lse), _ptr(ws), ws.numel(), _stream(stream))
+    rows = _distill_rows(scores, n_vis, max_n, t_idx, t_logit)
+    each = (rows[3],)
+    outs = (_arg(loss, torch.float32, each, "loss"), _arg(lse, torch.float32, each, "lse"),
+            _arg(t_lse, torch.float32, each, "t_lse"), _arg(ws, torch.uint8, ws.shape, "ws"))
+    _same_gpu(scores, n_vis, t_idx, t_logit, loss, lse, t_lse, ws)
+    _call(lib.idx_distill, *rows, inv_temp, *outs, ws.numel(), _stream(stream))
     return loss
 
 
@@ -487,12 +478,11 @@ def idx_distill_bwd(scores, n_vis, max_n: int, t_idx, t_logit, lse, t_lse, dloss
                     stream=None):
     """Gradient of idx_distill with dloss [nq], from its lse and t_lse, into dscores [nq, >= max_n] (visible
     positions only; may be scores itself)."""
-    nq, teacher = _distill_rows(scores, n_vis, t_idx, t_logit, dict(lse=lse, t_lse=t_lse, dloss=dloss),
-                                dict(dscores=dscores))
-    _need(dscores, torch.float32, "dscores")
-    if dscores.dim() != 2 or dscores.shape[0] != nq:
-        raise ValueError("dscores must have a row for each of n_vis")
-    _call(lib.idx_distill_bwd, _rows_ptr(scores), _width(scores, max_n, "scores"), _ptr(n_vis), nq, max_n, *teacher,
-          inv_temp, _ptr(lse), _ptr(t_lse), _ptr(dloss), _rows_ptr(dscores), _width(dscores, max_n, "dscores"),
-          _stream(stream))
+    rows = _distill_rows(scores, n_vis, max_n, t_idx, t_logit)
+    each = (rows[3],)
+    ins = (_arg(lse, torch.float32, each, "lse"), _arg(t_lse, torch.float32, each, "t_lse"),
+           _arg(dloss, torch.float32, each, "dloss"))
+    d_ptr, d_stride = _rows_arg(dscores, torch.float32, rows[3], max_n, "dscores")
+    _same_gpu(scores, n_vis, t_idx, t_logit, lse, t_lse, dloss, dscores)
+    _call(lib.idx_distill_bwd, *rows, inv_temp, *ins, d_ptr, d_stride, _stream(stream))
     return dscores

@@ -573,18 +573,19 @@ __global__ __launch_bounds__(128) void attend_join_kernel(const AttendArgs a, in
         a.lse[blockIdx.x] = L == 0.0f ? ninf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
-constexpr int kWeightHeads = 32;
-
 // The attention's probability of every entry, mean over the heads, from the saved lse:
 //   w_i = 1/H sum_h exp(s_{h,i} - lse_h).
-// The first product alone; entries are independent, so a query's entries spread over blocks freely.
-// Heads beyond 32 are further rounds over the same entries, added by the lane that wrote them.
-template <bool LIST, bool PAGED>
-__global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,
+// The first product alone, with heads as rows: a lane's column is one entry, whose terms it adds up over the heads.
+// Each wavefront takes 16 entries per step by itself (no barrier); the exponentials of a step run under the matrix
+// instructions of the next. Heads beyond the block's 16 NH are further rounds over the same entries, added by the lane
+// that wrote them.
+template <int NH, bool LIST, bool PAGED>
+__global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,
                                                                 float* __restrict__ weights, int64_t w_stride,
                                                                 int splits) {
-    __shared__ __align__(16) _Float16 s_q[kWeightHeads * kRow];
-    __shared__ float2 s_factor[kWeightHeads];
+    constexpr int kHeads = 16 * NH;
+    __shared__ __align__(16) _Float16 s_q[kHeads * kRow];
+    __shared__ float2 s_factor[kHeads];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int g = lane >> 4, c = lane & 15;
@@ -592,71 +593,105 @@ __global__ __launch_bounds__(256, 2) void attend_weights_kernel(const AttendArgs
     const int part = (int)(blockIdx.x % splits);
     const Entries e = entries_of(a, t);
     // a list's slots are all written; of a range, the visible positions
-    const int slots = a.idx ? a.k : e.visible;
+    const int slots = LIST ? a.k : e.visible;
     const int steps_all = (slots + kTile - 1) / kTile;
     const int per = (steps_all + splits - 1) / splits;
     const int step0 = part * per;
-    const int step1 = min(step0 + per, steps_all);
-    if (step0 >= step1) return;
+    const int steps = min(per, steps_all - step0);
+    if (steps <= 0) return;
     float* out = weights + t * w_stride;
+    const int end = min((step0 + steps) * kTile, slots);
     if (e.count == 0) {  // no row is read (the cache may hold none)
-        for (int i = step0 * kTile + (int)threadIdx.x; i < min(step1 * kTile, slots); i += 256) out[i] = 0.0f;
+        for (int i = step0 * kTile + (int)threadIdx.x; i < end; i += 256) out[i] = 0.0f;
         return;
     }
+    const int i0 = step0 * kTile + w * 16 + c;  // this lane's entry of the first step
     const float mean = 1.0f / (float)a.heads;
 
-    for (int h0 = 0; h0 < a.heads; h0 += kWeightHeads) {
-        __syncthreads();
-        QueryRows<kWeightHeads> qr;
-        load_query<kWeightHeads>(a, t, h0, qr);
-        stage_query<kWeightHeads>(a, h0, qr, s_q, s_factor);
-        __syncthreads();
-        h8 q[2][16];
-        float f[2][4], off[2][4];
+    for (int h0 = 0; h0 < a.heads; h0 += kHeads) {
+        QueryRows<kHeads> qr;
+        load_query<kHeads>(a, t, h0, qr);
+        Feed fd;
+        {
+            const int32_t p = position_of<LIST>(e, i0, end);
+            fd.pos1 = position_of<LIST>(e, i0 + kTile, end);
+            fd.pos2 = position_of<LIST>(e, i0 + 2 * kTile, end);
+            const int32_t page = page_of<PAGED>(a, e, p);
+            fd.page1 = page_of<PAGED>(a, e, fd.pos1);
+            fd.row = row_of<PAGED>(a, e, p, page);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+            for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
+        }
+        if (h0) __syncthreads();
+        stage_query<kHeads>(a, h0, qr, s_q, s_factor);
+        __syncthreads();
+        h8 q[NH][16];
+        float f[NH][4], off[NH][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int hl = hf * 16 + g * 4 + i;
-                f[hf][i] = s_factor[hl].x;
-                // a head that is not there, or that saw nothing, adds nothing
-                float y = h0 + hl < a.heads ? lse[t * a.heads + h0 + hl] : ninf();
-                off[hf][i] = y == ninf() ? __builtin_inff() : y * kLog2e;
-            }
+        for (int n = 0; n < NH; ++n) {
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-                q[hf][x] =
-                    *reinterpret_cast<const h8*>(s_q + (hf * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
-        }
-        for (int step = step0; step < step1; ++step) {
-            const int i = step * kTile + w * 16 + c;
-            const int32_t pos = position_of<LIST>(e, i, e.count);
-            const int32_t row = row_of<PAGED>(a, e, pos, page_of<PAGED>(a, e, pos));
-            RowPart kv;
+                q[n][x] = *reinterpret_cast<const h8*>(s_q + (n * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_chunk(a, row, g, j, kv);
-            v4f s[2] = {};
+            for (int x = 0; x < 16; ++x) asm volatile("" : "+a"(q[n][x]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const h8 v = values8(kv, j, u, g, row >= 0);
-                    s[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[0][j * 4 + u], v, s[0], 0, 0, 0);
-                    s[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[1][j * 4 + u], v, s[1], 0, 0, 0);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int hl = n * 16 + g * 4 + i, h = min(h0 + hl, a.heads - 1);
+                f[n][i] = s_factor[hl].x;
+                // a head that is not there, or that saw nothing, adds nothing
+                const float y = h0 + hl < a.heads ? lse[t * a.heads + h] : ninf();
+                off[n][i] = y == ninf() ? ninf() : -y * kLog2e;
             }
-            float sum = 0.0f;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[hf][k], f[hf][k], -off[hf][k]));
+        }
+        v4f s[NH], last[NH];  // products of the step at hand and of the one before, whose row was last_row
+        int32_t last_row;
+        const auto store = [&](int i, float sum) {
             sum = group_sum(sum);
-            if (g == 0 && i < slots) {
-                const float x = row >= 0 ? sum * mean : 0.0f;
+            if (g == 0 && i < end) {
+                const float x = last_row >= 0 ? sum * mean : 0.0f;
                 out[i] = h0 ? out[i] + x : x;
             }
-        }
+        };
+        const auto turn = [&](auto first, int step) {
+            constexpr bool kFirst = decltype(first)::value;
+            const bool there = fd.row >= 0;
+            const int32_t row1 = row_of<PAGED>(a, e, fd.pos1, fd.page1);
+            fd.pos1 = fd.pos2;
+            fd.page1 = page_of<PAGED>(a, e, fd.pos2);
+            fd.pos2 = position_of<LIST>(e, i0 + (step + 3) * kTile, end);
+            float sum = 0.0f;
+            h8 k = values8(fd.kv, 0, 0, g, there);
+#pragma unroll
+            for (int n = 0; n < NH; ++n) s[n] = v4f{};
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const h8 kx = k;
+                if (x < 15) k = values8(fd.kv, (x + 1) >> 2, (x + 1) & 3, g, there);
+                if ((x & 3) == 3) load_chunk(a, row1, g, x >> 2, fd.kv);
+                if (!kFirst && x < 4 * NH)
+                    sum += __builtin_amdgcn_exp2f(__builtin_fmaf(last[x >> 2][x & 3], f[x >> 2][x & 3], off[x >> 2][x & 3]));
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[n][x], kx, s[n], 0, 0, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (!kFirst) store(i0 + (step - 1) * kTile, sum);
+#pragma unroll
+            for (int n = 0; n < NH; ++n) last[n] = s[n];
+            last_row = fd.row;
+            fd.row = row1;
+        };
+        turn(std::true_type{}, 0);
+        for (int step = 1; step < steps; ++step) turn(std::false_type{}, step);
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(last[n][i], f[n][i], off[n][i]));
+        store(i0 + (steps - 1) * kTile, sum);
     }
 }
 
@@ -759,12 +794,23 @@ hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights,
     const int64_t entries = a.idx ? a.k : a.max_n;
     if (entries == 0) return hipSuccess;
     set_page_division(a);
-    // two blocks for each compute unit, at least one step of 64 entries each
-    const int64_t steps = (entries + kTile - 1) / kTile, want = (512 + a.nq - 1) / a.nq;
+    // a block for each of the 256 compute units, four times over where a query's entries are many; at least one step of
+    // 64 entries each
+    const int64_t steps = (entries + kTile - 1) / kTile;
+    const int64_t want = steps >= 32 ? (1024 + a.nq - 1) / a.nq : (256 + a.nq - 1) / a.nq;
     const int splits = (int)(want < steps ? want : steps);
     by_entries(a, [&](auto list, auto paged) {
-        hipLaunchKernelGGL((attend_weights_kernel<decltype(list)::value, decltype(paged)::value>),
-                           dim3((uint32_t)a.nq * splits), dim3(256), 0, stream, a, lse, weights, w_stride, splits);
+        constexpr bool L = decltype(list)::value, P = decltype(paged)::value;
+        const dim3 grid((uint32_t)a.nq * splits);
+        if (a.heads > 32)
+            hipLaunchKernelGGL((attend_weights_kernel<4, L, P>), grid, dim3(256), 0, stream, a, lse, weights, w_stride,
+                               splits);
+        else if (a.heads > 16)
+            hipLaunchKernelGGL((attend_weights_kernel<2, L, P>), grid, dim3(256), 0, stream, a, lse, weights, w_stride,
+                               splits);
+        else
+            hipLaunchKernelGGL((attend_weights_kernel<1, L, P>), grid, dim3(256), 0, stream, a, lse, weights, w_stride,
+                               splits);
     });
     return hipGetLastError();
 }
