@@ -26,6 +26,10 @@ Prefill (a chunk of queries sharing one key range, causal): idx_score_full write
 for every query; idx_top_blocks keeps the 512 best blocks per query (a top-512 key's block is among
 them); idx_score_pool_gather re-scores those 4096 keys; idx_topk takes the final 512.
 
+Core attention (the consumer of a layer's selection): CoreAttention keeps the FP4 main-KV cache in pages,
+rotates and quantises new rows into them, and attends over the selected positions. IndexerDistill trains a
+layer's indexer towards it, on the score rows of the training form.
+
 All buffers are allocated once in the plan objects, so a step allocates nothing and can be
 captured in a HIP graph.
 """
@@ -36,8 +40,10 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (BLOCK, IDX_OP_BUILD_POOL, IDX_OP_TOPK, Recorded, idx_build_pool, idx_mask_pool, idx_quantize_q,
-               idx_score_full, idx_score_pool_gather, idx_top_blocks, idx_topk, idx_topk_pool, record, workspace)
+from . import (BLOCK, IDX_OP_ATTEND, IDX_OP_BUILD_POOL, IDX_OP_DISTILL, IDX_OP_TOPK, MKV_DIM, Recorded, idx_attend,
+               idx_attend_weights, idx_build_pool, idx_distill, idx_distill_bwd, idx_mask_pool, idx_quantize_kv,
+               idx_quantize_q, idx_rope, idx_score_full, idx_score_pool_gather, idx_top_blocks, idx_topk, idx_topk_pool,
+               record, rope_freqs, workspace)
 
 
 @dataclass
@@ -299,8 +305,6 @@ class MainKVGather:
     idx_quantize_kv from the supplied bf16 rows); the rest of the cache stays zero."""
 
     def __init__(self, nseq: int, n: int, selections: list, rows_for, device="cuda", chunk: int = 1 << 16):
-        from . import MKV_DIM, idx_quantize_kv
-
         self.nseq, self.n = nseq, n
         total = nseq * n
         self.codes = torch.zeros(total, MKV_DIM // 2, dtype=torch.uint8, device=device)
@@ -327,3 +331,89 @@ class MainKVGather:
 
         return idx_gather_kv(self.codes, self.scales, self.kv_base, self.n_vis, self.sel[i], out=self.out[i],
                              stream=stream)
+
+
+class CoreAttention:
+    """Core attention over a layer's selection: the FP4 main-KV cache of `nseq` sequences of up to `n` positions in
+    pages of `page_size`, given out as the sequences grow, and the buffers of a step of `nq` queries. The last `rot`
+    values of every query and row carry the rotary position; rows are rotated before they are quantised (the page on
+    the main KV quantises after the rotation). scale defaults to 512 ** -0.5; the other arguments of rope_freqs
+    stretch the context."""
+
+    def __init__(self, nseq: int, n: int, nq: int, heads: int = 64, k: int = 512, page_size: int = 64, rot: int = 64,
+                 scale: float | None = None, layout: str = "interleaved", device="cuda", **freqs):
+        per = (n + page_size - 1) // page_size
+        self.n, self.nq, self.k, self.page_size, self.layout = n, nq, k, page_size, layout
+        self.scale = MKV_DIM ** -0.5 if scale is None else scale
+        self.freq, self.mscale = rope_freqs(rot, device=device, **freqs)
+        self.codes = torch.zeros(nseq * per * page_size, MKV_DIM // 2, dtype=torch.uint8, device=device)
+        self.scales = torch.zeros(nseq * per * page_size, MKV_DIM // 16, dtype=torch.uint8, device=device)
+        self.pages = torch.full((nseq, per), -1, dtype=torch.int32, device=device)
+        self.given = [0] * nseq  # pages of each sequence
+        self.used = 0
+        self.q = torch.empty(nq, heads, MKV_DIM, dtype=torch.bfloat16, device=device)
+        self.out = torch.empty_like(self.q)
+        self.lse = torch.empty(nq, heads, dtype=torch.float32, device=device)
+        self.weights = torch.empty(nq, k, dtype=torch.float32, device=device)
+        self.ws = workspace(IDX_OP_ATTEND, nq, k, heads, device=device)
+
+    def write(self, b: int, first: int, x: torch.Tensor) -> None:
+        """Rows x [m, 512] (bf16, not rotated) of sequence b's positions first .. first + m - 1."""
+        m = x.shape[0]
+        if first < 0 or first + m > self.n:
+            raise ValueError(f"positions {first} .. {first + m - 1} lie outside the sequence's {self.n}")
+        need = (first + m + self.page_size - 1) // self.page_size
+        if need > self.given[b]:
+            new = torch.arange(self.used, self.used + need - self.given[b], dtype=torch.int32)
+            self.pages[b, self.given[b]:need] = new.to(self.pages.device)
+            self.used += need - self.given[b]
+            self.given[b] = need
+        pos = torch.arange(first, first + m, device=x.device)
+        y = idx_rope(x.view(m, 1, MKV_DIM), pos, self.freq, layout=self.layout, mscale=self.mscale)
+        codes, scales = idx_quantize_kv(y.view(m, MKV_DIM))
+        rows = self.pages[b].long()[pos // self.page_size] * self.page_size + pos % self.page_size
+        self.codes.index_copy_(0, rows, codes)
+        self.scales.index_copy_(0, rows, scales)
+
+    def run(self, q, pos, seq, n_vis, idx, stream=None):
+        """q [nq, heads, 512] (bf16, not rotated) at positions pos [nq] (int64) of sequences seq [nq], over the
+        selected positions idx [nq, k] below n_vis [nq] -> out, lse."""
+        idx_rope(q, pos, self.freq, layout=self.layout, mscale=self.mscale, out=self.q, stream=stream)
+        return idx_attend(self.q, self.codes, self.scales, n_vis, self.n, self.scale, self.out, self.ws, lse=self.lse,
+                          pages=self.pages, page_size=self.page_size, seq=seq, idx=idx, stream=stream)
+
+    def selection_weights(self, seq, n_vis, idx, stream=None):
+        """The probabilities [nq, k] that the last run gave its selection, mean over the heads."""
+        return idx_attend_weights(self.q, self.codes, self.scales, n_vis, self.n, self.scale, self.lse, self.weights,
+                                  pages=self.pages, page_size=self.page_size, seq=seq, idx=idx, stream=stream)
+
+
+class IndexerDistill:
+    """The indexer's training signal in its sparse phase ("DeepSeek-V4 model structure (2)", Q&A on the indexer's
+    training): the divergence of a layer's scores from the core attention's probabilities at the selected positions,
+    and its gradient with respect to the scores. `plan` holds the score rows of all layers; with write_mask they
+    are normalised over the pool."""
+
+    def __init__(self, plan: MaskFormPlan, core: CoreAttention):
+        nq, d = plan.dev.nq, plan.scores.device
+        self.plan, self.core = plan, core
+        self.idx = torch.empty(nq, plan.k, dtype=torch.int32, device=d)
+        self.t_logit = torch.empty(nq, plan.k, dtype=torch.float32, device=d)
+        self.loss, self.lse, self.t_lse = (torch.empty(nq, dtype=torch.float32, device=d) for _ in range(3))
+        self.dloss = torch.full((nq,), 1.0 / max(nq, 1), dtype=torch.float32, device=d)  # of the mean
+        self.dscores = torch.zeros(nq, plan.scores.shape[1], dtype=torch.float32, device=d)
+        self.ws = workspace(IDX_OP_DISTILL, nq, plan.dev.max_n, 1, device=d)
+
+    def run(self, layer: int, q, pos, seq):
+        """One layer after plan.run(), on the current stream: attends with its queries (as CoreAttention.run) and
+        returns (loss [nq], dscores [nq, max_n], written at visible positions)."""
+        dv = self.plan.dev
+        self.idx.copy_(self.plan.layer_topk(layer)[0])
+        self.core.run(q, pos, seq, dv.n_vis, self.idx)
+        self.core.selection_weights(seq, dv.n_vis, self.idx)
+        torch.log(self.core.weights, out=self.t_logit)  # -inf at the selection's padding
+        scores = self.plan.scores.view(dv.nq, self.plan.L, -1)[:, layer]
+        idx_distill(scores, dv.n_vis, dv.max_n, self.idx, self.t_logit, self.loss, self.lse, self.t_lse, self.ws)
+        idx_distill_bwd(scores, dv.n_vis, dv.max_n, self.idx, self.t_logit, self.lse, self.t_lse, self.dloss,
+                        self.dscores)
+        return self.loss, self.dscores
