@@ -29,6 +29,7 @@ constexpr int kTile = 64;        // entries per step
 constexpr int kRow = kD + 16;    // LDS row of a tile in fp16 values (the pad spreads rows over the banks)
 constexpr int kPRow = kTile + 8;
 constexpr int kQRow = 32;
+constexpr int kMostParts = 256;         // of a query's entries
 constexpr float kNone = -3.0e38f;  // reference of a head that has met no entry
 constexpr float kRoom = 7.0f;   // the reference lies this far below the largest logit (base 2) when it is set
 constexpr float kMost = 15.0f;   // and a logit at most this far above it: probabilities up to 2^15
@@ -549,28 +550,74 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     }
 }
 
-// join of the parts of one (query, head): 128 threads, 4 values each
-__global__ __launch_bounds__(128) void attend_join_kernel(const AttendArgs a, int splits) {
+// Join of the parts of one (query, head): o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i. 128 threads take 4 values
+// each; with many parts, G groups of them take every G-th.
+template <int G>
+__global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a, int splits) {
+    __shared__ float s_f[kMostParts];
+    __shared__ float2 s_wave[2 * G];
+    __shared__ __align__(16) v4f s_o[G > 1 ? (G - 1) * 128 : 1];
     const int64_t t = blockIdx.x / a.heads;
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t first = t * splits * a.heads + h;
     const int64_t step = a.heads;
-    float M = kNone;
-    for (int i = 0; i < splits; ++i) M = fmaxf(M, a.part_ml[2 * (first + i * step)]);
-    float L = 0.0f;
-    v4f o = {};
-    for (int i = 0; i < splits; ++i) {
-        const int64_t r = first + i * step;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * r] - M);
-        L += f * a.part_ml[2 * r + 1];
-        o += f * *reinterpret_cast<const v4f*>(a.part_o + r * kD + threadIdx.x * 4);
+    // references and sums: a part per thread
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    constexpr int kPer = (kMostParts + 128 * G - 1) / (128 * G);
+    float2 mine[kPer];
+    float R = kNone;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = k * 128 * G + (int)threadIdx.x;
+        mine[k] = i < splits ? ml[first + i * step] : float2{kNone, 0.0f};
+        R = fmaxf(R, mine[k].x);
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    o *= inv;
-    *reinterpret_cast<uint2*>(a.out + (int64_t)blockIdx.x * kD + threadIdx.x * 4) =
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) R = fmaxf(R, __shfl_xor(R, d));
+    if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6].x = R;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2 * G; ++k) R = fmaxf(R, s_wave[k].x);
+    float L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = k * 128 * G + (int)threadIdx.x;
+        const float f = __builtin_amdgcn_exp2f(mine[k].x - R);
+        if (i < splits) s_f[i] = f;
+        L += f * mine[k].y;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
+    if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6].y = L;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2 * G; ++k) L += s_wave[k].y;
+
+    const int grp = threadIdx.x >> 7, at = threadIdx.x & 127;
+    const float* po = a.part_o + first * kD + at * 4;
+    v4f o = {};
+    int i = grp;
+    for (; i + 7 * G < splits; i += 8 * G) {  // eight loads in flight
+        v4f v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const v4f*>(po + (int64_t)(i + k * G) * step * kD);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o += s_f[i + k * G] * v[k];
+    }
+#pragma unroll 4
+    for (; i < splits; i += G) o += s_f[i] * *reinterpret_cast<const v4f*>(po + (int64_t)i * step * kD);
+    if constexpr (G > 1) {
+        if (grp) s_o[(grp - 1) * 128 + at] = o;
+        __syncthreads();
+        if (grp) return;
+#pragma unroll
+        for (int k = 0; k < G - 1; ++k) o += s_o[k * 128 + at];
+    }
+    o *= L == 0.0f ? 0.0f : 1.0f / L;
+    *reinterpret_cast<uint2*>(a.out + (int64_t)blockIdx.x * kD + at * 4) =
         uint2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-    if (a.lse && threadIdx.x == 0)
-        a.lse[blockIdx.x] = L == 0.0f ? ninf() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    if (a.lse && at == 0) a.lse[blockIdx.x] = L == 0.0f ? ninf() : (R + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 // The attention's probability of every entry, mean over the heads, from the saved lse:
@@ -717,7 +764,7 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
     for (const auto& t : kTiles) {
         if (t.nh > 1 && heads <= 8 * t.nh) continue;  // half of the tile would be empty
         const int64_t blocks = (int64_t)nq * ((heads + 16 * t.nh - 1) / (16 * t.nh));
-        for (int64_t s = 1; s <= steps && s <= 256; ++s) {
+        for (int64_t s = 1; s <= steps && s <= kMostParts; ++s) {
             if (s > 1 && blocks * s > 8 * 256 + blocks) break;  // rounds are even enough
             const float rounds = (float)((blocks * s + 255) / 256);
             const float time = rounds * ((float)((steps + s - 1) / s) * t.step + t.block) +
@@ -785,7 +832,12 @@ hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream) {
         launch_attend_as<1>(a, cut.splits, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || cut.splits <= 1) return err;
-    hipLaunchKernelGGL(attend_join_kernel, dim3((uint32_t)a.nq * a.heads), dim3(128), 0, stream, a, cut.splits);
+    // (four groups: 17 -> 8 us for 512 pairs of 32 parts; one: 35 us for 33000 pairs of 3, bound by HBM)
+    const dim3 pairs((uint32_t)a.nq * a.heads);
+    if (cut.splits >= 8)
+        hipLaunchKernelGGL(attend_join_kernel<4>, pairs, dim3(512), 0, stream, a, cut.splits);
+    else
+        hipLaunchKernelGGL(attend_join_kernel<1>, pairs, dim3(128), 0, stream, a, cut.splits);
     return hipGetLastError();
 }
 

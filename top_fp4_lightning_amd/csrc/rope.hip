@@ -14,6 +14,7 @@ namespace fp4idx {
 namespace {
 
 constexpr int kRopeLds = 4096;  // (cos, sin) pairs per block: 32 KB
+constexpr int kRows = 4;        // rows of a lane in flight
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -52,59 +53,64 @@ __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a, int tokens_
     const int at = threadIdx.x & (lanes - 1);
     const int step = 256 >> lanes_log2;  // rows per pass of the block
     const int step_tok = step / a.heads, step_head = step - step_tok * a.heads;
-    int tk = (int)(threadIdx.x >> lanes_log2) / a.heads;
-    int h = (int)(threadIdx.x >> lanes_log2) - tk * a.heads;
     const T* xs = (const T*)a.x;
     T* ys = (T*)a.out;
     typedef Vec<T, V> W;
-    while (tk < toks) {
-        const T* x = xs + (tok0 + tk) * a.x_token + h * a.x_head;
-        T* y = ys + (tok0 + tk) * a.out_token + h * a.out_head;
-        const float2* cs = s_cs + tk * pairs;
-        for (int it = at; it < items; it += lanes) {
-            if (it < rot_items) {
-                if constexpr (HALF) {
-                    const int i = it * V;
-                    const W v0 = *reinterpret_cast<const W*>(x + a.offset + i);
-                    const W v1 = *reinterpret_cast<const W*>(x + a.offset + pairs + i);
-                    W o0, o1;
+    for (int it = at; it < items; it += lanes) {
+        // what the item reads and writes of a row: one vector, or two (n1 apart)
+        const bool turns = it < rot_items;
+        constexpr int P = HALF ? V : (V > 1 ? V / 2 : 1);  // pairs of an item
+        int i0 = (it - rot_items) * V;
+        if (turns)
+            i0 = a.offset + it * (HALF ? V : 2 * P);
+        else if (i0 >= a.offset)
+            i0 += a.rot;
+        const int i1 = i0 + (HALF ? pairs : V);
+        constexpr bool kTwo = HALF || V == 1;
+        int tk = (int)(threadIdx.x >> lanes_log2) / a.heads;
+        int h = (int)(threadIdx.x >> lanes_log2) - tk * a.heads;
+        while (tk < toks) {
+            // kRows rows at a time, their reads ahead of the first use
+            W v[kRows][kTwo ? 2 : 1];
+            int64_t to[kRows];
+            int tok[kRows];
+            int n = 0;
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float2 z = cs[i + k];
-                        const float x0 = to_f<T>(v0.v[k]), x1 = to_f<T>(v1.v[k]);
-                        o0.v[k] = from_f<T>(x0 * z.x - x1 * z.y);
-                        o1.v[k] = from_f<T>(x1 * z.x + x0 * z.y);
+            for (int r = 0; r < kRows; ++r) {
+                tok[r] = tk;
+                if (tk < toks) {
+                    const T* x = xs + (tok0 + tk) * a.x_token + h * a.x_head;
+                    to[r] = (tok0 + tk) * a.out_token + h * a.out_head;
+                    v[r][0] = *reinterpret_cast<const W*>(x + i0);
+                    if (kTwo && turns) v[r][kTwo ? 1 : 0] = *reinterpret_cast<const W*>(x + i1);
+                    n = r + 1;
+                    tk += step_tok;
+                    h += step_head;
+                    if (h >= a.heads) {
+                        h -= a.heads;
+                        ++tk;
                     }
-                    *reinterpret_cast<W*>(y + a.offset + i) = o0;
-                    *reinterpret_cast<W*>(y + a.offset + pairs + i) = o1;
-                } else {
-                    constexpr int P = V > 1 ? V / 2 : 1;  // pairs of an item
-                    constexpr int N = V > 1 ? 1 : 2;      // accesses of an item
-                    W v[N];
-                    T* e = reinterpret_cast<T*>(v);
+                }
+            }
 #pragma unroll
-                    for (int n = 0; n < N; ++n) v[n] = reinterpret_cast<const W*>(x + a.offset + it * 2 * P)[n];
+            for (int r = 0; r < kRows; ++r) {
+                if (r >= n) continue;
+                if (turns) {
+                    const float2* cs = s_cs + tok[r] * pairs + it * P;
+                    T* e = reinterpret_cast<T*>(v[r]);
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
-                        const float2 z = cs[it * P + k];
-                        const float x0 = to_f<T>(e[2 * k]), x1 = to_f<T>(e[2 * k + 1]);
-                        e[2 * k] = from_f<T>(x0 * z.x - x1 * z.y);
-                        e[2 * k + 1] = from_f<T>(x1 * z.x + x0 * z.y);
+                        const float2 z = cs[k];
+                        T& e0 = e[HALF ? k : 2 * k];
+                        T& e1 = e[HALF ? V + k : 2 * k + 1];
+                        const float x0 = to_f<T>(e0), x1 = to_f<T>(e1);
+                        e0 = from_f<T>(x0 * z.x - x1 * z.y);
+                        e1 = from_f<T>(x1 * z.x + x0 * z.y);
                     }
-#pragma unroll
-                    for (int n = 0; n < N; ++n) reinterpret_cast<W*>(y + a.offset + it * 2 * P)[n] = v[n];
                 }
-            } else {
-                int i = (it - rot_items) * V;
-                if (i >= a.offset) i += a.rot;
-                *reinterpret_cast<W*>(y + i) = *reinterpret_cast<const W*>(x + i);
+                *reinterpret_cast<W*>(ys + to[r] + i0) = v[r][0];
+                if (kTwo && turns) *reinterpret_cast<W*>(ys + to[r] + i1) = v[r][kTwo ? 1 : 0];
             }
-        }
-        tk += step_tok;
-        h += step_head;
-        if (h >= a.heads) {
-            h -= a.heads;
-            ++tk;
         }
     }
 }
