@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kD = 512;
 constexpr int kTile = 64;        // entries per step
-constexpr int kRow = kD + 16;    // LDS row of a tile in fp16 values (the pad spreads rows over the banks)
+constexpr int kRow = kD + 16;    // LDS row of a query or an output in 16-bit values (the pad spreads rows over the banks)
 constexpr int kPRow = kTile + 8;
 constexpr int kQRow = 32;
 constexpr int kMostParts = 256;         // of a query's entries
@@ -231,7 +231,7 @@ __device__ __forceinline__ bool unit_of(uint32_t b, uint32_t units, uint32_t til
 // NH: heads of a block in sixteens
 template <int NH>
 struct Shared {
-    _Float16 kv[2][kTile * kRow];
+    _Float16 kv[2 * kTile * kD];       // two steps' rows; the queries and the outputs on their ways
     _Float16 p[2][NH * 16 * kPRow];
     float m[NH * 16][4];
     float l[NH * 16][4];
@@ -283,12 +283,12 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
     }
-    stage_query<kHeads>(a, h0, qr, sh.kv[1], sh.fr);
+    stage_query<kHeads>(a, h0, qr, sh.kv, sh.fr);
     __syncthreads();
     h8 q[NH][15];
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-        const _Float16* at = sh.kv[1] + (n * 16 + c) * kRow + g * 32;
+        const _Float16* at = sh.kv + (n * 16 + c) * kRow + g * 32;
 #pragma unroll
         for (int x = 0; x < 15; ++x) q[n][x] = *reinterpret_cast<const h8*>(at + (x >> 2) * 128 + (x & 3) * 8);
         const h8 ql = *reinterpret_cast<const h8*>(at + 3 * 128 + 3 * 8);
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
 #pragma unroll
         for (int x = 0; x < 15; ++x) asm volatile("" : "+a"(q[n][x]));
     }
-    __syncthreads();  // before kv[1] takes rows
+    __syncthreads();  // before kv takes rows
     v4f o[NH][8] = {};
     v4f s[NH];
     float l[NH];         // this lane's part of the sum of 2^(s2 - R)
@@ -305,6 +305,12 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
 #pragma unroll
     for (int n = 0; n < NH; ++n) l[n] = 0.0f;
 
+    // A row of a step is 1024 bytes, and its 16-byte pieces are exchanged within each 128: piece p lies at
+    // p ^ (2 (row % 4) + row / 4 % 2). Eight rows' same pieces (a write), and four rows' same pairs of pieces (a
+    // transposed read), then lie in different banks. Addresses of other pieces, of rows 4 on and of the other buffer
+    // differ from these in single bits.
+    const int at_in = (w * 16 + c) * kD + ((g * 4) ^ ((c & 3) * 2 + ((c >> 2) & 1))) * 8;
+    const int at_out = (g * 8 + (c >> 2)) * kD + w * 128 + (((c >> 1) & 1) ^ ((c >> 2) * 2)) * 8 + (c & 1) * 4;
     // Probabilities 2^(s2 - R) of sixteen heads' products s into p[step & 1]; true if a logit lies too far above R.
     const auto probabilities = [&](int n, float2 fr, int step) {
         float y[4];
@@ -368,17 +374,17 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     const auto turn = [&](auto pv, auto qk, int i) {
         constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value;
         const int buf = i & 1;
-        _Float16* in = sh.kv[buf ^ 1] + (w * 16 + c) * kRow + g * 32;
-        const _Float16* out = sh.kv[buf] + (g * 8 + (c >> 2)) * kRow + w * 128 + (c & 3) * 4;
+        const int in = at_in ^ (buf ? 0 : kTile * kD), out = at_out ^ (buf ? kTile * kD : 0);
         const _Float16* prob = sh.p[buf] + c * kPRow + g * 8;
         // a transposed read: lane group g gets entries 32 (y / 8) + 8 g .. + 7 of value 16 (y % 8) + c
         const auto rows8 = [&](int y) {
-            const _Float16* at = out + (y >> 3) * 32 * kRow + (y & 7) * 16;
-            const hv4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
-            const hv4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 4 * kRow));
+            const int lo = out ^ ((y & 3) * 16), hi = out ^ ((y & 3) * 16 + 4 * kD + 8);
+            const int at = (y >> 3) * 32 * kD + ((y >> 2) & 1) * 64;
+            const hv4 l4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(sh.kv + lo + at));
+            const hv4 h4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(sh.kv + hi + at));
             h8 v;
-            __builtin_memcpy(&v, &lo, 8);
-            __builtin_memcpy((char*)&v + 8, &hi, 8);
+            __builtin_memcpy(&v, &l4, 8);
+            __builtin_memcpy((char*)&v + 8, &h4, 8);
             return v;
         };
         h8 k, v[4], p[NH], ql[NH];
@@ -428,7 +434,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         for (int x = 0; x < 16; ++x) {
             if constexpr (kQk) {
                 const h8 kx = k;
-                *reinterpret_cast<h8*>(in + (x >> 2) * 128 + (x & 3) * 8) = kx;
+                *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 3) * 8)) + (x >> 2) * 128) = kx;
                 if (x < 15) k = values8(fd.kv, (x + 1) >> 2, (x + 1) & 3, g, there);
                 if ((x & 3) == 3) load_chunk(a, row1, g, x >> 2, fd.kv);
 #pragma unroll
@@ -510,7 +516,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         if (g == 0) sh.l[n * 16 + c][w] = x;
     }
     __syncthreads();
-    _Float16* rows = sh.kv[0];  // (bf16) the block's output rows, to be written whole
+    _Float16* rows = sh.kv;  // (bf16) the block's output rows, to be written whole
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
         const int hl = n * 16 + c;

@@ -89,35 +89,44 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
     return v;
 }
 
-// the row's end: the teacher's sum and the loss. Whole block.
-__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, MaxSum row, MaxSum* lds_ms, double* lds_d) {
+// A thread's share of the row's teacher entries, asked for before the row's own sum is known: three dependent
+// reads (position, score, logit) would otherwise stand at the end of every row.
+struct Teacher {
+    float tl[kPerThread], sl[kPerThread];  // logits (-inf: not an entry), the row's scores there
+};
+__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, Teacher& e) {
     const float* s = a.scores + t * a.score_stride;
     const int32_t n = visible(a, t);
-    const float c = a.inv_temp * kLog2e;
-    float tl[kPerThread], sl[kPerThread];
-    MaxSum v{ninf(), 0.0f};
+    int32_t p[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-        tl[k] = ninf();
-        sl[k] = 0.0f;
         const int i = k * kThreads + (int)threadIdx.x;
-        if (i < a.k) {
-            const int32_t p = a.t_idx[t * a.t_stride + i];
-            if (p >= 0 && p < n) {
-                sl[k] = s[p];
-                if (sl[k] != ninf()) tl[k] = a.t_logit[t * a.t_stride + i];
-            }
-        }
-        if (tl[k] != ninf()) v = join(v, MaxSum{tl[k], 1.0f}, c);
+        p[k] = i < a.k ? a.t_idx[t * a.t_stride + i] : -1;
+        e.tl[k] = i < a.k ? a.t_logit[t * a.t_stride + i] : ninf();
     }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        e.sl[k] = p[k] >= 0 && p[k] < n ? s[p[k]] : ninf();
+        if (e.sl[k] == ninf()) e.tl[k] = ninf();
+    }
+}
+
+// the row's end: the teacher's sum and the loss. Whole block.
+__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, const Teacher& e, MaxSum row,
+                                           MaxSum* lds_ms, double* lds_d) {
+    const float c = a.inv_temp * kLog2e;
+    MaxSum v{ninf(), 0.0f};
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (e.tl[k] != ninf()) v = join(v, MaxSum{e.tl[k], 1.0f}, c);
     v = block_join(v, c, lds_ms);
     const double tlse = log_of(v, a.inv_temp), lse = log_of(row, a.inv_temp);
     double sum = 0.0;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k)
-        if (tl[k] != ninf()) {
-            const double d = (double)tl[k] * a.inv_temp - tlse;
-            sum += (double)expf((float)d) * (d - ((double)sl[k] * a.inv_temp - lse));
+        if (e.tl[k] != ninf()) {
+            const double d = (double)e.tl[k] * a.inv_temp - tlse;
+            sum += (double)expf((float)d) * (d - ((double)e.sl[k] * a.inv_temp - lse));
         }
     sum = block_sum(sum, lds_d);
     if (threadIdx.x == 0) {
@@ -138,9 +147,11 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a, 
     const int32_t i0 = (int32_t)min((int64_t)piece * per, (int64_t)n);
     const int32_t i1 = (int32_t)min((int64_t)i0 + per, (int64_t)n);
     const float c = a.inv_temp * kLog2e;
+    Teacher e;
+    if (pieces == 1) load_teacher(a, t, e);
     const MaxSum v = block_join(row_part(a.scores + t * a.score_stride, i0, i1, c), c, s_ms);
     if (pieces == 1)
-        finish_row(a, t, v, s_ms, s_d);
+        finish_row(a, t, e, v, s_ms, s_d);
     else if (threadIdx.x == 0)
         reinterpret_cast<MaxSum*>(a.ws)[blockIdx.x] = v;
 }
@@ -150,11 +161,13 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
     __shared__ double s_d[4];
     const int64_t t = blockIdx.x;
     const float c = a.inv_temp * kLog2e;
+    Teacher e;
+    load_teacher(a, t, e);
     MaxSum v{ninf(), 0.0f};
     for (int i = threadIdx.x; i < pieces; i += kThreads)
         v = join(v, reinterpret_cast<const MaxSum*>(a.ws)[t * pieces + i], c);
     v = block_join(v, c, s_ms);
-    finish_row(a, t, v, s_ms, s_d);
+    finish_row(a, t, e, v, s_ms, s_d);
 }
 
 __device__ __forceinline__ float softmax_of(float x, float inv_temp, float lse) {
