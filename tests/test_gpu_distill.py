@@ -147,6 +147,20 @@ def test_no_slots_and_no_positions(fx):
     check(fx, s[:, :0], [0, 0], 0, np.zeros((2, 3), int), np.zeros((2, 3)))
 
 
+def test_a_position_given_often_sums_in_one_order(fx):
+    rng = np.random.default_rng(8)
+    n, k = 9000, 2048
+    s, _, tl = rows(rng, 4, n, k)
+    idx = rng.integers(0, n // 100, (4, k)) * 100
+    check(fx, s, [n] * 4, n, idx, tl)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    args = (dev(s), dev(np.full(4, n, np.int32)), n, dev(idx.astype(np.int32)), dev(tl.astype(np.float32)))
+    loss, lse, tlse, dl = (torch.ones(4, device="cuda") for _ in range(4))
+    fx.idx_distill(*args, loss, lse, tlse, fx.workspace(fx.IDX_OP_DISTILL, 4, n, 1))
+    g = [fx.idx_distill_bwd(*args, lse, tlse, dl, torch.empty(4, n, device="cuda")) for _ in range(20)]
+    assert all(torch.equal(x, g[0]) for x in g)
+
+
 def test_gradient_against_differences(fx):
     """central differences of the loss in 64 bits from the scores the call saw"""
     rng = np.random.default_rng(6)

@@ -193,11 +193,14 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs
         for (int32_t i = p0 * kPiece + (int32_t)threadIdx.x; i < min(p1 * kPiece, n); i += kThreads) d[i] = 0.0f;
         return;
     }
+    // A position given several times sums in one order in every run: each wavefront has 512 consecutive slots, and
+    // the wavefronts add theirs one after the other (one turn up to 512 slots).
+    const int wave = (int)(threadIdx.x >> 6), turns = (a.k + kMaxK / 4 - 1) / (kMaxK / 4);
     int32_t at[kPerThread];
     float p[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-        const int i = k * kThreads + (int)threadIdx.x;
+        const int i = (wave * kPerThread + k) * 64 + (int)(threadIdx.x & 63);
         at[k] = -1;
         p[k] = 0.0f;
         if (i < a.k) {
@@ -209,10 +212,13 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs
     for (int32_t pc = p0; pc < p1; ++pc) {
         const int32_t i0 = pc * kPiece, i1 = min(i0 + kPiece, n);
         for (int i = threadIdx.x * 4; i < kPiece; i += kThreads * 4) *reinterpret_cast<v4f*>(s_p + i) = v4f{};
-        __syncthreads();
+        for (int turn = 0; turn < turns; ++turn) {
+            __syncthreads();
+            if (wave != turn) continue;
 #pragma unroll
-        for (int k = 0; k < kPerThread; ++k)
-            if (at[k] >= i0 && at[k] < i1) atomicAdd(s_p + (at[k] - i0), p[k]);
+            for (int k = 0; k < kPerThread; ++k)
+                if (at[k] >= i0 && at[k] < i1) atomicAdd(s_p + (at[k] - i0), p[k]);
+        }
         __syncthreads();
         for (int32_t i = i0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
             const v4f pv = *reinterpret_cast<const v4f*>(s_p + (i - i0));
