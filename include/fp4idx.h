@@ -413,10 +413,10 @@ idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double fact
  *             (freq at most 1).
  *   freq    : device double [rot / 2].
  *   rot     : even, 2 .. 8192; offset >= 0, offset + rot <= dim.
- *   out     : device, x's dtype; strides out_token, out_head (at least dim where the axis is longer than 1,
- *             so that rows do not overlap). May be x itself with x's strides: then only the rotated part is
- *             read and written. Otherwise out may not overlap x.
- *   tokens  : 0 .. 2^31 - 1 (0 enqueues nothing); heads 1 .. 65535; dim 2 .. 2^20.
+ *   out     : device, x's dtype; strides out_token, out_head: heads within a token's step or tokens within a
+ *             head's, at least dim apart (rows may not overlap). May be x itself with x's strides: then only the
+ *             rotated part is read and written. Otherwise out may not overlap x.
+ *   tokens  : 0 .. 2^24 - 1 (0 enqueues nothing); heads 1 .. 65535; dim 2 .. 2^20.
  */
 idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads, int32_t dim, int64_t x_token,
                     int64_t x_head, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
@@ -458,7 +458,8 @@ idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads,
  * out; what the cache holds there or at masked entries has no effect. A query without entries gets out = 0 and
  * lse = -inf. Products are exact in fp16 operands (q scaled by a power of two per row; values below 2^-28 of the
  * row's largest lose low bits), sums, maximum and normalisation fp32; probabilities are rounded to 11 bits for
- * the second product. A non-finite value in a q row makes that head's results NaN and no other's.
+ * the second product (those below 2^-20 of a head's largest to fewer, below 2^-31 perhaps to zero). A non-finite
+ * value in a q row makes that head's results NaN and no other's.
  */
 idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes, const uint8_t* scales,
                       int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,

@@ -92,6 +92,14 @@ def test_strides(fx, dtype):
     assert torch.equal(y[:, :, :8], big[:, :, :8]) and torch.equal(y[:, :, 72:], big[:, :, 72:])
 
 
+def test_outputs_with_heads_outermost(fx):
+    for gap in (0, 24):
+        buf = torch.full((40, 6 * (64 + gap) + 5), 5.0, device="cuda")
+        out = buf.as_strided((6, 40, 64), (64 + gap, buf.stride(0), 1))
+        run_case(fx, (6, 40, 64), 32, 16, "half", torch.float32, out=out)
+        assert (buf[:, 6 * (64 + gap):] == 5.0).all()
+
+
 def test_gradient_is_the_inverse_and_matches_differences(fx):
     """y is linear in x: (f(x + d) - f(x)) . w = d . grad, and rotating back gives x again"""
     g = torch.Generator(device="cuda").manual_seed(4)

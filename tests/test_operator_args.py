@@ -42,6 +42,16 @@ def test_rope_refusals(fx):
         (8, FAKE + 4, fx.IDX_EALIGN), ((0, 1), (FAKE + 2, 1), fx.IDX_EALIGN)])
 
 
+def test_rope_outputs_that_overlap(fx):
+    """rows dim apart are not enough: the heads of a token must end before the next token's, or the other way round"""
+    at = dict(tokens=2, heads=3, out_token=15, out_head=16)
+    good = [FAKE, 0, 4, 2, 128, 256, 128, FAKE, FAKE, 64, 64, 0, 1.0, 0, FAKE + 4096, 256, 128, None]
+    refuse(fx, "idx_rope", good, [
+        ((at["out_token"], at["out_head"]), v, fx.IDX_EINVAL)
+        for v in ((128, 128), (255, 128), (128, 511), (129, 500), (200, 300))])
+    refuse(fx, "idx_rope", good, [(at["tokens"], 1 << 24, fx.IDX_EUNSUPPORTED)])
+
+
 ATTEND = dict(q=0, nq=1, heads=2, codes=3, scales=4, rows=5, base=6, pages=7, pstride=8, nseq=9, psize=10, seq=11, nvis=12,
               maxn=13)
 

@@ -56,6 +56,7 @@ constexpr int64_t kMaxN = (int64_t)1 << 30;
 constexpr int32_t kMaxQueries = 65535;  // grid y dimension
 constexpr int32_t kMaxAttendHeads = 128;
 constexpr int32_t kMaxAttendList = 1 << 24;
+constexpr int64_t kMaxRopeTokens = (1 << 24) - 1;  // a block of 256 threads for each: below 2^32
 constexpr int64_t kMaxPoolScoreN = (int64_t)1 << 28;  // a score row read through a pool: below 2^30 bytes
 
 size_t ws_bytes_for(int32_t op, int32_t nq, int64_t max_n, int32_t k) {
@@ -496,7 +497,7 @@ idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads,
     REQUIRE(dtype == IDX_BF16 || dtype == IDX_F32, IDX_EUNSUPPORTED, "idx_rope: dtype=%d", dtype);
     REQUIRE(layout == IDX_ROPE_HALF || layout == IDX_ROPE_INTERLEAVED, IDX_EUNSUPPORTED, "idx_rope: layout=%d",
             layout);
-    REQUIRE(tokens >= 0 && tokens <= INT32_MAX, IDX_EUNSUPPORTED, "idx_rope: tokens=%lld out of [0, 2^31 - 1]",
+    REQUIRE(tokens >= 0 && tokens <= kMaxRopeTokens, IDX_EUNSUPPORTED, "idx_rope: tokens=%lld out of [0, 2^24 - 1]",
             (long long)tokens);
     REQUIRE(heads >= 1 && heads <= 65535, IDX_EUNSUPPORTED, "idx_rope: heads=%d out of [1, 65535]", heads);
     REQUIRE(dim >= 2 && dim <= (1 << 20), IDX_EUNSUPPORTED, "idx_rope: dim=%d out of [2, 2^20]", dim);
@@ -505,8 +506,13 @@ idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads,
     REQUIRE(isfinite(mscale), IDX_EINVAL, "idx_rope: mscale is not finite");
     if (tokens == 0) return ok();
     REQUIRE(x && pos && freq && out, IDX_EINVAL, "idx_rope: null pointer");
-    REQUIRE(x_token >= 0 && x_head >= 0 && (tokens == 1 || out_token >= dim) && (heads == 1 || out_head >= dim),
-            IDX_EINVAL, "idx_rope: strides must be >= 0, and out's at least dim (rows may not overlap)");
+    REQUIRE(x_token >= 0 && x_head >= 0, IDX_EINVAL, "idx_rope: strides must be >= 0");
+    // rows dim apart, and one axis of out inside a step of the other
+    REQUIRE((tokens == 1 || out_token >= dim) && (heads == 1 || out_head >= dim) &&
+                (tokens == 1 || heads == 1 || (out_token - dim) / (heads - 1) >= out_head ||
+                 (out_head - dim) / (tokens - 1) >= out_token),
+            IDX_EINVAL, "idx_rope: rows of out overlap: strides %lld and %lld", (long long)out_token,
+            (long long)out_head);
     REQUIRE(out != x || ((tokens == 1 || x_token == out_token) && (heads == 1 || x_head == out_head)), IDX_EINVAL,
             "idx_rope: in place, the strides must agree");
     const size_t size = dtype == IDX_BF16 ? 2 : 4;

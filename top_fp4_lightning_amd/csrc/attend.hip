@@ -114,6 +114,7 @@ __device__ __forceinline__ int32_t row_of(const AttendArgs& a, const Entries& e,
 
 // One lane's share of a cache row: lane group g (of 4) holds, for j = 0 .. 3, values 128j + 32g ..
 // 128j + 32g + 31: sixteen code bytes and two scales. The four groups read 64 consecutive bytes.
+typedef uint32_t u32_by2 __attribute__((aligned(2)));  // scales lie at any even address
 struct RowPart {
     uint4 code[4];
     uint32_t scale[4];  // four scales; the lane's two are the low or (odd g) the high half
@@ -123,7 +124,7 @@ struct RowPart {
 __device__ __forceinline__ void load_chunk(const AttendArgs& a, int32_t row, int g, int j, RowPart& r) {
     const int64_t at = row < 0 ? 0 : row;
     r.code[j] = *reinterpret_cast<const uint4*>(a.codes + at * 256 + g * 16 + 64 * j);
-    r.scale[j] = *reinterpret_cast<const uint32_t*>(a.scales + at * 32 + (g >> 1) * 4 + 8 * j);
+    r.scale[j] = *reinterpret_cast<const u32_by2*>(a.scales + at * 32 + (g >> 1) * 4 + 8 * j);
 }
 
 // values 8u .. 8u+7 of chunk j as fp16 (exact); there: the row is in the cache
