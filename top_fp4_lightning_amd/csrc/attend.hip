@@ -39,6 +39,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __fp16 hv4 __attribute__((vector_size(8)));
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) hv4 lds_hv4;
@@ -299,7 +300,14 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         for (int x = 0; x < 15; ++x) asm volatile("" : "+a"(q[n][x]));
     }
     __syncthreads();  // before kv takes rows
-    v4f o[NH][8] = {};
+    // The second product is 32 heads wide where the block has as many: half the instructions of 16, of twice the time
+    // (each holds back the wavefront's next ones as long as two others).
+    constexpr bool kWide = NH > 1;
+    constexpr int kOh = kWide ? NH / 2 : 1, kOv = kWide ? 4 : 8;  // output tiles: heads, values
+    typedef std::conditional_t<kWide, v16f, v4f> Out;
+    Out o[kOh][kOv] = {};
+    const int oc = kWide ? lane & 31 : c;          // this lane's head of an output tile
+    const int og = kWide ? lane >> 5 : g;          // and which fours of its values
     v4f s[NH];
     float l[NH];         // this lane's part of the sum of 2^(s2 - R)
     float sum[NH];       // and of the step whose probabilities were formed last
@@ -311,7 +319,8 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     // transposed read), then lie in different banks. Addresses of other pieces, of rows 4 on and of the other buffer
     // differ from these in single bits.
     const int at_in = (w * 16 + c) * kD + ((g * 4) ^ ((c & 3) * 2 + ((c >> 2) & 1))) * 8;
-    const int at_out = (g * 8 + (c >> 2)) * kD + w * 128 + (((c >> 1) & 1) ^ ((c >> 2) * 2)) * 8 + (c & 1) * 4;
+    const int first = kWide ? (g & 1) * 2 + ((c >> 1) & 1) : (c >> 1) & 1;  // piece
+    const int at_out = (og * 8 + (c >> 2)) * kD + w * 128 + (first ^ ((c >> 2) * 2)) * 8 + (c & 1) * 4;
     // Probabilities 2^(s2 - R) of sixteen heads' products s into p[step & 1]; true if a logit lies too far above R.
     const auto probabilities = [&](int n, float2 fr, int step) {
         float y[4];
@@ -349,16 +358,20 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     };
     const auto rebase = [&](int step) {
         float2 fr[NH];
-        float r[NH];
+        float r[NH], was[kOh];
 #pragma unroll
         for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
+#pragma unroll
+        for (int n = 0; n < kOh; ++n) was[n] = sh.fr[n * 32 + oc].y;
         new_reference(fr, r);
 #pragma unroll
-        for (int n = 0; n < NH; ++n) {
-            const float alpha = __builtin_amdgcn_exp2f(-fr[n].y - r[n]);  // 0 at a head's first entry (o is 0 then)
+        for (int n = 0; n < NH; ++n) l[n] *= __builtin_amdgcn_exp2f(-fr[n].y - r[n]);  // 0 at a head's first entry
 #pragma unroll
-            for (int d = 0; d < 8; ++d) o[n][d] *= alpha;
-            l[n] *= alpha;
+        for (int n = 0; n < kOh; ++n) {
+            const v4f mv = *reinterpret_cast<const v4f*>(sh.m[n * 32 + oc]);
+            const float alpha = __builtin_amdgcn_exp2f(-was[n] - fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3])));
+#pragma unroll
+            for (int d = 0; d < kOv; ++d) o[n][d] *= alpha;
         }
         if (w == 0 && g == 0) {  // (every wavefront has read the old ones)
 #pragma unroll
@@ -376,11 +389,17 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value;
         const int buf = i & 1;
         const int in = at_in ^ (buf ? 0 : kTile * kD), out = at_out ^ (buf ? kTile * kD : 0);
-        const _Float16* prob = sh.p[buf] + c * kPRow + g * 8;
-        // a transposed read: lane group g gets entries 32 (y / 8) + 8 g .. + 7 of value 16 (y % 8) + c
+        const _Float16* prob = sh.p[buf] + oc * kPRow + og * 8;
+        // a transposed read of unit y's eight entries (below) of this lane's value
         const auto rows8 = [&](int y) {
-            const int lo = out ^ ((y & 3) * 16), hi = out ^ ((y & 3) * 16 + 4 * kD + 8);
-            const int at = (y >> 3) * 32 * kD + ((y >> 2) & 1) * 64;
+            int lo, hi, at;
+            if constexpr (kWide) {
+                lo = out ^ ((y & 1) * 32), hi = out ^ ((y & 1) * 32 + 4 * kD + 8);
+                at = (y >> 2) * 16 * kD + ((y >> 1) & 1) * 64;
+            } else {
+                lo = out ^ ((y & 3) * 16), hi = out ^ ((y & 3) * 16 + 4 * kD + 8);
+                at = (y >> 3) * 32 * kD + ((y >> 2) & 1) * 64;
+            }
             const hv4 l4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(sh.kv + lo + at));
             const hv4 h4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(sh.kv + hi + at));
             h8 v;
@@ -388,12 +407,12 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             __builtin_memcpy((char*)&v + 8, &h4, 8);
             return v;
         };
-        h8 k, v[4], p[NH], ql[NH];
+        h8 k, v[4], p[kOh], ql[NH];
         int4 ov{0, 0, 0, 0};
         if constexpr (kPv) {
             ov = *reinterpret_cast<const int4*>(sh.over[buf]);
 #pragma unroll
-            for (int n = 0; n < NH; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow);
+            for (int n = 0; n < kOh; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow);
             v[0] = rows8(0);
         }
         const bool there = fd.row >= 0;
@@ -409,12 +428,13 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
                 rebase(i);
 #pragma unroll
-                for (int n = 0; n < NH; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow);
+                for (int n = 0; n < kOh; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow);
             }
 #pragma unroll
             for (int n = 0; n < NH; ++n) l[n] += sum[n];
         }
-        // y-th unit of the second product: entries 32 (y / 8) .. + 31 of values 16 (y % 8) .. + 15
+        // y-th unit of the second product: entries 32 (y / 8) .. + 31 of values 16 (y % 8) .. + 15, or, wide, entries
+        // 16 (y / 4) .. + 15 of values 32 (y % 4) .. + 31
         const auto unit = [&](int y) {
             // operands are read one unit ahead, three where units follow each other closely
             const auto ahead = [](int u) { return u < 0 ? 0 : u + 1 + (u >= 4) + (u >= 6); };
@@ -422,9 +442,15 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             for (int r = 1; r < 16; ++r)
                 if (r > ahead(y - 1) && r <= ahead(y)) v[r & 3] = rows8(r);
 #pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                o[n][y & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y & 3], p[n], o[n][y & 7], 0, 0, 0);
-                if (y == 7) p[n] = *reinterpret_cast<const h8*>(prob + n * 16 * kPRow + 32);
+            for (int n = 0; n < kOh; ++n) {
+                if constexpr (kWide) {
+                    o[n][y & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[y & 3], p[n], o[n][y & 3], 0, 0, 0);
+                    if ((y & 3) == 3 && y < 15)
+                        p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow + ((y >> 2) + 1) * 16);
+                } else {
+                    o[n][y & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y & 3], p[n], o[n][y & 7], 0, 0, 0);
+                    if (y == 7) p[n] = *reinterpret_cast<const h8*>(prob + 32);
+                }
             }
         };
         if constexpr (kQk) {
@@ -433,6 +459,9 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
+            if constexpr (kPv) {
+                if (!kQk || (x & 1)) unit(kQk ? x >> 1 : x);
+            }
             if constexpr (kQk) {
                 const h8 kx = k;
                 *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 3) * 8)) + (x >> 2) * 128) = kx;
@@ -444,11 +473,8 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
                     s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, x < 15 ? q[n][x < 15 ? x : 0] : ql[n], s[n], 0, 0, 0);
                 }
             }
-            if constexpr (kPv) {
-                if (!kQk || (x & 1)) unit(kQk ? x >> 1 : x);
-            }
 #pragma unroll
-            for (int y = 0; y < NH * (kQk + (kPv && (x & 1))); ++y) {
+            for (int y = 0; y < NH * kQk + kOh * (kPv && (x & 1)); ++y) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
             }
@@ -489,9 +515,9 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
                 over |= probabilities(n, fr[n], i + 1);
                 if constexpr (kPv) {
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
+                    for (int y = 0; y < 8 * kOh / NH; ++y) {
                         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, 3 * NH / kOh, 0);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -519,30 +545,42 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     __syncthreads();
     _Float16* rows = sh.kv;  // (bf16) the block's output rows, to be written whole
 #pragma unroll
-    for (int n = 0; n < NH; ++n) {
-        const int hl = n * 16 + c;
+    for (int n = 0; n < kOh; ++n) {
+        const int hl = n * 32 + oc;
         const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
         const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]);
         const int h = h0 + hl;
+        // four values of tile d lie at 16 d + 4 g, or, wide, at 32 (d / 4) + 8 (d % 4) + 4 og
+        const auto four = [&](int d) {
+            if constexpr (kWide) {
+                const Out& x = o[n][d >> 2];
+                const int i = (d & 3) * 4;
+                return v4f{x[i], x[i + 1], x[i + 2], x[i + 3]};
+            } else {
+                return o[n][d];
+            }
+        };
+        const auto at_four = [&](int d) { return kWide ? (d >> 2) * 32 + (d & 3) * 8 + og * 4 : d * 16 + og * 4; };
+        constexpr int kFours = kWide ? 16 : 8;
         if (splits > 1) {
             if (h >= a.heads) continue;
             const int64_t r = (int64_t)unit * a.heads + h;
-            float* po = a.part_o + r * kD + w * 128 + g * 4;
+            float* po = a.part_o + r * kD + w * 128;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) *reinterpret_cast<v4f*>(po + d * 16) = o[n][d];
-            if (w == 0 && g == 0) {
+            for (int d = 0; d < kFours; ++d) *reinterpret_cast<v4f*>(po + at_four(d)) = four(d);
+            if (w == 0 && og == 0) {
                 a.part_ml[2 * r] = -sh.fr[hl].y;
                 a.part_ml[2 * r + 1] = L;
             }
         } else {
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            _Float16* po = rows + hl * kRow + w * 128 + g * 4;
+            _Float16* po = rows + hl * kRow + w * 128;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                const v4f y = o[n][d] * inv;
-                *reinterpret_cast<uint2*>(po + d * 16) = uint2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+            for (int d = 0; d < kFours; ++d) {
+                const v4f y = four(d) * inv;
+                *reinterpret_cast<uint2*>(po + at_four(d)) = uint2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
             }
-            if (a.lse && h < a.heads && w == 0 && g == 0)
+            if (a.lse && h < a.heads && w == 0 && og == 0)
                 a.lse[t * a.heads + h] = L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) - sh.fr[hl].y) * kLn2;
         }
     }
