@@ -793,8 +793,8 @@ namespace {
 
 // How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
 // units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
-// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.8 and 13 at 64
-// heads, 1.35 and 9 at 32, 1.15 and 7 at 16; a join 4, and its parts at 4 TB/s.
+// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.7 and 13 at 64
+// heads, 1.17 and 9 at 32, 1.14 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
 struct Cut {
     int nh, splits;
 };
@@ -802,7 +802,7 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
     static constexpr struct {
         int nh;
         float step, block;
-    } kTiles[] = {{4, 1.8f, 13.0f}, {2, 1.35f, 9.0f}, {1, 1.15f, 7.0f}};
+    } kTiles[] = {{4, 1.7f, 13.0f}, {2, 1.17f, 9.0f}, {1, 1.14f, 7.0f}};
     const int64_t steps = entries > kTile ? (entries + kTile - 1) / kTile : 1;
     Cut best{1, 1};
     float least = 0.0f;
