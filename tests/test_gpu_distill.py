@@ -111,6 +111,19 @@ def test_few_long_and_many_short_rows(fx, nq, n, k):
     check(fx, s, rng.integers(0, n + 1, nq), n, idx, tl)
 
 
+def test_a_gradient_beyond_the_last_level_cache(fx):
+    """above 2^25 scores: most rows short, some of several pieces, the strides as wide as the longest"""
+    rng = np.random.default_rng(9)
+    nq, n, k = 1100, 31000, 40
+    nv = rng.integers(0, 50, nq)
+    nv[::150] = [n, n - 1, 4096, 8192, 8191, 12289, 20000, 30000]
+    s = np.zeros((nq, n), np.float32)
+    for t in range(nq):
+        s[t, :nv[t]] = rng.standard_normal(nv[t]) * 3
+    idx = (rng.random((nq, k)) * (nv[:, None] + 1)).astype(np.int64) - 1
+    check(fx, s, nv, n, idx, rng.standard_normal((nq, k)) * 2)
+
+
 @pytest.mark.parametrize("inv_temp", [0.25, 1.0, 3.0])
 @pytest.mark.parametrize("spread", [0.1, 30.0])
 def test_temperatures_and_spreads(fx, inv_temp, spread):

@@ -5,7 +5,10 @@
 //
 // Both directions are one pass over the row: the forward reads it (running maximum and sum per
 // thread, base 2), the gradient reads it and writes as much, with the teacher's probabilities of a piece
-// of the row laid out in LDS before the piece is streamed. They are bound by HBM.
+// of the row laid out in LDS before the piece is streamed. They are bound by HBM: 4096 rows of 32768 scores (0.54 GB)
+// take 100 us forward and 293 us with the gradient (5.5 TB/s over both; a copy reaches 4.8). Few rows are cut into
+// pieces of at least 4096 scores, so that the compute units have about four blocks each, and joined by a second launch
+// (8 rows of 2^20: 9 and 5 us, the gradient 13).
 #include "operators.h"
 
 namespace fp4idx {
@@ -57,14 +60,50 @@ __device__ __forceinline__ double log_of(MaxSum v, float inv_temp) {
     return v.l == 0.0f ? -__builtin_inf() : (double)v.m * inv_temp + log((double)v.l);
 }
 
-// the sum over s[i0 .. i1), this thread's share
-__device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t i0, int32_t i1, float c) {
+// A thread's share of the row's teacher entries, asked for before the row's own sum is known: three dependent
+// reads (position, score, logit) would otherwise stand at the end of every row.
+struct Teacher {
+    int32_t p[kPerThread];                 // positions, -1: not an entry
+    float tl[kPerThread], sl[kPerThread];  // logits, the row's scores there
+};
+__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, Teacher& e) {
+    const int32_t n = visible(a, t);
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int i = k * kThreads + (int)threadIdx.x;
+        const int32_t p = i < a.k ? a.t_idx[t * a.t_stride + i] : -1;
+        e.tl[k] = i < a.k ? a.t_logit[t * a.t_stride + i] : ninf();
+        e.p[k] = p < n ? p : -1;
+    }
+}
+__device__ __forceinline__ void load_scores(const float* __restrict__ s, int32_t from, Teacher& e) {
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (e.p[k] >= from) e.sl[k] = s[e.p[k]];
+}
+
+// The sum over s[i0 .. i1), this thread's share. With teacher entries (i0 = 0, the whole row), their scores are taken
+// on the way, from a copy of each piece in LDS: read by themselves they would cost a line each (4096 rows of up to
+// 32768 scores with 512 entries: 0.72 GB of reads in place of 0.49).
+template <bool TAKE>
+__device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t i0, int32_t i1, float c, Teacher* e,
+                                           float* piece) {
     MaxSum v{ninf(), 0.0f};
-    int32_t i = i0 + (int32_t)threadIdx.x * 4;
-    for (; i + 3 * kThreads * 4 + 4 <= i1; i += 4 * kThreads * 4) {
+    int32_t p0 = i0;
+    for (; p0 + kPiece <= i1; p0 += kPiece) {
+        const int32_t i = p0 + (int32_t)threadIdx.x * 4;
         f4u x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * kThreads * 4);
+        if constexpr (TAKE) {
+            if (p0) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<v4f*>(piece + (threadIdx.x + k * kThreads) * 4) = x[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k)
+                if (e->p[k] >= p0 && e->p[k] < p0 + kPiece) e->sl[k] = piece[e->p[k] - p0];
+        }
         float top = ninf();
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3])));
@@ -78,7 +117,8 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
         v.l = v.l * __builtin_amdgcn_exp2f((v.m - r) * c) + sum;
         v.m = m;
     }
-    for (; i < i1; i += kThreads * 4) {
+    if constexpr (TAKE) load_scores(s, p0, *e);
+    for (int32_t i = p0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (i + j < i1) {
@@ -89,36 +129,16 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
     return v;
 }
 
-// A thread's share of the row's teacher entries, asked for before the row's own sum is known: three dependent
-// reads (position, score, logit) would otherwise stand at the end of every row.
-struct Teacher {
-    float tl[kPerThread], sl[kPerThread];  // logits (-inf: not an entry), the row's scores there
-};
-__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, Teacher& e) {
-    const float* s = a.scores + t * a.score_stride;
-    const int32_t n = visible(a, t);
-    int32_t p[kPerThread];
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-        const int i = k * kThreads + (int)threadIdx.x;
-        p[k] = i < a.k ? a.t_idx[t * a.t_stride + i] : -1;
-        e.tl[k] = i < a.k ? a.t_logit[t * a.t_stride + i] : ninf();
-    }
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-        e.sl[k] = p[k] >= 0 && p[k] < n ? s[p[k]] : ninf();
-        if (e.sl[k] == ninf()) e.tl[k] = ninf();
-    }
-}
-
 // the row's end: the teacher's sum and the loss. Whole block.
-__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, const Teacher& e, MaxSum row,
+__device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teacher& e, MaxSum row,
                                            MaxSum* lds_ms, double* lds_d) {
     const float c = a.inv_temp * kLog2e;
     MaxSum v{ninf(), 0.0f};
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k)
+    for (int k = 0; k < kPerThread; ++k) {
+        if (e.p[k] < 0 || e.sl[k] == ninf()) e.tl[k] = ninf();
         if (e.tl[k] != ninf()) v = join(v, MaxSum{e.tl[k], 1.0f}, c);
+    }
     v = block_join(v, c, lds_ms);
     const double tlse = log_of(v, a.inv_temp), lse = log_of(row, a.inv_temp);
     double sum = 0.0;
@@ -136,10 +156,22 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, cons
     }
 }
 
-// one block per row (pieces == 1), or per piece of a row: then only (max, sum) of the piece is written
-__global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a, int pieces) {
+// a block for every row
+__global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a) {
     __shared__ MaxSum s_ms[4];
     __shared__ double s_d[4];
+    __shared__ __align__(16) float s_piece[kPiece];
+    const int64_t t = blockIdx.x;
+    const float c = a.inv_temp * kLog2e;
+    Teacher e;
+    load_teacher(a, t, e);
+    const MaxSum v = row_part<true>(a.scores + t * a.score_stride, 0, visible(a, t), c, &e, s_piece);
+    finish_row(a, t, e, block_join(v, c, s_ms), s_ms, s_d);
+}
+
+// few rows: a block for a piece of one, whose (max, sum) it writes
+__global__ __launch_bounds__(kThreads) void distill_piece_kernel(const DistillArgs a, int pieces) {
+    __shared__ MaxSum s_ms[4];
     const int64_t t = blockIdx.x / pieces;
     const int piece = (int)(blockIdx.x % pieces);
     const int32_t n = visible(a, t);
@@ -147,13 +179,8 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a, 
     const int32_t i0 = (int32_t)min((int64_t)piece * per, (int64_t)n);
     const int32_t i1 = (int32_t)min((int64_t)i0 + per, (int64_t)n);
     const float c = a.inv_temp * kLog2e;
-    Teacher e;
-    if (pieces == 1) load_teacher(a, t, e);
-    const MaxSum v = block_join(row_part(a.scores + t * a.score_stride, i0, i1, c), c, s_ms);
-    if (pieces == 1)
-        finish_row(a, t, e, v, s_ms, s_d);
-    else if (threadIdx.x == 0)
-        reinterpret_cast<MaxSum*>(a.ws)[blockIdx.x] = v;
+    const MaxSum v = block_join(row_part<false>(a.scores + t * a.score_stride, i0, i1, c, nullptr, nullptr), c, s_ms);
+    if (threadIdx.x == 0) reinterpret_cast<MaxSum*>(a.ws)[blockIdx.x] = v;
 }
 
 __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArgs a, int pieces) {
@@ -163,6 +190,7 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
     const float c = a.inv_temp * kLog2e;
     Teacher e;
     load_teacher(a, t, e);
+    load_scores(a.scores + t * a.score_stride, 0, e);
     MaxSum v{ninf(), 0.0f};
     for (int i = threadIdx.x; i < pieces; i += kThreads)
         v = join(v, reinterpret_cast<const MaxSum*>(a.ws)[t * pieces + i], c);
@@ -174,10 +202,12 @@ __device__ __forceinline__ float softmax_of(float x, float inv_temp, float lse) 
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, inv_temp, -lse) * kLog2e);
 }
 
-// gradient: a block takes a range of whole pieces of one row
+// Gradient: a block takes a range of whole pieces of one row. The last rows come first: after the forward the last-level
+// cache holds those. PAST: the gradient is written past that cache, which leaves it to the scores.
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs a, int blocks_per_row) {
     __shared__ float s_p[kPiece];
-    const int64_t t = blockIdx.x / blocks_per_row;
+    const int64_t t = a.nq - 1 - (int64_t)(blockIdx.x / blocks_per_row);
     const int part = (int)(blockIdx.x % blocks_per_row);
     const int32_t n = visible(a, t);
     const int32_t pieces = (n + kPiece - 1) / kPiece;
@@ -228,7 +258,10 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     y[j] = x[j] == ninf() ? 0.0f : gain * (softmax_of(x[j], a.inv_temp, lse) - pv[j]);
-                *reinterpret_cast<f4u*>(d + i) = y;
+                if constexpr (PAST)
+                    __builtin_nontemporal_store(y, reinterpret_cast<f4u*>(d + i));
+                else
+                    *reinterpret_cast<f4u*>(d + i) = y;
             } else {
                 for (int j = 0; i + j < i1; ++j) {
                     const float x = s[i + j];
@@ -257,16 +290,26 @@ size_t distill_workspace_bytes(int32_t nq, int64_t max_n) {
 
 hipError_t launch_distill(const DistillArgs& a, hipStream_t stream) {
     const int pieces = distill_pieces(a.nq, a.max_n);
-    hipLaunchKernelGGL(distill_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
+    if (pieces == 1) {
+        hipLaunchKernelGGL(distill_kernel, dim3((unsigned)a.nq), dim3(kThreads), 0, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(distill_piece_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
     hipError_t err = hipGetLastError();
-    if (err != hipSuccess || pieces == 1) return err;
+    if (err != hipSuccess) return err;
     hipLaunchKernelGGL(distill_join_kernel, dim3((unsigned)a.nq), dim3(kThreads), 0, stream, a, pieces);
     return hipGetLastError();
 }
 
 hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t stream) {
     const int pieces = distill_pieces(a.nq, a.max_n);
-    hipLaunchKernelGGL(distill_bwd_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
+    // Past the 256 MB cache from 128 MB of scores on. Both directions and a read of the gradient, us (past / not): 1024 x
+    // 32768 100 / 102, 2048 206 / 225, 4096 395 / 416; 256 (32 MB) 43 / 40.
+    const dim3 grid((unsigned)a.nq * pieces);
+    if ((int64_t)a.nq * a.max_n >= (int64_t)1 << 25)
+        hipLaunchKernelGGL(distill_bwd_kernel<true>, grid, dim3(kThreads), 0, stream, a, pieces);
+    else
+        hipLaunchKernelGGL(distill_bwd_kernel<false>, grid, dim3(kThreads), 0, stream, a, pieces);
     return hipGetLastError();
 }
 
