@@ -17,6 +17,17 @@
 // (below that they lose bits worth less than 2^-39 of it). Products and sums are fp32 in the matrix
 // units. Probabilities enter the second product as fp16 values (11 bits) up to 2^15, the largest so far of a
 // head above 2^6: values down to 2^-20 of it are normal numbers, and what rounds to zero is below 2^-31 of it.
+//
+// What bounds it. Per step and wavefront at 64 heads: 2048 cycles of matrix instructions (64 of 16x16x32, 32 of
+// 32x32x16) and about 290 others, in 1.65 us. The matrix units are busy 42% of the time (counters, 514 queries): one
+// wavefront per SIMD issues everything in order, since queries and outputs fill its registers, and what it waits for
+// adds up, none of it large: 16-byte LDS writes (52 cycles for the four wavefronts' one), transposed reads, the
+// barrier and the probabilities between the two products. Leaving any one of these out saved 1 to 14%.
+// Measured at 64 heads: 4096 queries over 512 listed rows 381 us (0.72 PFLOP/s; a block's query, first rows and output
+// take 11 of its 24 us), 514 over about 14600 rows 984 us (0.97), 8 over about 115000 rows 152 us (0.79).
+// Measured and not taken: rows kept as codes in LDS and widened twice (a step 20% slower), eight wavefronts of 256
+// registers (spills, three times slower), two blocks of 32 heads per compute unit (equal), blocks that take
+// several queries (+10%), the probabilities under the next step's first product (+5%), stores past the cache (equal).
 #include <type_traits>
 
 #include "operators.h"
@@ -113,26 +124,35 @@ __device__ __forceinline__ int32_t row_of(const AttendArgs& a, const Entries& e,
     return there ? (int32_t)r : -1;
 }
 
-// One lane's share of a cache row: lane group g (of 4) holds, for j = 0 .. 3, values 128j + 32g ..
-// 128j + 32g + 31: sixteen code bytes and two scales. The four groups read 64 consecutive bytes.
+// One lane's share of a cache row: lane group g (of 4) holds values 128g .. 128g + 127, 64 code bytes (read 16 at a
+// time) and eight scales. (The products take the values in any order that queries and rows share. A read of 16 bytes
+// by every lane touches 64 places and holds the address unit for as many cycles; with 32 values of each 128 per
+// lane group, the scales took four reads and the address unit bounded the weights' kernel.)
 typedef uint32_t u32_by2 __attribute__((aligned(2)));  // scales lie at any even address
 struct RowPart {
     uint4 code[4];
-    uint32_t scale[4];  // four scales; the lane's two are the low or (odd g) the high half
+    uint32_t scale[2];
 };
 
-// chunk j of a row; a row that is not there counts as zeros (codes are always finite)
+// chunk j of a row and the scales; a row that is not there counts as zeros (codes are always finite)
 __device__ __forceinline__ void load_chunk(const AttendArgs& a, int32_t row, int g, int j, RowPart& r) {
     const int64_t at = row < 0 ? 0 : row;
-    r.code[j] = *reinterpret_cast<const uint4*>(a.codes + at * 256 + g * 16 + 64 * j);
-    r.scale[j] = *reinterpret_cast<const u32_by2*>(a.scales + at * 32 + (g >> 1) * 4 + 8 * j);
+    r.code[j] = *reinterpret_cast<const uint4*>(a.codes + at * 256 + g * 64 + 16 * j);
+}
+__device__ __forceinline__ void load_scales(const AttendArgs& a, int32_t row, int g, uint32_t (&scale)[2]) {
+    const u32_by2* at = reinterpret_cast<const u32_by2*>(a.scales + (int64_t)(row < 0 ? 0 : row) * 32 + g * 8);
+    scale[0] = at[0];
+    scale[1] = at[1];
 }
 
-// values 8u .. 8u+7 of chunk j as fp16 (exact); there: the row is in the cache
-__device__ __forceinline__ h8 values8(const RowPart& r, int j, int u, int g, bool there) {
-    const uint32_t w = u == 0 ? r.code[j].x : u == 1 ? r.code[j].y : u == 2 ? r.code[j].z : r.code[j].w;
-    const h2 sp = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(there ? (int)(r.scale[j] >> (16 * (g & 1))) : 0, 1.0f, false);
-    const _Float16 s1 = u < 2 ? sp[0] : sp[1];
+// values 8x .. 8x + 7 of the part as fp16 (exact); there: the row is in the cache
+__device__ __forceinline__ h8 values8(const RowPart& r, int x, bool there) {
+    const uint4 c = r.code[x >> 2];
+    const uint32_t w = (x & 3) == 0 ? c.x : (x & 3) == 1 ? c.y : (x & 3) == 2 ? c.z : c.w;
+    const int e = there ? (int)r.scale[x >> 3] : 0;
+    const h2 sp = (x >> 2) & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(e, 1.0f, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(e, 1.0f, false);
+    const _Float16 s1 = (x & 2) == 0 ? sp[0] : sp[1];
     const h2 s = {s1, s1};
     const h2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s;
     const h2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s;
@@ -246,6 +266,7 @@ struct Shared {
 // the position of the one after that.
 struct Feed {
     RowPart kv;
+    uint32_t scale1[2];      // one step on
     int32_t row;             // of the step whose rows kv holds
     int32_t pos1, page1;     // one step on
     int32_t pos2;            // two steps on
@@ -284,16 +305,17 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
         fd.row = row_of<PAGED>(a, e, p, page);
 #pragma unroll
         for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
+        load_scales(a, fd.row, g, fd.kv.scale);
     }
     stage_query<kHeads>(a, h0, qr, sh.kv, sh.fr);
     __syncthreads();
     h8 q[NH][15];
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-        const _Float16* at = sh.kv + (n * 16 + c) * kRow + g * 32;
+        const _Float16* at = sh.kv + (n * 16 + c) * kRow + g * 128;
 #pragma unroll
-        for (int x = 0; x < 15; ++x) q[n][x] = *reinterpret_cast<const h8*>(at + (x >> 2) * 128 + (x & 3) * 8);
-        const h8 ql = *reinterpret_cast<const h8*>(at + 3 * 128 + 3 * 8);
+        for (int x = 0; x < 15; ++x) q[n][x] = *reinterpret_cast<const h8*>(at + x * 8);
+        const h8 ql = *reinterpret_cast<const h8*>(at + 15 * 8);
         if (w == 0) *reinterpret_cast<h8*>(sh.q + (n * 16 + c) * kQRow + g * 8) = ql;
         // in the accumulation half of the register file: matrix operands only
 #pragma unroll
@@ -318,7 +340,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     // p ^ (2 (row % 4) + row / 4 % 2). Eight rows' same pieces (a write), and four rows' same pairs of pieces (a
     // transposed read), then lie in different banks. Addresses of other pieces, of rows 4 on and of the other buffer
     // differ from these in single bits.
-    const int at_in = (w * 16 + c) * kD + ((g * 4) ^ ((c & 3) * 2 + ((c >> 2) & 1))) * 8;
+    const int at_in = (w * 16 + c) * kD + g * 128 + ((c & 3) * 2 + ((c >> 2) & 1)) * 8;
     const int first = kWide ? (g & 1) * 2 + ((c >> 1) & 1) : (c >> 1) & 1;  // piece
     const int at_out = (og * 8 + (c >> 2)) * kD + w * 128 + (first ^ ((c >> 2) * 2)) * 8 + (c & 1) * 4;
     // Probabilities 2^(s2 - R) of sixteen heads' products s into p[step & 1]; true if a logit lies too far above R.
@@ -422,7 +444,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             fd.pos1 = fd.pos2;
             fd.page1 = page_of<PAGED>(a, e, fd.pos2);
             fd.pos2 = position_of<LIST>(e, i0 + (i + 4) * kTile, end);
-            k = values8(fd.kv, 0, 0, g, there);
+            k = values8(fd.kv, 0, there);
         }
         if constexpr (kPv) {
             if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
@@ -464,8 +486,9 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
             }
             if constexpr (kQk) {
                 const h8 kx = k;
-                *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 3) * 8)) + (x >> 2) * 128) = kx;
-                if (x < 15) k = values8(fd.kv, (x + 1) >> 2, (x + 1) & 3, g, there);
+                *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 7) * 8)) + (x >> 3) * 64) = kx;
+                if (x < 15) k = values8(fd.kv, x + 1, there);
+                if (x == 3) load_scales(a, row1, g, fd.scale1);
                 if ((x & 3) == 3) load_chunk(a, row1, g, x >> 2, fd.kv);
 #pragma unroll
                 for (int n = 0; n < NH; ++n) {
@@ -495,6 +518,8 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
                 }
             }
             fd.row = row1;
+            fd.kv.scale[0] = fd.scale1[0];
+            fd.kv.scale[1] = fd.scale1[1];
             bool over = false;
             if constexpr (!kPv) {
                 // the first step sets R
@@ -670,7 +695,8 @@ __global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a
 // The first product alone, with heads as rows: a lane's column is one entry, whose terms it adds up over the heads.
 // Each wavefront takes 16 entries per step by itself (no barrier); the exponentials of a step run under the matrix
 // instructions of the next. Heads beyond the block's 16 NH are further rounds over the same entries, added by the lane
-// that wrote them.
+// that wrote them. 1021 queries of 64 heads over about 3600 rows: 225 us (0.95 PFLOP/s), 0.8 us a step, of which the
+// matrix instructions are 0.43; without reading the rows 0.68.
 template <int NH, bool LIST, bool PAGED>
 __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,
                                                                 float* __restrict__ weights, int64_t w_stride,
@@ -713,6 +739,7 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
             fd.row = row_of<PAGED>(a, e, p, page);
 #pragma unroll
             for (int j = 0; j < 4; ++j) load_chunk(a, fd.row, g, j, fd.kv);
+            load_scales(a, fd.row, g, fd.kv.scale);
         }
         if (h0) __syncthreads();
         stage_query<kHeads>(a, h0, qr, s_q, s_factor);
@@ -723,7 +750,7 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
         for (int n = 0; n < NH; ++n) {
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-                q[n][x] = *reinterpret_cast<const h8*>(s_q + (n * 16 + c) * kRow + (x >> 2) * 128 + g * 32 + (x & 3) * 8);
+                q[n][x] = *reinterpret_cast<const h8*>(s_q + (n * 16 + c) * kRow + g * 128 + x * 8);
 #pragma unroll
             for (int x = 0; x < 16; ++x) asm volatile("" : "+a"(q[n][x]));
 #pragma unroll
@@ -752,13 +779,14 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
             fd.page1 = page_of<PAGED>(a, e, fd.pos2);
             fd.pos2 = position_of<LIST>(e, i0 + (step + 3) * kTile, end);
             float sum = 0.0f;
-            h8 k = values8(fd.kv, 0, 0, g, there);
+            h8 k = values8(fd.kv, 0, there);
 #pragma unroll
             for (int n = 0; n < NH; ++n) s[n] = v4f{};
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
                 const h8 kx = k;
-                if (x < 15) k = values8(fd.kv, (x + 1) >> 2, (x + 1) & 3, g, there);
+                if (x < 15) k = values8(fd.kv, x + 1, there);
+                if (x == 3) load_scales(a, row1, g, fd.scale1);
                 if ((x & 3) == 3) load_chunk(a, row1, g, x >> 2, fd.kv);
                 if (!kFirst && x < 4 * NH)
                     sum += __builtin_amdgcn_exp2f(__builtin_fmaf(last[x >> 2][x & 3], f[x >> 2][x & 3], off[x >> 2][x & 3]));
@@ -775,6 +803,8 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
             for (int n = 0; n < NH; ++n) last[n] = s[n];
             last_row = fd.row;
             fd.row = row1;
+            fd.kv.scale[0] = fd.scale1[0];
+            fd.kv.scale[1] = fd.scale1[1];
         };
         turn(std::true_type{}, 0);
         for (int step = 1; step < steps; ++step) turn(std::false_type{}, step);
@@ -793,8 +823,8 @@ namespace {
 
 // How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
 // units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
-// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.7 and 13 at 64
-// heads, 1.17 and 9 at 32, 1.14 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
+// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.65 and 13 at 64
+// heads, 1.16 and 9 at 32, 1.1 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
 struct Cut {
     int nh, splits;
 };
@@ -802,7 +832,7 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
     static constexpr struct {
         int nh;
         float step, block;
-    } kTiles[] = {{4, 1.7f, 13.0f}, {2, 1.17f, 9.0f}, {1, 1.14f, 7.0f}};
+    } kTiles[] = {{4, 1.65f, 13.0f}, {2, 1.16f, 9.0f}, {1, 1.1f, 7.0f}};
     const int64_t steps = entries > kTile ? (entries + kTile - 1) / kTile : 1;
     Cut best{1, 1};
     float least = 0.0f;
@@ -818,6 +848,24 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
                 least = time;
                 best = Cut{t.nh, (int)s};
             }
+        }
+    }
+    return best;
+}
+
+// Parts of a query's entries in the weights' kernel, in the same way. Measured per step and per block apart from its
+// steps, in microseconds: 0.8 and 7.5 at 64 heads, 0.55 and 3.2 at 32, 0.5 and 2.6 at 16 (1024 queries over 64 .. 4096
+// rows).
+int weights_parts(int32_t nq, int32_t heads, int64_t steps) {
+    const float step = heads > 32 ? 0.8f : heads > 16 ? 0.55f : 0.5f, block = heads > 32 ? 7.5f : heads > 16 ? 3.2f : 2.6f;
+    int best = 1;
+    float least = 0.0f;
+    for (int64_t s = 1; s <= steps; ++s) {
+        if (s > 1 && nq * s > 8 * 256 + nq) break;  // rounds are even enough
+        const float time = (float)((nq * s + 255) / 256) * ((float)((steps + s - 1) / s) * step + block);
+        if (least == 0.0f || time < least) {
+            least = time;
+            best = (int)s;
         }
     }
     return best;
@@ -891,11 +939,7 @@ hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights,
     const int64_t entries = a.idx ? a.k : a.max_n;
     if (entries == 0) return hipSuccess;
     set_page_division(a);
-    // a block for each of the 256 compute units, four times over where a query's entries are many; at least one step of
-    // 64 entries each
-    const int64_t steps = (entries + kTile - 1) / kTile;
-    const int64_t want = steps >= 32 ? (1024 + a.nq - 1) / a.nq : (256 + a.nq - 1) / a.nq;
-    const int splits = (int)(want < steps ? want : steps);
+    const int splits = weights_parts(a.nq, a.heads, (entries + kTile - 1) / kTile);
     by_entries(a, [&](auto list, auto paged) {
         constexpr bool L = decltype(list)::value, P = decltype(paged)::value;
         const dim3 grid((uint32_t)a.nq * splits);
