@@ -308,11 +308,11 @@ def idx_topk_pool(scores, n_vis, max_n: int, pool_blocks, pool_count, max_blocks
     return out_idx, out_val
 
 
-def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
-    """Address of a contiguous argument of this type and shape (its place is checked by _same_gpu)."""
+def _arg(t: torch.Tensor, dtype: torch.dtype, shape: tuple | None, name: str) -> int:
+    """Address of a contiguous argument of this type and shape (None: any; its place is checked by _same_gpu)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -323,21 +323,23 @@ def _rows_arg(t: torch.Tensor, dtype: torch.dtype, rows: int, width: int, name: 
     """(address, row stride) of a 2-D argument of at least `width` columns, each row contiguous."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < width:
-        raise ValueError(f"{name} must be [{rows}, >= {width}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < width:
+        raise ValueError(f"{name} must be [{rows}, >= {width}], got {tuple(shape)}")
     stride, one = t.stride()
-    if one != 1 and t.shape[1] > 1:
+    columns = shape[1]
+    if one != 1 and columns > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), stride if rows > 1 else max(stride, t.shape[1])
+    return t.data_ptr(), stride if rows > 1 else max(stride, columns)
 
 
 def _same_gpu(*tensors) -> None:
     """The arguments lie together on the current device (the library launches there)."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"fp4idx tensors must live on one GPU, got {tensors[0].device} and {t.device}")
-    if dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"fp4idx tensors must live on the current GPU, got {tensors[0].device}")
 
 
@@ -391,15 +393,16 @@ def idx_rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, offset: int
 
 def _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx) -> tuple:
     """Checks shared by the attention calls: the arguments from q to n_vis, and those of the list."""
-    if q.dim() != 3 or q.shape[2] != MKV_DIM:
-        raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(q.shape)}")
-    nq, heads, _ = q.shape
-    rows = codes.numel() // (MKV_DIM // 2)
-    if codes.numel() != rows * (MKV_DIM // 2) or scales.numel() != rows * (MKV_DIM // 16):
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != MKV_DIM:
+        raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(shape)}")
+    nq, heads, _ = shape
+    rows, rest = divmod(codes.numel(), MKV_DIM // 2)
+    if rest or scales.numel() != rows * (MKV_DIM // 16):
         raise ValueError("codes and scales must hold 256 and 32 bytes for each cache row")
-    q_ptr = _arg(q, torch.bfloat16, q.shape, "q")
-    codes_ptr = _arg(codes, torch.uint8, codes.shape, "codes")
-    scales_ptr = _arg(scales, torch.uint8, scales.shape, "scales")
+    q_ptr = _arg(q, torch.bfloat16, None, "q")
+    codes_ptr = _arg(codes, torch.uint8, None, "codes")
+    scales_ptr = _arg(scales, torch.uint8, None, "scales")
     nv_ptr = _arg(n_vis, torch.int32, (nq,), "n_vis")
     base_ptr = pages_ptr = seq_ptr = idx_ptr = None
     pages_stride = nseq = idx_stride = k = 0
@@ -429,7 +432,7 @@ def idx_attend(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=N
     where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx)
     out_ptr = _arg(out, torch.bfloat16, q.shape, "out")
     lse_ptr = None if lse is None else _arg(lse, torch.float32, q.shape[:2], "lse")
-    ws_ptr = _arg(ws, torch.uint8, ws.shape, "ws")
+    ws_ptr = _arg(ws, torch.uint8, None, "ws")
     _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, idx, out, lse, ws)
     _call(lib.idx_attend, *where, max_n, window, *lst, scale, out_ptr, lse_ptr, ws_ptr, ws.numel(), _stream(stream))
     return out, lse
@@ -468,7 +471,7 @@ def idx_distill(scores, n_vis, max_n: int, t_idx, t_logit, loss, lse, t_lse, ws,
     rows = _distill_rows(scores, n_vis, max_n, t_idx, t_logit)
     each = (rows[3],)
     outs = (_arg(loss, torch.float32, each, "loss"), _arg(lse, torch.float32, each, "lse"),
-            _arg(t_lse, torch.float32, each, "t_lse"), _arg(ws, torch.uint8, ws.shape, "ws"))
+            _arg(t_lse, torch.float32, each, "t_lse"), _arg(ws, torch.uint8, None, "ws"))
     _same_gpu(scores, n_vis, t_idx, t_logit, loss, lse, t_lse, ws)
     _call(lib.idx_distill, *rows, inv_temp, *outs, ws.numel(), _stream(stream))
     return loss
