@@ -315,3 +315,50 @@ def test_results_do_not_depend_on_the_batch_stride_or_stream(fx):
     fx.idx_attend(q[1:2], codes, scales, nv[1:2], 3000, SCALE, one, fx.workspace(fx.IDX_OP_ATTEND, 1, 512, 64),
                   kv_base=base[1:2], idx=idx[1:2])
     assert (one[0].float() - a[0][1].float()).abs().max() <= 2.0 ** -7 * a[0][1].float().abs().max()
+
+
+def test_scales_at_an_even_address(fx):
+    rng = np.random.default_rng(15)
+    part = cache(rng, 700)
+    codes = dev(part[0])
+    room = torch.full((700 * 32 + 6,), 0x7F, dtype=torch.uint8, device="cuda")  # NaN scales around
+    q, _ = bf16(rng.standard_normal((3, 40, 512)) * 2)
+    nv, base = dev([700, 333, 64], np.int32), dev([0, 0, 0], np.int64)
+    idx = dev(np.stack([rng.permutation(700)[:90] for _ in range(3)]), np.int32)
+    ws = fx.workspace(fx.IDX_OP_ATTEND, 3, 700, 40)
+    got = []
+    for off in (0, 2, 4, 6):
+        room.fill_(0x7F)
+        scales = room[off:off + 700 * 32].view(700, 32)
+        scales.copy_(dev(part[1]))
+        for lst in (None, idx):
+            out, lse = torch.empty_like(q), torch.empty(3, 40, device="cuda")
+            fx.idx_attend(q, codes, scales, nv, 700, SCALE, out, ws, lse=lse, kv_base=base, idx=lst)
+            w = torch.zeros(3, 700 if lst is None else 90, device="cuda")
+            fx.idx_attend_weights(q, codes, scales, nv, 700, SCALE, lse, w, kv_base=base, idx=lst)
+            got.append((out, lse, w))
+    for i, x in enumerate(got):
+        assert all(torch.equal(a, b) and not b.isnan().any() for a, b in zip(got[i % 2], x)), i
+
+
+def test_two_calls_at_once(fx):
+    """on two streams, with workspaces of their own, both in parts that are joined"""
+    rng = np.random.default_rng(16)
+    codes, scales = (dev(x) for x in cache(rng, 30000))
+    q, _ = bf16(rng.standard_normal((2, 2, 64, 512)) * 2)
+    nv, base = dev([30000, 29000], np.int32), dev([0, 0], np.int64)
+    ws = [fx.workspace(fx.IDX_OP_ATTEND, 2, 30000, 64) for _ in range(2)]
+    assert ws[0].numel() > 16
+    want = [torch.empty_like(q[0]) for _ in range(2)]
+    for i in range(2):
+        fx.idx_attend(q[i], codes, scales, nv, 30000, SCALE, want[i], ws[i], kv_base=base)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = [[torch.empty_like(q[0]) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for rep in range(20):
+        for i in range(2):
+            fx.idx_attend(q[i], codes, scales, nv, 30000, SCALE, out[i][rep], ws[i], kv_base=base, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in out[i])
