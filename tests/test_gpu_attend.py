@@ -257,6 +257,24 @@ def test_one_token_over_a_long_range(fx):
     check(fx, rng.standard_normal((2, 3, 512)) * 4, codes, scales, [20011, 19000], 20011, kv_base=[0, 500])
 
 
+@pytest.mark.parametrize("nq,heads,n", [(300, 2, 1000), (300, 40, 4096), (200, 16, 9000), (300, 20, 6000), (90, 64, 12000)])
+def test_queries_in_unequal_numbers_of_parts(fx, nq, heads, n):
+    """sizes at which some queries are cut into one part more than others (one and two, two and three, five and six):
+    a few of full length on both sides of the change, the others short or empty"""
+    rng = np.random.default_rng(17)
+    codes, scales = cache(rng, n + 50)
+    nv = rng.integers(0, 90, nq)
+    for t in (0, 1, nq // 4, nq // 3, nq // 2, nq - 2, nq - 1):
+        nv[t] = rng.integers(n - 100, n + 1)
+    nv[2] = 0
+    q = rng.standard_normal((nq, heads, 512)) * 2
+    base = rng.integers(0, 50, nq)
+    check(fx, q, codes, scales, nv, n, kv_base=base)
+    if n <= 1000:
+        idx = rng.integers(-1, n, (nq, n))
+        check(fx, q, codes, scales, nv, n, kv_base=base, idx=idx)
+
+
 def test_a_cache_beyond_32_bit_offsets(fx):
     rng = np.random.default_rng(13)
     rows = (1 << 24) + 1000  # 4.3 GB of codes

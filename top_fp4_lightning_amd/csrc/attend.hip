@@ -24,7 +24,7 @@
 // adds up, none of it large: 16-byte LDS writes (52 cycles for the four wavefronts' one), transposed reads, the
 // barrier and the probabilities between the two products. Leaving any one of these out saved 1 to 14%.
 // Measured at 64 heads: 4096 queries over 512 listed rows 381 us (0.72 PFLOP/s; a block's query, first rows and output
-// take 11 of its 24 us), 514 over about 14600 rows 984 us (0.97), 8 over about 115000 rows 152 us (0.79).
+// take 11 of its 24 us), 514 over about 14600 rows 924 us (1.04), 8 over about 115000 rows 152 us (0.79).
 // Measured and not taken: rows kept as codes in LDS and widened twice (a step 20% slower), eight wavefronts of 256
 // registers (spills, three times slower), two blocks of 32 heads per compute unit (equal), blocks that take
 // several queries (+10%), the probabilities under the next step's first product (+5%), stores past the cache (equal).
@@ -241,6 +241,24 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int h0, QueryRo
     }
 }
 
+// How a call's queries are cut: those below `whole` into `parts` parts of their entries, the others into one more, so
+// that units (a part of a query each) come in whole rounds over the compute units; the longer ones come first. 514
+// queries over 16384 rows: 1005 us in 3 parts each (6.02 rounds), 924 us in 2 or 3 (1280 units).
+struct Place {
+    uint32_t t, part, parts;
+};
+struct Cut {
+    int nh;  // head sixteens of a block
+    uint32_t parts, whole;
+    __host__ __device__ uint32_t units(uint32_t nq) const { return nq * parts + (nq - whole); }
+    __device__ uint32_t parts_of(uint32_t t) const { return parts + (t >= whole); }
+    __device__ uint32_t first_of(uint32_t t) const { return t * parts + (t >= whole ? t - whole : 0); }
+    __device__ Place place(uint32_t unit) const {
+        const uint32_t longer = whole * parts, by = parts + (unit >= longer), rest = unit >= longer ? unit - longer : unit;
+        return Place{(unit >= longer ? whole : 0) + rest / by, rest % by, by};
+    }
+};
+
 // block -> (query and part, head tile): the head tiles of one query run on one XCD (blocks b and
 // b + 8 do), so the second reads the rows from that XCD's L2
 __device__ __forceinline__ bool unit_of(uint32_t b, uint32_t units, uint32_t tiles, uint32_t& unit, uint32_t& tile) {
@@ -273,7 +291,7 @@ struct Feed {
 };
 
 template <int NH, bool LIST, bool PAGED>
-__global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int splits) {
+__global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, Cut cut) {
     __shared__ __align__(16) Shared<NH> sh;
     constexpr int kHeads = NH * 16;
     const int lane = threadIdx.x & 63;
@@ -281,9 +299,10 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
     const int g = lane >> 4, c = lane & 15;
     const uint32_t head_tiles = (a.heads + kHeads - 1) / kHeads;
     uint32_t unit, tile;
-    if (!unit_of(blockIdx.x, (uint32_t)a.nq * splits, head_tiles, unit, tile)) return;
-    const int64_t t = unit / splits;
-    const int part = (int)(unit % splits);
+    if (!unit_of(blockIdx.x, cut.units((uint32_t)a.nq), head_tiles, unit, tile)) return;
+    const Place at_cut = cut.place(unit);
+    const int64_t t = at_cut.t;
+    const int part = (int)at_cut.part, splits = (int)at_cut.parts;
     const int h0 = (int)tile * kHeads;
     const Entries e = entries_of(a, t);
     const int steps_all = (e.count + kTile - 1) / kTile;
@@ -623,13 +642,14 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, int 
 // Join of the parts of one (query, head): o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i. 128 threads take 4 values
 // each; with many parts, G groups of them take every G-th.
 template <int G>
-__global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a, int splits) {
+__global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a, Cut cut, int t0) {
     __shared__ float s_f[kMostParts];
     __shared__ float2 s_wave[2 * G];
     __shared__ __align__(16) v4f s_o[G > 1 ? (G - 1) * 128 : 1];
-    const int64_t t = blockIdx.x / a.heads;
-    const int h = (int)(blockIdx.x % a.heads);
-    const int64_t first = t * splits * a.heads + h;
+    const uint32_t t = t0 + blockIdx.x / a.heads;
+    const int h = (int)(blockIdx.x % a.heads), splits = (int)cut.parts_of(t);
+    const int64_t first = (int64_t)cut.first_of(t) * a.heads + h;
+    const int64_t pair = (int64_t)t * a.heads + h;
     const int64_t step = a.heads;
     // references and sums: a part per thread
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
@@ -685,9 +705,8 @@ __global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a
         for (int k = 0; k < G - 1; ++k) o += s_o[k * 128 + at];
     }
     o *= L == 0.0f ? 0.0f : 1.0f / L;
-    *reinterpret_cast<uint2*>(a.out + (int64_t)blockIdx.x * kD + at * 4) =
-        uint2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-    if (a.lse && at == 0) a.lse[blockIdx.x] = L == 0.0f ? ninf() : (R + __builtin_amdgcn_logf(L)) * kLn2;
+    *reinterpret_cast<uint2*>(a.out + pair * kD + at * 4) = uint2{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+    if (a.lse && at == 0) a.lse[pair] = L == 0.0f ? ninf() : (R + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 // The attention's probability of every entry, mean over the heads, from the saved lse:
@@ -825,32 +844,66 @@ namespace {
 // units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
 // even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.65 and 13 at 64
 // heads, 1.16 and 9 at 32, 1.1 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
-struct Cut {
-    int nh, splits;
-};
-Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
+// Time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first unit that is free.
+float time_of(int64_t n1, float t1, int64_t n2, float t2) {
+    const int64_t rest = n1 % 256;
+    const float before = (float)(n1 / 256) * t1;
+    if (n2 == 0) return before + (rest ? t1 : 0.0f);
+    if (rest == 0) return before + (float)((n2 + 255) / 256) * t2;
+    // `rest` units end their long block at t1; the others take short ones from the start
+    for (int64_t j = 0;; ++j) {
+        const float end = t1 + (float)j * t2;
+        const int64_t k = (int64_t)(end / t2);
+        if (k * (256 - rest) + j * rest < n2) continue;
+        const float sooner = (float)k * t2;  // without the j-th of the late units?
+        const bool enough = j > 0 && sooner >= t1 && k * (256 - rest) + (j - 1) * rest >= n2;
+        return before + (enough ? sooner : end);
+    }
+}
+Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
     static constexpr struct {
         int nh;
         float step, block;
     } kTiles[] = {{4, 1.65f, 13.0f}, {2, 1.16f, 9.0f}, {1, 1.1f, 7.0f}};
     const int64_t steps = entries > kTile ? (entries + kTile - 1) / kTile : 1;
-    Cut best{1, 1};
+    Cut best{1, 1, (uint32_t)nq};
     float least = 0.0f;
     for (const auto& t : kTiles) {
         if (t.nh > 1 && heads <= 8 * t.nh) continue;  // half of the tile would be empty
-        const int64_t blocks = (int64_t)nq * ((heads + 16 * t.nh - 1) / (16 * t.nh));
-        for (int64_t s = 1; s <= steps && s <= kMostParts; ++s) {
-            if (s > 1 && blocks * s > 8 * 256 + blocks) break;  // rounds are even enough
-            const float rounds = (float)((blocks * s + 255) / 256);
-            const float time = rounds * ((float)((steps + s - 1) / s) * t.step + t.block) +
-                               (s > 1 ? 4.0f + 1e-3f * (float)nq * heads * s : 0.0f);
+        const int64_t tiles = (heads + 16 * t.nh - 1) / (16 * t.nh);
+        const auto one = [&](int64_t parts) { return (float)((steps + parts - 1) / parts) * t.step + t.block; };
+        const auto consider = [&](int64_t parts, int64_t whole) {
+            const int64_t n1 = whole * parts, n2 = (nq - whole) * (parts + 1), joined = parts > 1 ? n1 + n2 : n2;
+            const float time = time_of(n1 * tiles, one(parts), n2 * tiles, one(parts + 1)) +
+                               (joined ? 4.0f + 1e-3f * (float)heads * (float)joined : 0.0f);
             if (least == 0.0f || time < least) {
                 least = time;
-                best = Cut{t.nh, (int)s};
+                best = Cut{t.nh, (uint32_t)parts, (uint32_t)whole};
             }
+        };
+        for (int64_t s = 1; s <= steps && s <= kMostParts; ++s) {
+            if (s > 1 && nq * tiles * s > 8 * 256 + nq * tiles) break;  // rounds are even enough
+            consider(s, nq);
+        }
+        for (int64_t rounds = 1; rounds <= 8; ++rounds) {  // units for whole rounds
+            const int64_t units = rounds * 256 / tiles, parts = units / nq;
+            if (parts >= 1 && parts < steps && parts < kMostParts && units % nq) consider(parts, nq * (parts + 1) - units);
         }
     }
     return best;
+}
+
+// the same for the sizes asked for last (a call asks twice, for its workspace and for its launch)
+Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
+    thread_local int64_t of[3] = {0, 0, 0};
+    thread_local Cut cut{};
+    if (of[0] != nq || of[1] != heads || of[2] != entries) {
+        cut = best_cut(nq, heads, entries);
+        of[0] = nq;
+        of[1] = heads;
+        of[2] = entries;
+    }
+    return cut;
 }
 
 // Parts of a query's entries in the weights' kernel, in the same way. Measured per step and per block apart from its
@@ -893,11 +946,11 @@ void by_entries(const AttendArgs& a, F&& launch) {
 }
 
 template <int NH>
-void launch_attend_as(const AttendArgs& a, int splits, hipStream_t stream) {
-    const uint32_t units = (uint32_t)a.nq * splits, head_tiles = (a.heads + 16 * NH - 1) / (16 * NH);
+void launch_attend_as(const AttendArgs& a, const Cut& cut, hipStream_t stream) {
+    const uint32_t units = cut.units((uint32_t)a.nq), head_tiles = (a.heads + 16 * NH - 1) / (16 * NH);
     by_entries(a, [&](auto list, auto paged) {
         hipLaunchKernelGGL((attend_kernel<NH, decltype(list)::value, decltype(paged)::value>),
-                           dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, splits);
+                           dim3((units + 7) / 8 * 8 * head_tiles), dim3(256), 0, stream, a, cut);
     });
 }
 
@@ -905,32 +958,36 @@ void launch_attend_as(const AttendArgs& a, int splits, hipStream_t stream) {
 
 size_t attend_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
     if (nq <= 0 || entries <= 0) return 16;
-    const int splits = cut_of(nq, heads, entries).splits;
-    return splits <= 1 ? 16 : (size_t)nq * splits * heads * (kD + 2) * sizeof(float);
+    const Cut cut = cut_of(nq, heads, entries);
+    const size_t units = cut.units((uint32_t)nq);
+    return units == (size_t)nq ? 16 : units * heads * (kD + 2) * sizeof(float);
 }
 
 hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream) {
     const int64_t entries = a.idx ? a.k : (a.window > 0 && a.window < a.max_n ? a.window : a.max_n);
     const Cut cut = cut_of(a.nq, a.heads, entries);
     set_page_division(a);
-    if (cut.splits > 1) {
+    const uint32_t units = cut.units((uint32_t)a.nq);
+    if (units > (uint32_t)a.nq) {
         a.part_o = (float*)ws;
-        a.part_ml = a.part_o + (size_t)a.nq * cut.splits * a.heads * kD;
+        a.part_ml = a.part_o + (size_t)units * a.heads * kD;
     }
     if (cut.nh == 4)
-        launch_attend_as<4>(a, cut.splits, stream);
+        launch_attend_as<4>(a, cut, stream);
     else if (cut.nh == 2)
-        launch_attend_as<2>(a, cut.splits, stream);
+        launch_attend_as<2>(a, cut, stream);
     else
-        launch_attend_as<1>(a, cut.splits, stream);
+        launch_attend_as<1>(a, cut, stream);
     hipError_t err = hipGetLastError();
-    if (err != hipSuccess || cut.splits <= 1) return err;
+    if (err != hipSuccess || units == (uint32_t)a.nq) return err;
+    // queries in one part are done
+    const int t0 = cut.parts > 1 ? 0 : (int)cut.whole;
     // (four groups: 17 -> 8 us for 512 pairs of 32 parts; one: 35 us for 33000 pairs of 3, bound by HBM)
-    const dim3 pairs((uint32_t)a.nq * a.heads);
-    if (cut.splits >= 8)
-        hipLaunchKernelGGL(attend_join_kernel<4>, pairs, dim3(512), 0, stream, a, cut.splits);
+    const dim3 pairs((uint32_t)(a.nq - t0) * a.heads);
+    if (cut.parts >= 8)
+        hipLaunchKernelGGL(attend_join_kernel<4>, pairs, dim3(512), 0, stream, a, cut, t0);
     else
-        hipLaunchKernelGGL(attend_join_kernel<1>, pairs, dim3(128), 0, stream, a, cut.splits);
+        hipLaunchKernelGGL(attend_join_kernel<1>, pairs, dim3(128), 0, stream, a, cut, t0);
     return hipGetLastError();
 }
 
