@@ -840,10 +840,6 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
 
 namespace {
 
-// How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
-// units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
-// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.65 and 13 at 64
-// heads, 1.16 and 9 at 32, 1.1 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
 // Time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first unit that is free.
 float time_of(int64_t n1, float t1, int64_t n2, float t2) {
     const int64_t rest = n1 % 256;
@@ -855,11 +851,15 @@ float time_of(int64_t n1, float t1, int64_t n2, float t2) {
         const float end = t1 + (float)j * t2;
         const int64_t k = (int64_t)(end / t2);
         if (k * (256 - rest) + j * rest < n2) continue;
-        const float sooner = (float)k * t2;  // without the j-th of the late units?
+        const float sooner = (float)k * t2;  // the free units' last one ends before the late ones' j-th
         const bool enough = j > 0 && sooner >= t1 && k * (256 - rest) + (j - 1) * rest >= n2;
         return before + (enough ? sooner : end);
     }
 }
+// How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
+// units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
+// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.65 and 13 at 64
+// heads, 1.16 and 9 at 32, 1.1 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
 Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
     static constexpr struct {
         int nh;
