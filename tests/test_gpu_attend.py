@@ -257,7 +257,8 @@ def test_one_token_over_a_long_range(fx):
     check(fx, rng.standard_normal((2, 3, 512)) * 4, codes, scales, [20011, 19000], 20011, kv_base=[0, 500])
 
 
-@pytest.mark.parametrize("nq,heads,n", [(300, 2, 1000), (300, 40, 4096), (200, 16, 9000), (300, 20, 6000), (90, 64, 12000)])
+@pytest.mark.parametrize("nq,heads,n", [(300, 2, 1000), (300, 40, 4096), (200, 16, 9000), (300, 20, 6000), (90, 64, 12000),
+                                        (600, 5, 3000), (700, 16, 2000)])
 def test_queries_in_unequal_numbers_of_parts(fx, nq, heads, n):
     """sizes at which some queries are cut into one part more than others (one and two, two and three, five and six):
     a few of full length on both sides of the change, the others short or empty"""

@@ -268,10 +268,16 @@ __device__ __forceinline__ bool unit_of(uint32_t b, uint32_t units, uint32_t til
     return unit < units;
 }
 
+// Blocks of 16 heads come in pairs on a compute unit: half its registers each, and one step's rows in LDS, so the two
+// products of a block take turns and the blocks cover each other's waits. 8000 queries of one head over 64 rows: 163 ->
+// 87 us, 8000 of 16 heads over 512 rows 424 -> 274; one block by itself is as fast either way.
+template <int NH>
+constexpr bool kPair = NH == 1;
+
 // NH: heads of a block in sixteens
 template <int NH>
 struct Shared {
-    _Float16 kv[2 * kTile * kD];       // two steps' rows; the queries and the outputs on their ways
+    _Float16 kv[(kPair<NH> ? 1 : 2) * kTile * kD];  // a step's or two steps' rows; queries and outputs on their ways
     _Float16 p[2][NH * 16 * kPRow];
     float m[NH * 16][4];
     float l[NH * 16][4];
@@ -291,7 +297,7 @@ struct Feed {
 };
 
 template <int NH, bool LIST, bool PAGED>
-__global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, Cut cut) {
+__global__ __launch_bounds__(256, kPair<NH> ? 2 : 1) void attend_kernel(const AttendArgs a, Cut cut) {
     __shared__ __align__(16) Shared<NH> sh;
     constexpr int kHeads = NH * 16;
     const int lane = threadIdx.x & 63;
@@ -426,10 +432,11 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, Cut 
     // Turn i of the pipe, after a barrier: the first product of step i + 1 and the second product of step i, then the
     // probabilities of step i + 1 under the rest of the second product. Widening, exponentials, LDS and loads run
     // under the matrix instructions: one takes 16 cycles, four times another instruction.
-    const auto turn = [&](auto pv, auto qk, int i) {
-        constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value;
+    const auto turn = [&](auto pv, auto qk, auto first_step, int i) {
+        constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value, kFirst = decltype(first_step)::value;
         const int buf = i & 1;
-        const int in = at_in ^ (buf ? 0 : kTile * kD), out = at_out ^ (buf ? kTile * kD : 0);
+        const int in = at_in ^ (kPair<NH> || buf ? 0 : kTile * kD);
+        const int out = at_out ^ (!kPair<NH> && buf ? kTile * kD : 0);
         const _Float16* prob = sh.p[buf] + oc * kPRow + og * 8;
         // a transposed read of unit y's eight entries (below) of this lane's value
         const auto rows8 = [&](int y) {
@@ -540,7 +547,7 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, Cut 
             fd.kv.scale[0] = fd.scale1[0];
             fd.kv.scale[1] = fd.scale1[1];
             bool over = false;
-            if constexpr (!kPv) {
+            if constexpr (kFirst) {
                 // the first step sets R
                 float r[NH];
                 new_reference(fr, r);
@@ -575,9 +582,17 @@ __global__ __launch_bounds__(256, 1) void attend_kernel(const AttendArgs a, Cut 
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
     if (steps > 0) {
-        turn(no, yes, -1);
-        for (int i = 0; i + 1 < steps; ++i) turn(yes, yes, i);
-        turn(yes, no, steps - 1);
+        turn(no, yes, yes, -1);
+        if constexpr (kPair<NH>) {
+            for (int i = 0; i + 1 < steps; ++i) {
+                turn(yes, no, no, i);
+                __syncthreads();  // before the next step's rows take the place
+                turn(no, yes, no, i);
+            }
+        } else {
+            for (int i = 0; i + 1 < steps; ++i) turn(yes, yes, no, i);
+        }
+        turn(yes, no, no, steps - 1);
     }
 
     // the sum over the four lane groups and the four wavefronts
@@ -840,41 +855,45 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
 
 namespace {
 
-// Time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first unit that is free.
-float time_of(int64_t n1, float t1, int64_t n2, float t2) {
-    const int64_t rest = n1 % 256;
-    const float before = (float)(n1 / 256) * t1;
+// Time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first of `places` that is free.
+float time_of(int64_t places, int64_t n1, float t1, int64_t n2, float t2) {
+    const int64_t rest = n1 % places;
+    const float before = (float)(n1 / places) * t1;
     if (n2 == 0) return before + (rest ? t1 : 0.0f);
-    if (rest == 0) return before + (float)((n2 + 255) / 256) * t2;
-    // `rest` units end their long block at t1; the others take short ones from the start
+    if (rest == 0) return before + (float)((n2 + places - 1) / places) * t2;
+    // `rest` places end their long block at t1; the others take short ones from the start
     for (int64_t j = 0;; ++j) {
         const float end = t1 + (float)j * t2;
         const int64_t k = (int64_t)(end / t2);
-        if (k * (256 - rest) + j * rest < n2) continue;
-        const float sooner = (float)k * t2;  // the free units' last one ends before the late ones' j-th
-        const bool enough = j > 0 && sooner >= t1 && k * (256 - rest) + (j - 1) * rest >= n2;
+        if (k * (places - rest) + j * rest < n2) continue;
+        const float sooner = (float)k * t2;  // the other places' last one ends before these places' j-th
+        const bool enough = j > 0 && sooner >= t1 && k * (places - rest) + (j - 1) * rest >= n2;
         return before + (enough ? sooner : end);
     }
 }
 // How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
-// units (a block each) would take. Large head tiles widen a row for more heads, small ones and parts give blocks and
-// even rounds. Measured per step of 64 entries and per block apart from its steps, in microseconds: 1.65 and 13 at 64
-// heads, 1.16 and 9 at 32, 1.1 and 7 at 16 (256 queries over 64 .. 8192 rows); a join 4, and its parts at 4 TB/s.
+// units (a block each, or two of 16 heads) would take. Large head tiles widen a row for more heads, small ones and
+// parts give blocks and even rounds. Measured per step of 64 entries and per block apart from its steps, in
+// microseconds: 1.65 and 10.5 at 64 heads, 1.2 and 6 at 32, 1.6 and 5 for the pairs at 16 (2048 queries over 64 .. 4096
+// rows); with at most one block for every compute unit 1.65 and 13, 1.16 and 9, 1.2 and 7 (256 queries); a join 4, and its
+// parts at 4 TB/s.
 Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
     static constexpr struct {
-        int nh;
-        float step, block;
-    } kTiles[] = {{4, 1.65f, 13.0f}, {2, 1.16f, 9.0f}, {1, 1.1f, 7.0f}};
+        int nh, places;
+        float step, block, step_alone, block_alone;
+    } kTiles[] = {{4, 256, 1.65f, 10.5f, 1.65f, 13.0f}, {2, 256, 1.2f, 6.0f, 1.16f, 9.0f}, {1, 512, 1.6f, 5.0f, 1.2f, 7.0f}};
     const int64_t steps = entries > kTile ? (entries + kTile - 1) / kTile : 1;
     Cut best{1, 1, (uint32_t)nq};
     float least = 0.0f;
     for (const auto& t : kTiles) {
         if (t.nh > 1 && heads <= 8 * t.nh) continue;  // half of the tile would be empty
         const int64_t tiles = (heads + 16 * t.nh - 1) / (16 * t.nh);
-        const auto one = [&](int64_t parts) { return (float)((steps + parts - 1) / parts) * t.step + t.block; };
         const auto consider = [&](int64_t parts, int64_t whole) {
             const int64_t n1 = whole * parts, n2 = (nq - whole) * (parts + 1), joined = parts > 1 ? n1 + n2 : n2;
-            const float time = time_of(n1 * tiles, one(parts), n2 * tiles, one(parts + 1)) +
+            const bool alone = (n1 + n2) * tiles <= 256;
+            const float step = alone ? t.step_alone : t.step, block = alone ? t.block_alone : t.block;
+            const auto one = [&](int64_t n) { return (float)((steps + n - 1) / n) * step + block; };
+            const float time = time_of(t.places, n1 * tiles, one(parts), n2 * tiles, one(parts + 1)) +
                                (joined ? 4.0f + 1e-3f * (float)heads * (float)joined : 0.0f);
             if (least == 0.0f || time < least) {
                 least = time;
@@ -882,11 +901,11 @@ Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
             }
         };
         for (int64_t s = 1; s <= steps && s <= kMostParts; ++s) {
-            if (s > 1 && nq * tiles * s > 8 * 256 + nq * tiles) break;  // rounds are even enough
+            if (s > 1 && nq * tiles * s > 8 * t.places + nq * tiles) break;  // rounds are even enough
             consider(s, nq);
         }
         for (int64_t rounds = 1; rounds <= 8; ++rounds) {  // units for whole rounds
-            const int64_t units = rounds * 256 / tiles, parts = units / nq;
+            const int64_t units = rounds * t.places / tiles, parts = units / nq;
             if (parts >= 1 && parts < steps && parts < kMostParts && units % nq) consider(parts, nq * (parts + 1) - units);
         }
     }
