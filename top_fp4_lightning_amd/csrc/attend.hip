@@ -19,7 +19,7 @@
 // head above 2^6: values down to 2^-20 of it are normal numbers, and what rounds to zero is below 2^-31 of it.
 //
 // What bounds it. Per step and wavefront at 64 heads: 2048 cycles of matrix instructions (64 of 16x16x32, 32 of
-// 32x32x16) and about 290 others, in 1.65 us. The matrix units are busy 42% of the time (counters, 514 queries): one
+// 32x32x16) and about 290 others, in 1.65 us. The matrix units are busy 46% of the time (counters, 514 queries): one
 // wavefront per SIMD issues everything in order, since queries and outputs fill its registers, and what it waits for
 // adds up, none of it large: 16-byte LDS writes (52 cycles for the four wavefronts' one), transposed reads, the
 // barrier and the probabilities between the two products. Leaving any one of these out saved 1 to 14%.
