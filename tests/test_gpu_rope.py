@@ -69,6 +69,21 @@ def test_shapes(fx, tokens, heads, dim, rot, offset, layout, dtype):
             run_case(fx, (tokens, heads, dim), rot, offset, layout, dtype, inverse, in_place=in_place, mscale=1.25)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("heads,dim,rot,offset", [
+    (3, 96, 2, 0), (3, 96, 2, 94), (5, 128, 18, 16), (5, 128, 8, 8), (3, 128, 16, 16), (2, 100, 20, 40), (7, 130, 64, 66),
+    (1, 512, 512, 0), (2, 516, 256, 0), (2, 520, 64, 456), (1, 1024, 64, 960), (4, 66, 4, 2), (3, 65, 6, 1)])
+def test_widths_of_access(fx, heads, dim, rot, offset, layout, dtype):
+    """sizes that allow 16, 8 or 4 bytes or one value, halves of odd length, rows of more and of fewer vectors than a
+    wavefront has lanes; whole and in place, at an odd address, too"""
+    for in_place in (False, True):
+        run_case(fx, (23, heads, dim), rot, offset, layout, dtype, in_place=in_place, mscale=0.75)
+    room = torch.randn(23 * heads * dim + 1, device="cuda").to(dtype)
+    x = room[1:].view(23, heads, dim)
+    run_case(fx, (23, heads, dim), rot, offset, layout, dtype, x=x, inverse=True)
+
+
 @pytest.mark.parametrize("far", [1 << 20, 1 << 24, 1 << 31])
 def test_far_positions(fx, far):
     run_case(fx, (64, 4, 64), 64, 0, "half", torch.float32, pos=far - np.arange(64))
