@@ -76,10 +76,10 @@ __device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, Te
         e.p[k] = p < n ? p : -1;
     }
 }
-__device__ __forceinline__ void load_scores(const float* __restrict__ s, int32_t from, Teacher& e) {
+__device__ __forceinline__ void load_scores(const float* __restrict__ s, Teacher& e) {
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k)
-        if (e.p[k] >= from) e.sl[k] = s[e.p[k]];
+        if (e.p[k] >= 0) e.sl[k] = s[e.p[k]];
 }
 
 // The sum over s[i0 .. i1), this thread's share. With teacher entries (i0 = 0, the whole row), their scores are taken
@@ -89,12 +89,25 @@ template <bool TAKE>
 __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t i0, int32_t i1, float c, Teacher* e,
                                            float* piece) {
     MaxSum v{ninf(), 0.0f};
-    int32_t p0 = i0;
-    for (; p0 + kPiece <= i1; p0 += kPiece) {
+    for (int32_t p0 = i0; p0 < i1; p0 += kPiece) {
         const int32_t i = p0 + (int32_t)threadIdx.x * 4;
         f4u x[4];
+        if (p0 + kPiece <= i1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * kThreads * 4);
+            for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * kThreads * 4);
+        } else {
+            // the row's end; what is past it adds nothing
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int32_t ik = i + k * kThreads * 4;
+                if (ik + 4 <= i1) {
+                    x[k] = *reinterpret_cast<const f4u*>(s + ik);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[k][j] = ik + j < i1 ? s[ik + j] : ninf();
+                }
+            }
+        }
         if constexpr (TAKE) {
             if (p0) __syncthreads();
 #pragma unroll
@@ -116,15 +129,6 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
             for (int j = 0; j < 4; ++j) sum += __builtin_amdgcn_exp2f((x[k][j] - r) * c);
         v.l = v.l * __builtin_amdgcn_exp2f((v.m - r) * c) + sum;
         v.m = m;
-    }
-    if constexpr (TAKE) load_scores(s, p0, *e);
-    for (int32_t i = p0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i + j < i1) {
-                const float x = s[i + j];
-                v = join(v, MaxSum{x, x == ninf() ? 0.0f : 1.0f}, c);
-            }
     }
     return v;
 }
@@ -190,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
     const float c = a.inv_temp * kLog2e;
     Teacher e;
     load_teacher(a, t, e);
-    load_scores(a.scores + t * a.score_stride, 0, e);
+    load_scores(a.scores + t * a.score_stride, e);
     MaxSum v{ninf(), 0.0f};
     for (int i = threadIdx.x; i < pieces; i += kThreads)
         v = join(v, reinterpret_cast<const MaxSum*>(a.ws)[t * pieces + i], c);
