@@ -111,6 +111,17 @@ def test_few_long_and_many_short_rows(fx, nq, n, k):
     check(fx, s, rng.integers(0, n + 1, nq), n, idx, tl)
 
 
+@pytest.mark.parametrize("n,k", [(1, 1), (77, 5), (1023, 64), (1024, 100), (1025, 512), (2500, 300), (2500, 600)])
+def test_many_short_rows(fx, n, k):
+    rng = np.random.default_rng(n + k)
+    nq = 2050
+    s = (rng.standard_normal((nq, n)) * 3).astype(np.float32)
+    s[rng.random((nq, n)) < 0.2] = -np.inf
+    nv = rng.integers(0, n + 1, nq)
+    nv[:3] = [n, 0, n]
+    check(fx, s, nv, n, rng.integers(-1, n, (nq, k)), rng.standard_normal((nq, k)) * 2)
+
+
 def test_a_gradient_beyond_the_last_level_cache(fx):
     """above 2^25 scores: most rows short, some of several pieces, the strides as wide as the longest"""
     rng = np.random.default_rng(9)

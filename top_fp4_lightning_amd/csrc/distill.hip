@@ -33,17 +33,22 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
     const float r = m == ninf() ? 0.0f : m;
     return MaxSum{m, a.l * __builtin_amdgcn_exp2f((a.m - r) * c) + b.l * __builtin_amdgcn_exp2f((b.m - r) * c)};
 }
+// (G: threads of the block, 256 or one wavefront)
+template <int G>
 __device__ __forceinline__ MaxSum block_join(MaxSum v, float c, MaxSum* lds) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v = join(v, MaxSum{__shfl_xor(v.m, d), __shfl_xor(v.l, d)}, c);
+    if (G == 64) return v;
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     return join(join(lds[0], lds[1], c), join(lds[2], lds[3], c), c);
 }
+template <int G>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    if (G == 64) return v;
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -66,11 +71,12 @@ struct Teacher {
     int32_t p[kPerThread];                 // positions, -1: not an entry
     float tl[kPerThread], sl[kPerThread];  // logits, the row's scores there
 };
+template <int G>
 __device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t t, Teacher& e) {
     const int32_t n = visible(a, t);
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-        const int i = k * kThreads + (int)threadIdx.x;
+        const int i = k * G + (int)threadIdx.x;
         const int32_t p = i < a.k ? a.t_idx[t * a.t_stride + i] : -1;
         e.tl[k] = i < a.k ? a.t_logit[t * a.t_stride + i] : ninf();
         e.p[k] = p < n ? p : -1;
@@ -85,21 +91,22 @@ __device__ __forceinline__ void load_scores(const float* __restrict__ s, Teacher
 // The sum over s[i0 .. i1), this thread's share. With teacher entries (i0 = 0, the whole row), their scores are taken
 // on the way, from a copy of each piece in LDS: read by themselves they would cost a line each (4096 rows of up to
 // 32768 scores with 512 entries: 0.72 GB of reads in place of 0.49).
-template <bool TAKE>
+template <int G, bool TAKE>
 __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t i0, int32_t i1, float c, Teacher* e,
                                            float* piece) {
+    constexpr int kPart = 16 * G;
     MaxSum v{ninf(), 0.0f};
-    for (int32_t p0 = i0; p0 < i1; p0 += kPiece) {
+    for (int32_t p0 = i0; p0 < i1; p0 += kPart) {
         const int32_t i = p0 + (int32_t)threadIdx.x * 4;
         f4u x[4];
-        if (p0 + kPiece <= i1) {
+        if (p0 + kPart <= i1) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * kThreads * 4);
+            for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f4u*>(s + i + k * G * 4);
         } else {
             // the row's end; what is past it adds nothing
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int32_t ik = i + k * kThreads * 4;
+                const int32_t ik = i + k * G * 4;
                 if (ik + 4 <= i1) {
                     x[k] = *reinterpret_cast<const f4u*>(s + ik);
                 } else {
@@ -111,11 +118,11 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
         if constexpr (TAKE) {
             if (p0) __syncthreads();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<v4f*>(piece + (threadIdx.x + k * kThreads) * 4) = x[k];
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<v4f*>(piece + (threadIdx.x + k * G) * 4) = x[k];
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kPerThread; ++k)
-                if (e->p[k] >= p0 && e->p[k] < p0 + kPiece) e->sl[k] = piece[e->p[k] - p0];
+                if (e->p[k] >= p0 && e->p[k] < p0 + kPart) e->sl[k] = piece[e->p[k] - p0];
         }
         float top = ninf();
 #pragma unroll
@@ -134,6 +141,7 @@ __device__ __forceinline__ MaxSum row_part(const float* __restrict__ s, int32_t 
 }
 
 // the row's end: the teacher's sum and the loss. Whole block.
+template <int G>
 __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teacher& e, MaxSum row,
                                            MaxSum* lds_ms, double* lds_d) {
     const float c = a.inv_temp * kLog2e;
@@ -143,7 +151,7 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teac
         if (e.p[k] < 0 || e.sl[k] == ninf()) e.tl[k] = ninf();
         if (e.tl[k] != ninf()) v = join(v, MaxSum{e.tl[k], 1.0f}, c);
     }
-    v = block_join(v, c, lds_ms);
+    v = block_join<G>(v, c, lds_ms);
     const double tlse = log_of(v, a.inv_temp), lse = log_of(row, a.inv_temp);
     double sum = 0.0;
 #pragma unroll
@@ -152,7 +160,7 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teac
             const double d = (double)e.tl[k] * a.inv_temp - tlse;
             sum += (double)expf((float)d) * (d - ((double)e.sl[k] * a.inv_temp - lse));
         }
-    sum = block_sum(sum, lds_d);
+    sum = block_sum<G>(sum, lds_d);
     if (threadIdx.x == 0) {
         a.loss[t] = (float)sum;
         a.lse[t] = (float)lse;
@@ -161,16 +169,17 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teac
 }
 
 // a block for every row
-__global__ __launch_bounds__(kThreads) void distill_kernel(const DistillArgs a) {
+template <int G>
+__global__ __launch_bounds__(G) void distill_kernel(const DistillArgs a) {
     __shared__ MaxSum s_ms[4];
     __shared__ double s_d[4];
-    __shared__ __align__(16) float s_piece[kPiece];
+    __shared__ __align__(16) float s_piece[16 * G];
     const int64_t t = blockIdx.x;
     const float c = a.inv_temp * kLog2e;
     Teacher e;
-    load_teacher(a, t, e);
-    const MaxSum v = row_part<true>(a.scores + t * a.score_stride, 0, visible(a, t), c, &e, s_piece);
-    finish_row(a, t, e, block_join(v, c, s_ms), s_ms, s_d);
+    load_teacher<G>(a, t, e);
+    const MaxSum v = row_part<G, true>(a.scores + t * a.score_stride, 0, visible(a, t), c, &e, s_piece);
+    finish_row<G>(a, t, e, block_join<G>(v, c, s_ms), s_ms, s_d);
 }
 
 // few rows: a block for a piece of one, whose (max, sum) it writes
@@ -183,7 +192,8 @@ __global__ __launch_bounds__(kThreads) void distill_piece_kernel(const DistillAr
     const int32_t i0 = (int32_t)min((int64_t)piece * per, (int64_t)n);
     const int32_t i1 = (int32_t)min((int64_t)i0 + per, (int64_t)n);
     const float c = a.inv_temp * kLog2e;
-    const MaxSum v = block_join(row_part<false>(a.scores + t * a.score_stride, i0, i1, c, nullptr, nullptr), c, s_ms);
+    const float* s = a.scores + t * a.score_stride;
+    const MaxSum v = block_join<kThreads>(row_part<kThreads, false>(s, i0, i1, c, nullptr, nullptr), c, s_ms);
     if (threadIdx.x == 0) reinterpret_cast<MaxSum*>(a.ws)[blockIdx.x] = v;
 }
 
@@ -193,13 +203,13 @@ __global__ __launch_bounds__(kThreads) void distill_join_kernel(const DistillArg
     const int64_t t = blockIdx.x;
     const float c = a.inv_temp * kLog2e;
     Teacher e;
-    load_teacher(a, t, e);
+    load_teacher<kThreads>(a, t, e);
     load_scores(a.scores + t * a.score_stride, e);
     MaxSum v{ninf(), 0.0f};
     for (int i = threadIdx.x; i < pieces; i += kThreads)
         v = join(v, reinterpret_cast<const MaxSum*>(a.ws)[t * pieces + i], c);
-    v = block_join(v, c, s_ms);
-    finish_row(a, t, e, v, s_ms, s_d);
+    v = block_join<kThreads>(v, c, s_ms);
+    finish_row<kThreads>(a, t, e, v, s_ms, s_d);
 }
 
 __device__ __forceinline__ float softmax_of(float x, float inv_temp, float lse) {
@@ -295,7 +305,12 @@ size_t distill_workspace_bytes(int32_t nq, int64_t max_n) {
 hipError_t launch_distill(const DistillArgs& a, hipStream_t stream) {
     const int pieces = distill_pieces(a.nq, a.max_n);
     if (pieces == 1) {
-        hipLaunchKernelGGL(distill_kernel, dim3((unsigned)a.nq), dim3(kThreads), 0, stream, a);
+        // Many short rows: a wavefront each, which has no barriers to wait at (4096 rows of 500 scores 21 -> 12 us, of
+        // 16000 49 -> 48, 20000 of 2000 91 -> 46; 1024 rows 11 -> 12).
+        if (a.nq >= 2048 && a.max_n <= 16384 && a.k <= 64 * kPerThread)
+            hipLaunchKernelGGL(distill_kernel<64>, dim3((unsigned)a.nq), dim3(64), 0, stream, a);
+        else
+            hipLaunchKernelGGL(distill_kernel<kThreads>, dim3((unsigned)a.nq), dim3(kThreads), 0, stream, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(distill_piece_kernel, dim3((unsigned)a.nq * pieces), dim3(kThreads), 0, stream, a, pieces);
