@@ -912,7 +912,8 @@ Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
     return best;
 }
 
-// the same for the sizes asked for last (a call asks twice, for its workspace and for its launch)
+// The same for the sizes asked for last: a call asks twice, for its workspace and for its launch, and the next call
+// mostly has the same (a search takes up to some ten microseconds).
 Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
     thread_local int64_t of[3] = {0, 0, 0};
     thread_local Cut cut{};
@@ -928,7 +929,7 @@ Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
 // Parts of a query's entries in the weights' kernel, in the same way. Measured per step and per block apart from its
 // steps, in microseconds: 0.8 and 7.5 at 64 heads, 0.55 and 3.2 at 32, 0.5 and 2.6 at 16 (1024 queries over 64 .. 4096
 // rows).
-int weights_parts(int32_t nq, int32_t heads, int64_t steps) {
+int best_parts(int32_t nq, int32_t heads, int64_t steps) {
     const float step = heads > 32 ? 0.8f : heads > 16 ? 0.55f : 0.5f, block = heads > 32 ? 7.5f : heads > 16 ? 3.2f : 2.6f;
     int best = 1;
     float least = 0.0f;
@@ -941,6 +942,17 @@ int weights_parts(int32_t nq, int32_t heads, int64_t steps) {
         }
     }
     return best;
+}
+int weights_parts(int32_t nq, int32_t heads, int64_t steps) {
+    thread_local int64_t of[3] = {0, 0, 0};
+    thread_local int parts = 1;
+    if (of[0] != nq || of[1] != heads || of[2] != steps) {
+        parts = best_parts(nq, heads, steps);
+        of[0] = nq;
+        of[1] = heads;
+        of[2] = steps;
+    }
+    return parts;
 }
 
 // p / page_size for 0 <= p < 2^30 as a product: with d <= 2^b < 2 d, mul = floor(2^(31+b) / d) + 1 is below 2^32 and exceeds
