@@ -27,8 +27,9 @@ for every query; idx_top_blocks keeps the 512 best blocks per query (a top-512 k
 them); idx_score_pool_gather re-scores those 4096 keys; idx_topk takes the final 512.
 
 Core attention (the consumer of a layer's selection): CoreAttention keeps the FP4 main-KV cache in pages,
-rotates and quantises new rows into them, and attends over the selected positions. IndexerDistill trains a
-layer's indexer towards it, on the score rows of the training form.
+rotates and quantises new rows into them, and attends over the selected positions; layer() gives the result
+with the values turned back to the query's frame. IndexerDistill trains a layer's indexer towards it, on the
+score rows of the training form.
 
 All buffers are allocated once in the plan objects, so a step allocates nothing and can be
 captured in a HIP graph.
@@ -338,7 +339,13 @@ class CoreAttention:
     pages of `page_size`, given out as the sequences grow, and the buffers of a step of `nq` queries. The last `rot`
     values of every query and row carry the rotary position; rows are rotated before they are quantised (the page on
     the main KV quantises after the rotation). scale defaults to 512 ** -0.5; the other arguments of rope_freqs
-    stretch the context."""
+    stretch the context.
+
+    A row is key and value at once, so what is averaged has been turned by its position p and scaled by mscale (which
+    is meant for the logits): m R_p x. layer() turns the result back by the query's position t and takes the factor
+    out, R_{p-t} x: it depends on distances only, as the logits do. run() leaves it in the cache's frame, for callers
+    that join it with attention over another cache of the same frame by the two lse first (the sum over both turns
+    back as one)."""
 
     def __init__(self, nseq: int, n: int, nq: int, heads: int = 64, k: int = 512, page_size: int = 64, rot: int = 64,
                  scale: float | None = None, layout: str = "interleaved", device="cuda", **freqs):
@@ -377,10 +384,19 @@ class CoreAttention:
 
     def run(self, q, pos, seq, n_vis, idx, stream=None):
         """q [nq, heads, 512] (bf16, not rotated) at positions pos [nq] (int64) of sequences seq [nq], over the
-        selected positions idx [nq, k] below n_vis [nq] -> out, lse."""
+        selected positions idx [nq, k] below n_vis [nq] -> out, lse. out is the average of cache rows as they are
+        stored: its last rot values are still turned by the rows' positions and mscale times too large (see layer)."""
         idx_rope(q, pos, self.freq, layout=self.layout, mscale=self.mscale, out=self.q, stream=stream)
         return idx_attend(self.q, self.codes, self.scales, n_vis, self.n, self.scale, self.out, self.ws, lse=self.lse,
                           pages=self.pages, page_size=self.page_size, seq=seq, idx=idx, stream=stream)
+
+    def layer(self, q, pos, seq, n_vis, idx, stream=None):
+        """The layer's attention output: run() with out turned back by pos, in place (its rotated values are rounded
+        to bf16 once more) -> out, lse."""
+        self.run(q, pos, seq, n_vis, idx, stream=stream)
+        idx_rope(self.out, pos, self.freq, layout=self.layout, mscale=1.0 / self.mscale, inverse=True, out=self.out,
+                 stream=stream)
+        return self.out, self.lse
 
     def selection_weights(self, seq, n_vis, idx, stream=None):
         """The probabilities [nq, k] that the last run gave its selection, mean over the heads."""
