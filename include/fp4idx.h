@@ -500,7 +500,8 @@ idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, cons
  *
  *   scores  : device fp32 [nq][score_stride], score_stride >= max_n.   n_vis, max_n : as above.
  *   t_idx   : device int32 [nq][t_stride]; t_logit : device fp32 [nq][t_stride]; k 0 .. 2048 slots, t_stride >= k.
- *   inv_temp: 1 / T, above 0; scores and logits times it stay in fp32's range.
+ *   inv_temp: 1 / T, above 0; scores and logits times it stay in fp32's range. Only differences within a row count:
+ *             a row may lie anywhere in that range, at the type's lowest value throughout, too.
  *   loss, lse, t_lse : device fp32 [nq] (written); lse and t_lse are the logarithms of the two sums, for
  *             idx_distill_bwd (-inf for none).
  *   ws, ws_bytes : at least idx_workspace_size(IDX_OP_DISTILL, nq, max_n, 1) bytes, 16-byte aligned; as for
@@ -512,7 +513,9 @@ idx_status idx_distill(const float* scores, int64_t score_stride, const int32_t*
 
 /*
  * idx_distill_bwd: its gradient, dscores[t][s] = dloss[t] * inv_temp * (q_s - sum of p_i over x_i = s).
- * Written for s < n_t only; 0 where the score is -inf and for a row without entries.
+ * Written for s < n_t only; 0 where the score is -inf and for a row without entries. q and p come out of the fp32 lse
+ * and t_lse, each within 2^-24 of the logarithm's size; where one is 1024 or more the row's sums are taken again (one
+ * block per row: slower, for few long rows by much).
  *
  *   lse, t_lse : idx_distill's, of the same arguments.   dloss : device fp32 [nq].
  *   dscores : device fp32 [nq][d_stride], d_stride >= max_n; may be scores itself (with its stride).

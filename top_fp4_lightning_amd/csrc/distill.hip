@@ -9,6 +9,8 @@
 // take 100 us forward and 293 us with the gradient (5.5 TB/s over both; a copy reaches 4.8). Few rows are cut into
 // pieces of at least 4096 scores, so that the compute units have about four blocks each, and joined by a second launch
 // (8 rows of 2^20: 9 and 5 us, the gradient 13).
+#include <type_traits>
+
 #include "operators.h"
 
 namespace fp4idx {
@@ -152,19 +154,20 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, int64_t t, Teac
         if (e.tl[k] != ninf()) v = join(v, MaxSum{e.tl[k], 1.0f}, c);
     }
     v = block_join<G>(v, c, lds_ms);
-    const double tlse = log_of(v, a.inv_temp), lse = log_of(row, a.inv_temp);
+    // differences to the largest first: a logarithm near the type's lowest value would swallow the sum's
+    const double tlog = log((double)v.l), log_sum = log((double)row.l);
     double sum = 0.0;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k)
         if (e.tl[k] != ninf()) {
-            const double d = (double)e.tl[k] * a.inv_temp - tlse;
-            sum += (double)expf((float)d) * (d - ((double)e.sl[k] * a.inv_temp - lse));
+            const double d = ((double)e.tl[k] - v.m) * a.inv_temp - tlog;
+            sum += (double)expf((float)d) * (d - (((double)e.sl[k] - row.m) * a.inv_temp - log_sum));
         }
     sum = block_sum<G>(sum, lds_d);
     if (threadIdx.x == 0) {
         a.loss[t] = (float)sum;
-        a.lse[t] = (float)lse;
-        a.t_lse[t] = (float)tlse;
+        a.lse[t] = (float)log_of(row, a.inv_temp);
+        a.t_lse[t] = (float)log_of(v, a.inv_temp);
     }
 }
 
@@ -216,22 +219,31 @@ __device__ __forceinline__ float softmax_of(float x, float inv_temp, float lse) 
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, inv_temp, -lse) * kLog2e);
 }
 
+// From this size of a logarithm on, a row's gradient takes its sums again, as (largest, sum): half a step of fp32 at
+// the logarithm is 2^-15 of every q and p below it and 1 at 2^24 (a row of equal scores at the type's lowest value would
+// get q = 1 for each). What that costs, against rows about zero: 4096 rows of 32768 scores 215 -> 288 us, 64 of 131072
+// 16 -> 121, 8 of 2^20 15 -> 860.
+constexpr float kFar = 1024.0f;
+
 // Gradient: a block takes a range of whole pieces of one row. The last rows come first: after the forward the last-level
-// cache holds those. PAST: the gradient is written past that cache, which leaves it to the scores.
+// cache holds those. PAST: the gradient is written past that cache, which leaves it to the scores. A far row is one
+// block's: in place, another's writes would be in the sums.
 template <bool PAST>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs a, int blocks_per_row) {
     __shared__ float s_p[kPiece];
+    __shared__ MaxSum s_ms[4];
     const int64_t t = a.nq - 1 - (int64_t)(blockIdx.x / blocks_per_row);
     const int part = (int)(blockIdx.x % blocks_per_row);
     const int32_t n = visible(a, t);
     const int32_t pieces = (n + kPiece - 1) / kPiece;
-    const int32_t per = (pieces + blocks_per_row - 1) / blocks_per_row;
+    const float tlse = a.t_lse[t];
+    const float lse = a.lse[t];
+    const bool far = tlse != ninf() && (fabsf(lse) >= kFar || fabsf(tlse) >= kFar);
+    const int32_t per = far ? pieces : (pieces + blocks_per_row - 1) / blocks_per_row;
     const int32_t p0 = min(part * per, pieces), p1 = min(p0 + per, pieces);
     if (p0 >= p1) return;
     const float* s = a.scores + t * a.score_stride;
     float* d = a.dscores + t * a.d_stride;
-    const float tlse = a.t_lse[t];
-    const float lse = a.lse[t];
     const float gain = tlse == ninf() ? 0.0f : a.dloss[t] * a.inv_temp;
     if (tlse == ninf()) {  // no teacher entry: no gradient
         for (int32_t i = p0 * kPiece + (int32_t)threadIdx.x; i < min(p1 * kPiece, n); i += kThreads) d[i] = 0.0f;
@@ -246,13 +258,53 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs
     for (int k = 0; k < kPerThread; ++k) {
         const int i = (wave * kPerThread + k) * 64 + (int)(threadIdx.x & 63);
         at[k] = -1;
-        p[k] = 0.0f;
+        p[k] = ninf();
         if (i < a.k) {
             at[k] = a.t_idx[t * a.t_stride + i];
-            const float x = a.t_logit[t * a.t_stride + i];
-            p[k] = x == ninf() ? 0.0f : softmax_of(x, a.inv_temp, tlse);
+            p[k] = a.t_logit[t * a.t_stride + i];
         }
+        if (!far) p[k] = p[k] == ninf() ? 0.0f : softmax_of(p[k], a.inv_temp, tlse);
     }
+    const float c = a.inv_temp * kLog2e;
+    float row_m = 0.0f, row_inv = 0.0f;
+    if (far) {
+        const MaxSum row = block_join<kThreads>(row_part<kThreads, false>(s, 0, n, c, nullptr, nullptr), c, s_ms);
+        row_m = row.m;
+        row_inv = 1.0f / row.l;
+        MaxSum v{ninf(), 0.0f};
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            if (at[k] < 0 || at[k] >= n || s[at[k]] == ninf()) p[k] = ninf();
+            if (p[k] != ninf()) v = join(v, MaxSum{p[k], 1.0f}, c);
+        }
+        v = block_join<kThreads>(v, c, s_ms);
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) p[k] = __builtin_amdgcn_exp2f((p[k] - v.m) * c) / v.l;
+    }
+    const auto q_of = [&](auto is_far, float x) {
+        if constexpr (decltype(is_far)::value) return __builtin_amdgcn_exp2f((x - row_m) * c) * row_inv;
+        else return softmax_of(x, a.inv_temp, lse);
+    };
+    const auto stream_piece = [&](auto is_far, int32_t i0, int32_t i1) {
+        for (int32_t i = i0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
+            const v4f pv = *reinterpret_cast<const v4f*>(s_p + (i - i0));
+            if (i + 4 <= i1) {
+                const f4u x = *reinterpret_cast<const f4u*>(s + i);
+                f4u y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = x[j] == ninf() ? 0.0f : gain * (q_of(is_far, x[j]) - pv[j]);
+                if constexpr (PAST)
+                    __builtin_nontemporal_store(y, reinterpret_cast<f4u*>(d + i));
+                else
+                    *reinterpret_cast<f4u*>(d + i) = y;
+            } else {
+                for (int j = 0; i + j < i1; ++j) {
+                    const float x = s[i + j];
+                    d[i + j] = x == ninf() ? 0.0f : gain * (q_of(is_far, x) - pv[j]);
+                }
+            }
+        }
+    };
     for (int32_t pc = p0; pc < p1; ++pc) {
         const int32_t i0 = pc * kPiece, i1 = min(i0 + kPiece, n);
         for (int i = threadIdx.x * 4; i < kPiece; i += kThreads * 4) *reinterpret_cast<v4f*>(s_p + i) = v4f{};
@@ -264,25 +316,10 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(const DistillArgs
                 if (at[k] >= i0 && at[k] < i1) atomicAdd(s_p + (at[k] - i0), p[k]);
         }
         __syncthreads();
-        for (int32_t i = i0 + (int32_t)threadIdx.x * 4; i < i1; i += kThreads * 4) {
-            const v4f pv = *reinterpret_cast<const v4f*>(s_p + (i - i0));
-            if (i + 4 <= i1) {
-                const f4u x = *reinterpret_cast<const f4u*>(s + i);
-                f4u y;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    y[j] = x[j] == ninf() ? 0.0f : gain * (softmax_of(x[j], a.inv_temp, lse) - pv[j]);
-                if constexpr (PAST)
-                    __builtin_nontemporal_store(y, reinterpret_cast<f4u*>(d + i));
-                else
-                    *reinterpret_cast<f4u*>(d + i) = y;
-            } else {
-                for (int j = 0; i + j < i1; ++j) {
-                    const float x = s[i + j];
-                    d[i + j] = x == ninf() ? 0.0f : gain * (softmax_of(x, a.inv_temp, lse) - pv[j]);
-                }
-            }
-        }
+        if (far)
+            stream_piece(std::true_type{}, i0, i1);
+        else
+            stream_piece(std::false_type{}, i0, i1);
         __syncthreads();
     }
 }
