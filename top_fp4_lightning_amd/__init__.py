@@ -144,6 +144,19 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An output that a call on `stream` writes. Memory that was free on the current stream may still be read there by
+    work queued before it was freed, so the output comes from the stream that writes it (as a tensor made inside
+    `with torch.cuda.stream(stream)`: a use on another stream needs its wait and record_stream)."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -173,9 +186,9 @@ def idx_quantize_q(x: torch.Tensor, signs: torch.Tensor, codes: torch.Tensor | N
     lead = x.shape[:-1]
     rows = x.numel() // DIM
     if codes is None:
-        codes = torch.empty(*lead, 64, dtype=torch.uint8, device=x.device)
+        codes = _empty((*lead, 64), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(*lead, 4, dtype=torch.uint8, device=x.device)
+        scales = _empty((*lead, 4), torch.uint8, x.device, stream)
     _call(lib.idx_quantize_q, _ptr(x), rows, _ptr(signs), _ptr(codes), _ptr(scales), _stream(stream))
     return codes, scales
 
@@ -260,9 +273,9 @@ def idx_quantize_kv(x: torch.Tensor, codes: torch.Tensor | None = None, scales: 
     lead = x.shape[:-1]
     rows = x.numel() // MKV_DIM
     if codes is None:
-        codes = torch.empty(*lead, MKV_DIM // 2, dtype=torch.uint8, device=x.device)
+        codes = _empty((*lead, MKV_DIM // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(*lead, MKV_DIM // 16, dtype=torch.uint8, device=x.device)
+        scales = _empty((*lead, MKV_DIM // 16), torch.uint8, x.device, stream)
     _call(lib.idx_quantize_kv, _ptr(x), rows, _ptr(codes), _ptr(scales), _stream(stream))
     return codes, scales
 
@@ -275,7 +288,7 @@ def idx_gather_kv(codes, scales, kv_base, n_vis, idx, out=None, k: int | None = 
     nq = idx.shape[0]
     k = idx.shape[1] if k is None else k
     if out is None:
-        out = torch.empty(nq, k, MKV_DIM, dtype=torch.bfloat16, device=idx.device)
+        out = _empty((nq, k, MKV_DIM), torch.bfloat16, idx.device, stream)
     _need(out, torch.bfloat16, "out")
     _call(lib.idx_gather_kv, _ptr(codes), _ptr(scales), _ptr(kv_base), _ptr(n_vis), nq, _ptr(idx), idx.stride(0), k,
           _ptr(out), _stream(stream))
@@ -373,7 +386,7 @@ def idx_rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, offset: int
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _empty(x.shape, dtype, x.device, stream)
     elif out.dtype is not dtype:
         raise TypeError(f"out must be {dtype}, got {out.dtype}")
     elif out.shape != x.shape or (out.shape[2] > 1 and out.stride(2) != 1):
