@@ -459,7 +459,7 @@ idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads,
  * lse = -inf. Products are exact in fp16 operands (q scaled by a power of two per row; values below 2^-28 of the
  * row's largest lose low bits), sums, maximum and normalisation fp32; probabilities are rounded to 11 bits for
  * the second product (those below 2^-20 of a head's largest to fewer, below 2^-31 perhaps to zero). A non-finite
- * value in a q row makes that head's results NaN and no other's.
+ * value in a q row makes that head's results NaN and no other's (where the query has entries).
  */
 idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes, const uint8_t* scales,
                       int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,

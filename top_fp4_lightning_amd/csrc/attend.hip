@@ -224,10 +224,12 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int h0, QueryRo
         m = max(m, dpp<0x140>(m));  // row_mirror
         m = max16(m);
         m = max32(m);
-        // 2^(14 - exponent of the largest), a power of two kept inside the normal range
+        // 2^(14 - exponent of the largest), a power of two kept inside the normal range. A row that is not finite
+        // becomes NaN throughout: an infinity's products may all be -inf, as if nothing had been attended to.
         int e = (int)(m >> 7);
+        const bool finite = e < 255;
         e = e < 15 ? 15 : (e > 254 ? 254 : e);
-        const float mul = __uint_as_float((uint32_t)(127 + 141 - e) << 23);
+        const float mul = finite ? __uint_as_float((uint32_t)(127 + 141 - e) << 23) : __builtin_nanf("");
         h8 o;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
