@@ -50,7 +50,7 @@ typedef int32_t idx_status;
 /* operation codes for idx_workspace_size */
 #define IDX_OP_BUILD_POOL 1
 #define IDX_OP_TOPK 2
-#define IDX_OP_ATTEND 3   /* nq queries, max_n list slots or positions attended to, k = heads */
+#define IDX_OP_ATTEND 3   /* nq queries, max_n list slots or positions attended to, k = heads; see idx_attend */
 #define IDX_OP_DISTILL 4  /* nq rows of at most max_n scores; any valid k */
 
 /* element types of idx_rope */
@@ -450,9 +450,13 @@ idx_status idx_rope(const void* x, int32_t dtype, int64_t tokens, int32_t heads,
  *   scale   : finite.
  *   out     : device bf16 [nq][heads][512], 16-byte aligned (written).
  *   lse     : device fp32 [nq][heads] or NULL (written; natural logarithm).
- *   ws, ws_bytes : at least idx_workspace_size(IDX_OP_ATTEND, nq, entries, heads) bytes, 16-byte aligned, with
- *             entries = k, or the window where one is given and shorter than max_n, or max_n. It holds nothing
- *             between calls; calls that may run concurrently need separate workspaces.
+ *   ws, ws_bytes : device, 16-byte aligned, at least 16 bytes; idx_workspace_size(IDX_OP_ATTEND, nq, entries, heads)
+ *             of them, with entries = k, or the window where one is given and shorter than max_n, or max_n, let the
+ *             call run fastest. That size does not grow with entries or nq (a batch that fills the GPU needs no parts),
+ *             so a workspace of another call's size may be smaller: the queries are then cut into the parts that fit,
+ *             which takes about the larger call's time at most. The parts, and with them the last
+ *             roundings of the joined sums, depend on sizes and ws_bytes alone. It holds nothing between calls; calls
+ *             that may run concurrently need separate workspaces.
  *
  * An entry whose row is outside [0, rows), whose page is negative, or whose seq is outside [0, nseq) is left
  * out; what the cache holds there or at masked entries has no effect. A query without entries gets out = 0 and

@@ -441,7 +441,8 @@ def idx_attend(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=N
                pages=None, page_size: int = 0, seq=None, idx=None, stream=None):
     """Core attention of q [nq, heads, 512] over the FP4 main-KV cache: all visible positions (or the last
     `window`), or those of idx [nq, k]. Rows lie at kv_base [nq] + position, or in pages [nseq, ...] of
-    page_size positions (seq [nq] names each query's page row). ws: workspace(IDX_OP_ATTEND, nq, entries, heads)."""
+    page_size positions (seq [nq] names each query's page row). ws: workspace(IDX_OP_ATTEND, nq, entries, heads),
+    or another call's: in a smaller one the queries are cut into fewer parts."""
     where, lst = _attend_where(q, codes, scales, n_vis, max_n, kv_base, pages, page_size, seq, idx)
     out_ptr = _arg(out, torch.bfloat16, q.shape, "out")
     lse_ptr = None if lse is None else _arg(lse, torch.float32, q.shape[:2], "lse")

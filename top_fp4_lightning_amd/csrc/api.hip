@@ -534,13 +534,11 @@ idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_
     if (st != IDX_OK || nq == 0) return st;
     REQUIRE(out, IDX_EINVAL, "idx_attend: null pointer");
     REQUIRE(aligned(out, 16) && aligned(lse, 4), IDX_EALIGN, "idx_attend: misaligned pointer");
-    const int64_t entries = idx ? k : (window > 0 && window < max_n ? window : max_n);
-    const size_t need = attend_workspace_bytes(nq, heads, entries);
-    REQUIRE(ws && ws_bytes >= need, IDX_EWORKSPACE, "idx_attend: workspace %zu bytes, need %zu", ws_bytes, need);
+    REQUIRE(ws && ws_bytes >= 16, IDX_EWORKSPACE, "idx_attend: workspace %zu bytes, need at least 16", ws_bytes);
     REQUIRE(aligned(ws, 16), IDX_EALIGN, "idx_attend: misaligned workspace");
     a.out = out;
     a.lse = lse;
-    return hip_status(launch_attend(a, ws, (hipStream_t)stream), "idx_attend");
+    return hip_status(launch_attend(a, ws, ws_bytes, (hipStream_t)stream), "idx_attend");
 }
 
 idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, const uint8_t* codes,

@@ -878,8 +878,9 @@ float time_of(int64_t places, int64_t n1, float t1, int64_t n2, float t2) {
 // parts give blocks and even rounds. Measured per step of 64 entries and per block apart from its steps, in
 // microseconds: 1.65 and 10.5 at 64 heads, 1.2 and 6 at 32, 1.6 and 5 for the pairs at 16 (2048 queries over 64 .. 4096
 // rows); with at most one block for every compute unit 1.65 and 13, 1.16 and 9, 1.2 and 7 (256 queries); a join 4, and its
-// parts at 4 TB/s.
-Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
+// parts at 4 TB/s. Where a query is cut at all, every unit's output and sums lie in the workspace, which has room for
+// `room` units.
+Cut best_cut(int32_t nq, int32_t heads, int64_t entries, uint64_t room) {
     static constexpr struct {
         int nh, places;
         float step, block, step_alone, block_alone;
@@ -892,6 +893,7 @@ Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
         const int64_t tiles = (heads + 16 * t.nh - 1) / (16 * t.nh);
         const auto consider = [&](int64_t parts, int64_t whole) {
             const int64_t n1 = whole * parts, n2 = (nq - whole) * (parts + 1), joined = parts > 1 ? n1 + n2 : n2;
+            if (n1 + n2 > nq && (uint64_t)(n1 + n2) > room) return;
             const bool alone = (n1 + n2) * tiles <= 256;
             const float step = alone ? t.step_alone : t.step, block = alone ? t.block_alone : t.block;
             const auto one = [&](int64_t n) { return (float)((steps + n - 1) / n) * step + block; };
@@ -914,19 +916,23 @@ Cut best_cut(int32_t nq, int32_t heads, int64_t entries) {
     return best;
 }
 
-// The same for the sizes asked for last: a call asks twice, for its workspace and for its launch, and the next call
-// mostly has the same (a search takes up to some ten microseconds).
-Cut cut_of(int32_t nq, int32_t heads, int64_t entries) {
+// The same for the sizes asked for last: the next call mostly has the same (a search takes up to some ten
+// microseconds). The best cut in some room is also the best in less that it fits into.
+Cut cut_of(int32_t nq, int32_t heads, int64_t entries, uint64_t room) {
     thread_local int64_t of[3] = {0, 0, 0};
+    thread_local uint64_t in = 0;
     thread_local Cut cut{};
-    if (of[0] != nq || of[1] != heads || of[2] != entries) {
-        cut = best_cut(nq, heads, entries);
+    const auto fits = [&] { return cut.units((uint32_t)nq) == (uint32_t)nq || cut.units((uint32_t)nq) <= room; };
+    if (of[0] != nq || of[1] != heads || of[2] != entries || in < room || !fits()) {
+        cut = best_cut(nq, heads, entries, room);
         of[0] = nq;
         of[1] = heads;
         of[2] = entries;
+        in = room;
     }
     return cut;
 }
+constexpr size_t unit_bytes(int32_t heads) { return (size_t)heads * (kD + 2) * sizeof(float); }
 
 // Parts of a query's entries in the weights' kernel, in the same way. Measured per step and per block apart from its
 // steps, in microseconds: 0.8 and 7.5 at 64 heads, 0.55 and 3.2 at 32, 0.5 and 2.6 at 16 (1024 queries over 64 .. 4096
@@ -991,14 +997,13 @@ void launch_attend_as(const AttendArgs& a, const Cut& cut, hipStream_t stream) {
 
 size_t attend_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
     if (nq <= 0 || entries <= 0) return 16;
-    const Cut cut = cut_of(nq, heads, entries);
-    const size_t units = cut.units((uint32_t)nq);
-    return units == (size_t)nq ? 16 : units * heads * (kD + 2) * sizeof(float);
+    const size_t units = cut_of(nq, heads, entries, UINT64_MAX).units((uint32_t)nq);
+    return units == (size_t)nq ? 16 : units * unit_bytes(heads);
 }
 
-hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream) {
+hipError_t launch_attend(AttendArgs a, void* ws, size_t ws_bytes, hipStream_t stream) {
     const int64_t entries = a.idx ? a.k : (a.window > 0 && a.window < a.max_n ? a.window : a.max_n);
-    const Cut cut = cut_of(a.nq, a.heads, entries);
+    const Cut cut = cut_of(a.nq, a.heads, entries, ws_bytes / unit_bytes(a.heads));
     set_page_division(a);
     const uint32_t units = cut.units((uint32_t)a.nq);
     if (units > (uint32_t)a.nq) {

@@ -43,9 +43,10 @@ struct AttendArgs {
     float* part_o;
     float* part_ml;
 };
-// entries: list slots, or the most positions a query attends to
+// the bytes of the fastest cut of such a call; a launch in fewer cuts into what fits. entries: list slots, or the most
+// positions a query attends to
 size_t attend_workspace_bytes(int32_t nq, int32_t heads, int64_t entries);
-hipError_t launch_attend(AttendArgs a, void* ws, hipStream_t stream);
+hipError_t launch_attend(AttendArgs a, void* ws, size_t ws_bytes, hipStream_t stream);
 hipError_t launch_attend_weights(AttendArgs a, const float* lse, float* weights, int64_t w_stride,
                                  hipStream_t stream);
 
