@@ -508,8 +508,9 @@ idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, cons
  *             a row may lie anywhere in that range, at the type's lowest value throughout, too.
  *   loss, lse, t_lse : device fp32 [nq] (written); lse and t_lse are the logarithms of the two sums, for
  *             idx_distill_bwd (-inf for none).
- *   ws, ws_bytes : at least idx_workspace_size(IDX_OP_DISTILL, nq, max_n, 1) bytes, 16-byte aligned; as for
- *             idx_attend.
+ *   ws, ws_bytes : device, 16-byte aligned, at least idx_workspace_size(IDX_OP_DISTILL, nq, max_n, 1) bytes (which
+ *             are enough for fewer and shorter rows, too). It holds nothing between calls; calls that may run
+ *             concurrently need separate workspaces.
  */
 idx_status idx_distill(const float* scores, int64_t score_stride, const int32_t* n_vis, int32_t nq, int64_t max_n,
                        const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,

@@ -334,9 +334,13 @@ int distill_pieces(int32_t nq, int64_t max_n) {
     return (int)(want < most ? want : (most < 1 ? 1 : most));
 }
 
+// For any number of rows up to nq and any length up to max_n: r ceil(1024 / r) pieces are below 1024 + r, of fewer than
+// 1024 rows (more are whole).
 size_t distill_workspace_bytes(int32_t nq, int64_t max_n) {
-    const int pieces = distill_pieces(nq, max_n);
-    return pieces == 1 ? 16 : (size_t)nq * pieces * sizeof(MaxSum);
+    const int64_t most = (max_n + kPiece - 1) / kPiece;
+    if (nq <= 0 || most <= 1) return 16;
+    const int64_t all = nq * most, few = 1023 + (nq < 1023 ? nq : 1023);
+    return (size_t)(all < few ? all : few) * sizeof(MaxSum);
 }
 
 hipError_t launch_distill(const DistillArgs& a, hipStream_t stream) {
