@@ -364,21 +364,25 @@ class CoreAttention:
         self.weights = torch.empty(nq, k, dtype=torch.float32, device=device)
         self.ws = workspace(IDX_OP_ATTEND, nq, k, heads, device=device)
 
-    def write(self, b: int, first: int, x: torch.Tensor) -> None:
-        """Rows x [m, 512] (bf16, not rotated) of sequence b's positions first .. first + m - 1."""
+    def write(self, b: int, first: int, x: torch.Tensor, pos: torch.Tensor | None = None) -> None:
+        """Rows x [m, 512] (bf16, not rotated) of sequence b's entries first .. first + m - 1. pos [m] (int64): the
+        positions that turn them, where an entry does not stand for the one token of its number (a cache compressed
+        along the sequence); queries are turned by token positions all the same."""
         m = x.shape[0]
         if first < 0 or first + m > self.n:
             raise ValueError(f"positions {first} .. {first + m - 1} lie outside the sequence's {self.n}")
+        if m == 0:
+            return
+        at = torch.arange(first, first + m, device=x.device)
+        y = idx_rope(x.view(m, 1, MKV_DIM), at if pos is None else pos, self.freq, layout=self.layout, mscale=self.mscale)
+        codes, scales = idx_quantize_kv(y.view(m, MKV_DIM))
         need = (first + m + self.page_size - 1) // self.page_size
         if need > self.given[b]:
             new = torch.arange(self.used, self.used + need - self.given[b], dtype=torch.int32)
             self.pages[b, self.given[b]:need] = new.to(self.pages.device)
             self.used += need - self.given[b]
             self.given[b] = need
-        pos = torch.arange(first, first + m, device=x.device)
-        y = idx_rope(x.view(m, 1, MKV_DIM), pos, self.freq, layout=self.layout, mscale=self.mscale)
-        codes, scales = idx_quantize_kv(y.view(m, MKV_DIM))
-        rows = self.pages[b].long()[pos // self.page_size] * self.page_size + pos % self.page_size
+        rows = self.pages[b].long()[at // self.page_size] * self.page_size + at % self.page_size
         self.codes.index_copy_(0, rows, codes)
         self.scales.index_copy_(0, rows, scales)
 
