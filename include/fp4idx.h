@@ -409,7 +409,7 @@ idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double fact
  *
  *   x       : device, dtype IDX_BF16 (bit patterns) or IDX_F32, [tokens][heads][dim]; a row's values are
  *             consecutive, x_token and x_head are the element strides of the other two axes (0 repeats).
- *   pos     : device int64 [tokens], any order, repeats allowed. Angles are good to 2^-21 rad up to |pos| = 2^31
+ *   pos     : device int64 [tokens], any order, repeats allowed. Angles are good to 2^-23 rad up to |pos| = 2^31
  *             (freq at most 1).
  *   freq    : device double [rot / 2].
  *   rot     : even, 2 .. 8192; offset >= 0, offset + rot <= dim.

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kRopeLds = 4096;  // (cos, sin) pairs per block: 32 KB
 constexpr int kRows = 4;        // rows of a lane in flight
+constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -37,8 +38,10 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int64_t tok0, int toks
     const int pairs = a.rot / 2;
     for (int i = threadIdx.x; i < toks * pairs; i += 256) {
         const int tk = i / pairs, pr = i - tk * pairs;
-        double turns = (double)a.pos[tok0 + tk] * (a.freq[pr] * 0.15915494309189533577);
-        turns -= rint(turns);
+        // freq / 2 pi with what its rounding leaves, and the product with pos without one: at 2^31 each is 2^-22 rad
+        const double pos = (double)a.pos[tok0 + tk], freq = a.freq[pr];
+        const double per = freq * kInv2Pi, per_low = fma(freq, kInv2Pi, -per) + freq * kInv2PiLow;
+        const double turns = fma(pos, per, -rint(pos * per)) + pos * per_low;
         float s, c;
         sincospif(2.0f * (float)turns, &s, &c);
         cs[i] = float2{c * a.mscale, (a.inverse ? -s : s) * a.mscale};
