@@ -476,8 +476,9 @@ idx_status idx_attend(const uint16_t* q, int32_t nq, int32_t heads, const uint8_
  *
  *   w_{t,i} = 1/heads sum_h exp(s_{t,h,i} - lse_{t,h})
  *
- * recomputed from lse (idx_attend's, or one that also covers other caches). The indexer is trained towards
- * it ([P3] Q&A: the divergence of the indexer from the main attention; idx_distill).
+ * recomputed from lse (idx_attend's, or one that also covers other caches), good to 2^-20 (4 + |s| + |lse|) of
+ * itself beyond the first product's own error. The indexer is trained towards it ([P3] Q&A: the divergence of the
+ * indexer from the main attention; idx_distill).
  *
  *   Arguments as for idx_attend (without a window).
  *   lse     : device fp32 [nq][heads]; a head with lse = -inf (nothing attended) adds nothing.
@@ -496,11 +497,12 @@ idx_status idx_attend_weights(const uint16_t* q, int32_t nq, int32_t heads, cons
  *   loss_t = sum_i p_i (log p_i - log q_{x_i}),  p = softmax over the teacher's entries of t_logit * inv_temp,
  *            q = softmax over the row of scores * inv_temp
  *
- * ([P3] Q&A: the indexer learns from the main attention by a KL divergence, first over all positions, then
- * over the selected ones). A row's positions are those below n_t with a score above -inf (so a row masked by
- * idx_mask_pool is normalised over its pool). The teacher's entries are the slots x_i = t_idx[t][i] that name
- * such a position and whose logit is above -inf; the others (the -1 padding) are left out, and a position given
- * twice counts twice. A row without entries has loss 0.
+ * ([P3] Q&A: the indexer learns from the main attention by a KL divergence, first over all positions, then over the
+ * selected ones. The teacher is a list of at most 2048 entries: the second phase, and the first for rows up to that
+ * length). A row's positions are those below n_t with a score above -inf (so a row masked by idx_mask_pool is
+ * normalised over its pool; not over the teacher's entries alone). The teacher's entries are the slots
+ * x_i = t_idx[t][i] that name such a position and whose logit is above -inf; the others (the -1 padding) are left
+ * out, and a position given twice counts twice. A row without entries has loss 0.
  *
  *   scores  : device fp32 [nq][score_stride], score_stride >= max_n.   n_vis, max_n : as above.
  *   t_idx   : device int32 [nq][t_stride]; t_logit : device fp32 [nq][t_stride]; k 0 .. 2048 slots, t_stride >= k.

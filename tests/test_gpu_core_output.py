@@ -112,3 +112,30 @@ def test_a_captured_layer_replays(pl):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(core.out, want[0]) and torch.equal(core.lse, want[1]), rep
+
+
+def test_parts_of_a_selection_join_by_their_lse(pl):
+    """attention over two halves of a selection, joined in the cache's frame and turned back, is attention over it all:
+    three roundings to bf16 of averages whose sizes add up to at most sum p |kv|, with the logits' own error"""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    core = pl.CoreAttention(1, 2000, 5, heads=20, k=300, page_size=64, scaling="yarn", factor=4.0, original=256.0)
+    core.write(0, 0, torch.randn(2000, 512, device="cuda", generator=g).bfloat16())
+    q = (2.0 * torch.randn(5, 20, 512, device="cuda", generator=g)).bfloat16()
+    pos = torch.arange(1995, 2000, device="cuda")
+    seq = torch.zeros(5, dtype=torch.int32, device="cuda")
+    nv = (pos + 1).int()
+    idx = torch.stack([torch.randperm(1990, device="cuda", generator=g)[:300] for _ in range(5)]).int()
+    parts = []
+    for lst in (idx[:, :100], idx[:, 100:]):
+        out, lse = core.run(q, pos, seq, nv, lst)
+        parts.append((out.double(), lse.double().clone()))
+    lse = torch.logaddexp(parts[0][1], parts[1][1])
+    joined = sum(o * (l - lse).exp()[:, :, None] for o, l in parts)
+    whole, whole_lse = core.run(q, pos, seq, nv, idx)
+    codes, scales, pages = core.codes.cpu().numpy(), core.scales.cpu().numpy(), core.pages.cpu().numpy()
+    for t in range(5):
+        _, rows = ref.entries(t, nv.tolist(), 2000, len(codes), pages=pages, page_size=64, seq=[0] * 5, idx=idx.cpu().numpy())
+        r = ref.attention(core.q[t].double().cpu().numpy(), codes, scales, core.scale, rows)
+        tol = 3 * ref.out_tolerance(r, 300) + 2 * 2.0 ** -8 * r["A"]
+        assert (np.abs((joined[t] - whole[t].double()).cpu().numpy()) <= tol).all(), t
+        assert (np.abs((lse[t] - whole_lse[t].double()).cpu().numpy()) <= 3 * ref.lse_tolerance(r, 300)).all(), t

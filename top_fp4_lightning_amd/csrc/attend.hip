@@ -23,8 +23,9 @@
 // wavefront per SIMD issues everything in order, since queries and outputs fill its registers, and what it waits for
 // adds up, none of it large: 16-byte LDS writes (52 cycles for the four wavefronts' one), transposed reads, the
 // barrier and the probabilities between the two products. Leaving any one of these out saved 1 to 14%.
-// Measured at 64 heads: 4096 queries over 512 listed rows 381 us (0.72 PFLOP/s; a block's query, first rows and output
-// take 11 of its 24 us), 514 over about 14600 rows 924 us (1.04), 8 over about 115000 rows 152 us (0.79).
+// Measured at 64 heads, in sessions that differ: 4096 queries over 512 listed rows 373 to 401 us (0.69 to 0.74 PFLOP/s; a
+// block's query, first rows and output take 11 of its 24 us), 514 over about 14600 rows 903 to 973 us (0.99 to 1.06), 8 over
+// about 115000 rows 142 us (0.85).
 // Measured and not taken: rows kept as codes in LDS and widened twice (a step 20% slower), eight wavefronts of 256
 // registers (spills, three times slower), two blocks of 32 heads per compute unit (equal), blocks that take
 // several queries (+10%), the probabilities under the next step's first product (+5%), stores past the cache (equal).
@@ -245,7 +246,7 @@ __device__ __forceinline__ void stage_query(const AttendArgs& a, int h0, QueryRo
 
 // How a call's queries are cut: those below `whole` into `parts` parts of their entries, the others into one more, so
 // that units (a part of a query each) come in whole rounds over the compute units; the longer ones come first. 514
-// queries over 16384 rows: 1005 us in 3 parts each (6.02 rounds), 924 us in 2 or 3 (1280 units).
+// queries over 16384 rows, in one session: 1005 us in 3 parts each (6.02 rounds), 924 us in 2 or 3 (1280 units).
 struct Place {
     uint32_t t, part, parts;
 };
@@ -731,7 +732,7 @@ __global__ __launch_bounds__(128 * G) void attend_join_kernel(const AttendArgs a
 // The first product alone, with heads as rows: a lane's column is one entry, whose terms it adds up over the heads.
 // Each wavefront takes 16 entries per step by itself (no barrier); the exponentials of a step run under the matrix
 // instructions of the next. Heads beyond the block's 16 NH are further rounds over the same entries, added by the lane
-// that wrote them. 1021 queries of 64 heads over about 3600 rows: 225 us (0.95 PFLOP/s), 0.8 us a step, of which the
+// that wrote them. 1021 queries of 64 heads over about 3600 rows: 213 us (1.0 PFLOP/s), 0.8 us a step, of which the
 // matrix instructions are 0.43; without reading the rows 0.68.
 template <int NH, bool LIST, bool PAGED>
 __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs a, const float* __restrict__ lse,

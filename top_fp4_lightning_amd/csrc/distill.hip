@@ -5,10 +5,11 @@
 //
 // Both directions are one pass over the row: the forward reads it (running maximum and sum per
 // thread, base 2), the gradient reads it and writes as much, with the teacher's probabilities of a piece
-// of the row laid out in LDS before the piece is streamed. They are bound by HBM: 4096 rows of 32768 scores (0.54 GB)
-// take 100 us forward and 293 us with the gradient (5.5 TB/s over both; a copy reaches 4.8). Few rows are cut into
-// pieces of at least 4096 scores, so that the compute units have about four blocks each, and joined by a second launch
-// (8 rows of 2^20: 9 and 5 us, the gradient 13).
+// of the row laid out in LDS before the piece is streamed. They are bound by HBM: 4096 whole rows of 32768 scores
+// (0.54 GB, moved three times) take 103 us forward and 294 us with the gradient (5.5 TB/s over both; a copy reaches 4.8).
+// Few rows are cut into pieces of at least 4096 scores, so that the compute units have about four blocks each, and joined
+// by a second launch
+// (8 rows of 2^20: 7 and 5 us, the gradient 13).
 #include <type_traits>
 
 #include "operators.h"

@@ -8,7 +8,7 @@
 //
 // The kernel is a copy: one read and one write of every value (the rotated part only, in place). A
 // lane moves 16, 8 or 4 bytes at a time as sizes and addresses allow, else one value or pair, of four rows at a time
-// (131 us with one). Bound by HBM: 4096 x 64 x 512 bf16 values take 101 us, 5.3 TB/s; one token of 32 heads 2.8 us.
+// (131 us with one). Bound by HBM: 4096 x 64 x 512 bf16 values take 102 us, 5.3 TB/s; one token of 32 heads 2.6 us.
 // Writing past the last-level cache gave 82 us for that call by itself, but the call that reads the result lost more
 // (chained with it 225 against 201 us; at 32 MB 38 against 27).
 #include "operators.h"

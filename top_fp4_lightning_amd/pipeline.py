@@ -32,7 +32,7 @@ with the values turned back to the query's frame. IndexerDistill trains a layer'
 score rows of the training form.
 
 All buffers are allocated once in the plan objects, so a step allocates nothing and can be
-captured in a HIP graph.
+captured in a HIP graph. (CoreAttention.write fills its cache between steps: it allocates and is not captured.)
 """
 from __future__ import annotations
 
@@ -335,10 +335,11 @@ class MainKVGather:
 
 
 class CoreAttention:
-    """Core attention over a layer's selection: the FP4 main-KV cache of `nseq` sequences of up to `n` positions in
-    pages of `page_size`, given out as the sequences grow, and the buffers of a step of `nq` queries. The last `rot`
-    values of every query and row carry the rotary position; rows are rotated before they are quantised (the page on
-    the main KV quantises after the rotation). scale defaults to 512 ** -0.5; the other arguments of rope_freqs
+    """Core attention over a layer's selection (not over the local positions beside it, which have a cache of their own:
+    the two join by their lse): the FP4 main-KV cache of `nseq` sequences of up to `n` positions in pages of `page_size`,
+    given out as the sequences grow, and the buffers of a step of `nq` queries. The last `rot` values of every query and
+    row carry the rotary position; rows are rotated before they are quantised (the page on the main KV quantises after
+    the rotation). scale defaults to 512 ** -0.5; the other arguments of rope_freqs
     stretch the context.
 
     A row is key and value at once, so what is averaged has been turned by its position p and scaled by mscale (which
@@ -367,7 +368,8 @@ class CoreAttention:
     def write(self, b: int, first: int, x: torch.Tensor, pos: torch.Tensor | None = None) -> None:
         """Rows x [m, 512] (bf16, not rotated) of sequence b's entries first .. first + m - 1. pos [m] (int64): the
         positions that turn them, where an entry does not stand for the one token of its number (a cache compressed
-        along the sequence); queries are turned by token positions all the same."""
+        along the sequence); queries are turned by token positions all the same. Runs on the current stream, one sequence a
+        call, between steps: it allocates, copies page numbers from the host and is not for a captured step."""
         m = x.shape[0]
         if first < 0 or first + m > self.n:
             raise ValueError(f"positions {first} .. {first + m - 1} lie outside the sequence's {self.n}")
