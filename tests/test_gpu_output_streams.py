@@ -68,3 +68,30 @@ def test_strided_rows_give_a_contiguous_output(fx):
     pos, (freq, _) = torch.arange(300, device="cuda"), fx.rope_freqs(64)
     y = fx.idx_rope(x, pos, freq, stream=torch.cuda.current_stream())
     assert y.is_contiguous() and torch.equal(y, fx.idx_rope(x.contiguous(), pos, freq))
+
+
+def test_an_output_read_on_the_current_stream_outlives_its_name(fx):
+    """freed while work that reads it is queued on the current stream: the next output of the side stream lies elsewhere
+    until that work is done"""
+    side = torch.cuda.Stream()
+    freq, _ = fx.rope_freqs(64)
+    pos = torch.arange(300, device="cuda")
+    x = torch.randn(300, 4, 128, device="cuda").bfloat16()
+    big, other = torch.randn(4096, 4096, device="cuda"), -x
+    want = fx.idx_rope(x, pos, freq)
+    torch.mm(big, big)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        y = fx.idx_rope(x, pos, freq, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for _ in range(20):
+            torch.mm(big, big)  # the current stream is busy; the read of y stands behind
+        got, place = y.clone(), y.data_ptr()
+        read = torch.cuda.Event()
+        read.record()
+        del y
+        z = fx.idx_rope(other, pos, freq, stream=side)
+        assert z.data_ptr() != place or read.query(), rep
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), rep
+        del z

@@ -146,15 +146,19 @@ def _stream(stream) -> int | None:
 
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """An output that a call on `stream` writes. Memory that was free on the current stream may still be read there by
-    work queued before it was freed, so the output comes from the stream that writes it (as a tensor made inside
-    `with torch.cuda.stream(stream)`: a use on another stream needs its wait and record_stream)."""
+    work queued before it was freed, so the output comes from the stream that writes it; and it goes back only behind
+    the work queued on the current stream by then, where the caller reads it after a wait."""
     if stream is None or device.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = _stream(stream)
         stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    here = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    if stream != here:
+        out.record_stream(here)
+    return out
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
