@@ -169,7 +169,7 @@ def prepare(case, seed):
     st["at"] = at.reshape(-1).contiguous()
     st["seq"] = torch.arange(seqs, device="cuda").repeat_interleave(per).int()
     st["base"] = None if st["starts"] is None else st["starts"].repeat_interleave(per)
-    st["max_n"] = int(c["n"]) + tokens  # entries a sequence may come to have
+    st["max_n"] = max(int(c["n"]), entries) + tokens  # entries a sequence may come to have
     if st["pages"] is not None and not c["ring"]:
         st["max_n"] = st["pages"].shape[1] * c["page"]
     st["freq"] = None
