@@ -53,6 +53,13 @@ typedef int32_t idx_status;
 #define IDX_OP_ATTEND 3   /* nq queries, max_n list slots or positions attended to, k = heads; see idx_attend */
 #define IDX_OP_DISTILL 4  /* nq rows of at most max_n scores; any valid k */
 
+/* formats of idx_write_rows and idx_read_rows */
+#define IDX_ROWS_MAIN 0   /* 512 values: E2M1 codes [256], an E4M3 scale per 16 [32] (idx_quantize_kv's) */
+#define IDX_ROWS_LOCAL 1  /* 512 values: E4M3 codes [512], a UE8M0 scale per 32 [16] */
+#define IDX_ROWS_KEY 2    /* 128 values: E2M1 codes [64], a UE8M0 scale per 32 [4] (an indexer row) */
+#define IDX_LOCAL_MIN_EXP (-15)
+#define IDX_LOCAL_MAX_EXP 7
+
 /* element types of idx_rope */
 #define IDX_BF16 0
 #define IDX_F32 1
@@ -531,6 +538,62 @@ idx_status idx_distill_bwd(const float* scores, int64_t score_stride, const int3
                            const int32_t* t_idx, const float* t_logit, int64_t t_stride, int32_t k, float inv_temp,
                            const float* lse, const float* t_lse, const float* dloss, float* dscores, int64_t d_stride,
                            void* stream);
+
+/*
+ * Rows at places of their own, in one of three caches (IDX_ROWS_*): the main KV, the indexer's keys, and the cache of
+ * local positions that a layer keeps beside its selection ([P1] "removing the global scale still leaves enough range":
+ * the sliding window's rows stay FP8, 512 values with a scale per 32). A local row's scale is 2^e, -15 <= e <= 7 (bytes
+ * 112 .. 134), and its codes are E4M3 ("fn"), so that every stored value, code times scale, is an fp16 number: a multiple
+ * of 2^-24 of at most 57344.
+ *
+ * An entry p, 0 <= p < max_n, of a sequence takes place p, or p % ring with ring > 0 (a cache that keeps the last `ring`
+ * entries). Place l lies in row kv_base[i] + l (kv_base NULL: row l), or with pages in row
+ * pages[s][l / page_size] * page_size + l % page_size, s = seq[i] (NULL: i). An entry outside [0, max_n), with a
+ * negative page, a sequence outside [0, nseq) or a row outside [0, rows) is not there: it is not written, and is read as
+ * zeros.
+ *
+ * idx_write_rows: for each token i < tokens, the row x_i is
+ *   normalised  : with norm != 0, y_c = x_c gamma_c / sqrt(mean x^2 + eps);
+ *   turned      : with freq, values offset .. offset + rot - 1 by pos[i] * freq (as idx_rope, layout and mscale its);
+ *   transformed : keys only: the signs and the Hadamard transform of idx_quantize_q;
+ *   quantised   : main as idx_quantize_kv, keys as idx_quantize_q; local: e the smallest exponent in range with
+ *                 448 2^e >= the group's largest magnitude, code = E4M3 of y / 2^e, to nearest, ties to the even
+ *                 code, 448 at most; zero is +0, a group of zeros has e = -15;
+ * and stored in the row of its entry at[i]. Everything up to the codes is in 64 bits (the keys' transform ends with the
+ * two fp32 roundings of idx_quantize_q), so a code is the nearest to the formula's value except within 2^-40 of it at a
+ * border. One launch that reads its places on the device: a captured step can make it.
+ *
+ *   x       : device, dtype IDX_BF16 or IDX_F32 [tokens][x_stride], dim (512, 128) consecutive values, finite.
+ *   gamma   : device fp32 [dim] or NULL (ones).   eps : above 0 with norm.
+ *   pos     : device int64 [tokens], or NULL: the entry's number at[i].   freq : device double [rot / 2], or NULL.
+ *   rot     : even, 2 .. dim; offset >= 0, offset + rot <= dim (not looked at without freq).
+ *   signs   : device int8 [128], 16-byte aligned (keys; else not looked at).
+ *   codes   : device uint8 [rows][256 | 512 | 64], 16-byte aligned.   scales : device uint8 [rows][32 | 16 | 4].
+ *   seq, at : device int32 [tokens], int64 [tokens]. Tokens of one call whose entries share a row leave unspecified
+ *             values in that row (and in no other).
+ *   max_n   : 0 .. 2^30; ring : 0 .. 2^30.   pages_stride >= ceil(min(max_n, ring) / page_size).
+ *   tokens  : 0 .. 2^24 - 1 (0 enqueues nothing).
+ */
+idx_status idx_write_rows(int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, int32_t norm,
+                          const float* gamma, double eps, const int64_t* pos, const double* freq, int32_t rot,
+                          int32_t offset, int32_t layout, double mscale, const int8_t* signs, uint8_t* codes,
+                          uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                          int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int64_t* at,
+                          int64_t max_n, int64_t ring, void* stream);
+
+/*
+ * idx_read_rows: the stored rows of entries at[i], as values: a code times its scale, exact in both output types, and
+ * with freq turned as by idx_rope (inverse != 0: back; not for keys, which are stored transformed), in fp32 and rounded
+ * once. Arguments as above; codes 8-byte aligned at least, and
+ *
+ *   out     : device, dtype IDX_BF16 or IDX_F32 [tokens][out_stride], out_stride >= dim (written; all values of a row).
+ */
+idx_status idx_read_rows(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                         const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,
+                         int32_t page_size, const int32_t* seq, const int64_t* at, int64_t max_n, int64_t ring,
+                         int64_t tokens, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
+                         int32_t layout, double mscale, int32_t inverse, void* out, int32_t dtype, int64_t out_stride,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -50,17 +50,21 @@ lib.idx_attend_weights.argtypes = [_P, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _
                                    _f32, _P, _P, _i64, _P]
 lib.idx_distill.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, _P, _P, _P, _P, _sz, _P]
 lib.idx_distill_bwd.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, _P, _P, _P, _P, _i64, _P]
+lib.idx_write_rows.argtypes = [_i32, _P, _i32, _i64, _i64, _i32, _P, _f64, _P, _P, _i32, _i32, _i32, _f64, _P, _P, _P, _i64,
+                               _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _P]
+lib.idx_read_rows.argtypes = [_i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _P, _P, _i32, _i32,
+                              _i32, _f64, _i32, _P, _i32, _i64, _P]
 for _f in ("idx_quantize_q", "idx_score_full", "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks",
            "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope",
-           "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd"):
+           "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows"):
     getattr(lib, _f).restype = _i32
 
 EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quantize_q", "idx_score_full",
            "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks", "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv",
            "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope", "idx_attend",
-           "idx_attend_weights", "idx_distill", "idx_distill_bwd")
+           "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows")
 MKV_DIM = 512
 
 
@@ -507,3 +511,104 @@ def idx_distill_bwd(scores, n_vis, max_n: int, t_idx, t_logit, lse, t_lse, dloss
     _same_gpu(scores, n_vis, t_idx, t_logit, lse, t_lse, dloss, dscores)
     _call(lib.idx_distill_bwd, *rows, inv_temp, *ins, d_ptr, d_stride, _stream(stream))
     return dscores
+
+
+# format: its number, values of a row, code bytes, scale bytes
+ROW_FORMATS = {"main": (0, MKV_DIM, MKV_DIM // 2, MKV_DIM // 16), "local": (1, MKV_DIM, MKV_DIM, MKV_DIM // 32),
+               "key": (2, DIM, DIM // 2, DIM // 32)}
+
+
+def _row_format(format, codes, scales) -> tuple:
+    """(number, values of a row, address of codes, of scales, rows) of a cache in a format"""
+    if format not in ROW_FORMATS:
+        raise ValueError(f"format must be one of {sorted(ROW_FORMATS)}, got {format!r}")
+    number, dim, width, groups = ROW_FORMATS[format]
+    codes_ptr, scales_ptr = _arg(codes, torch.uint8, None, "codes"), _arg(scales, torch.uint8, None, "scales")
+    rows, rest = divmod(codes.numel(), width)
+    if rest or scales.numel() != rows * groups:
+        raise ValueError(f"codes and scales must hold {width} and {groups} bytes for each cache row")
+    return number, dim, codes_ptr, scales_ptr, rows
+
+
+def _places(n, max_n, ring, kv_base, pages, page_size, seq) -> tuple:
+    """The arguments from kv_base to seq; n: how many kv_base and seq name."""
+    base_ptr = pages_ptr = seq_ptr = None
+    stride = nseq = 0
+    if kv_base is not None:
+        base_ptr = _arg(kv_base, torch.int64, (n,), "kv_base")
+    if pages is not None:
+        nseq = pages.shape[0]
+        pages_ptr, stride = _rows_arg(pages, torch.int32, nseq, 0, "pages")
+        most = min(max_n, ring) if ring else max_n
+        if pages.shape[1] * page_size < most:
+            raise ValueError(f"pages must cover {most} places: {pages.shape[1]} pages of {page_size}")
+        if pages_ptr == 0:  # no column: every place lies outside
+            raise ValueError("pages must not be empty")
+    if seq is not None:
+        seq_ptr = _arg(seq, torch.int32, (n,), "seq")
+    return base_ptr, pages_ptr, stride, nseq, page_size, seq_ptr
+
+
+def _turn(pos, freq, n, dim, offset, layout) -> tuple:
+    """The arguments pos, freq, rot, offset and layout (freq None: no rotation)"""
+    if freq is None:
+        return None, None, 0, 0, 0
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    rot = 2 * freq.numel()
+    freq_ptr = _arg(freq, torch.float64, (rot // 2,), "freq")
+    pos_ptr = None if pos is None else _arg(pos, torch.int64, (n,), "pos")
+    return pos_ptr, freq_ptr, rot, dim - rot if offset is None else offset, ROPE_LAYOUTS[layout]
+
+
+def _value_rows(x, tokens, dim, name) -> tuple:
+    """(address, type, row stride) of rows [tokens, dim] of consecutive values"""
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    if x.dim() != 2 or x.shape[0] != tokens or x.shape[1] != dim or x.stride(1) != 1:
+        raise ValueError(f"{name} must be [{tokens}, {dim}] with consecutive values, got {tuple(x.shape)}")
+    return x.data_ptr(), 0 if dtype is torch.bfloat16 else 1, x.stride(0) if tokens > 1 else dim
+
+
+def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, pages=None, page_size: int = 0, seq=None,
+                   ring: int = 0, gamma=None, eps: float | None = None, pos=None, freq=None, offset: int | None = None,
+                   layout: str = "half", mscale: float = 1.0, signs=None, stream=None):
+    """Rows x [tokens, 512] (keys: 128; bf16 or fp32, any row stride), normalised (with eps; times gamma), turned by
+    pos (default: at) * freq, quantised in the cache's format ("main", "local" or "key") and stored in codes and scales
+    at entries at [tokens] (int64) below max_n: rows kv_base [tokens] + entry, or of pages [nseq, ...] of page_size
+    (seq [tokens] names the page row); with ring, entry % ring takes the entry's place."""
+    number, dim, codes_ptr, scales_ptr, rows = _row_format(format, codes, scales)
+    tokens = at.shape[0]
+    x_ptr, dtype, stride = _value_rows(x, tokens, dim, "x")
+    at_ptr = _arg(at, torch.int64, (tokens,), "at")
+    where = _places(tokens, max_n, ring, kv_base, pages, page_size, seq)
+    turn = _turn(pos, freq, tokens, dim, offset, layout)
+    gamma_ptr = None if gamma is None or eps is None else _arg(gamma, torch.float32, (dim,), "gamma")
+    signs_ptr = None if signs is None else _arg(signs, torch.int8, (DIM,), "signs")
+    _same_gpu(codes, scales, x, at, kv_base, pages, seq, pos, freq, gamma, signs)
+    _call(lib.idx_write_rows, number, x_ptr, dtype, tokens, stride, int(eps is not None), gamma_ptr, eps or 0.0, *turn,
+          mscale, signs_ptr, codes_ptr, scales_ptr, rows, *where, at_ptr, max_n, ring, _stream(stream))
+    return codes, scales
+
+
+def idx_read_rows(format: str, codes, scales, at, max_n: int, kv_base=None, pages=None, page_size: int = 0, seq=None,
+                  ring: int = 0, pos=None, freq=None, offset: int | None = None, layout: str = "half",
+                  mscale: float = 1.0, inverse: bool = False, out=None, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """The stored rows of entries at [tokens] as values [tokens, 512] (keys: 128) of `dtype` or in out; with freq,
+    turned by pos (default: at) as by idx_rope. The other arguments as for idx_write_rows; entries that are not there
+    give zeros."""
+    number, dim, codes_ptr, scales_ptr, rows = _row_format(format, codes, scales)
+    tokens = at.shape[0]
+    at_ptr = _arg(at, torch.int64, (tokens,), "at")
+    where = _places(tokens, max_n, ring, kv_base, pages, page_size, seq)
+    turn = _turn(pos, freq, tokens, dim, offset, layout)
+    if out is None:
+        out = _empty((tokens, dim), dtype, at.device, stream)
+    out_ptr, number_out, stride = _value_rows(out, tokens, dim, "out")
+    if stride < dim:
+        raise ValueError("out's rows may not overlap")
+    _same_gpu(codes, scales, at, kv_base, pages, seq, pos, freq, out)
+    _call(lib.idx_read_rows, number, codes_ptr, scales_ptr, rows, *where, at_ptr, max_n, ring, tokens, *turn, mscale,
+          int(inverse), out_ptr, number_out, stride, _stream(stream))
+    return out

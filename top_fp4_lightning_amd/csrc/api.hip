@@ -8,6 +8,7 @@
 
 #include "../../include/fp4idx.h"
 #include "operators.h"
+#include "places.h"
 
 using namespace fp4idx;
 
@@ -164,6 +165,65 @@ idx_status distill_args(const char* fn, const float* scores, int64_t score_strid
     a.inv_temp = inv_temp;
     return ok();
 }
+
+// Validation of where a cache's entries lie (n: how many kv_base and seq name)
+idx_status places_args(const char* fn, int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride,
+                       int32_t nseq, int32_t page_size, const int32_t* seq, int64_t n, int64_t max_n, int64_t ring,
+                       Places& a) {
+    REQUIRE(rows >= 0 && rows <= kMaxRows, IDX_EUNSUPPORTED, "%s: rows=%lld out of [0, 2^36]", fn, (long long)rows);
+    REQUIRE(max_n >= 0 && max_n <= kMaxN, IDX_EUNSUPPORTED, "%s: max_n=%lld out of [0, 2^30]", fn, (long long)max_n);
+    REQUIRE(ring >= 0 && ring <= kMaxN, IDX_EUNSUPPORTED, "%s: ring=%lld out of [0, 2^30]", fn, (long long)ring);
+    REQUIRE(!(kv_base && pages), IDX_EINVAL, "%s: give either kv_base or pages", fn);
+    if (pages) {
+        const int64_t most = ring && ring < max_n ? ring : max_n;
+        REQUIRE(page_size >= 1, IDX_EINVAL, "%s: page_size=%d must be >= 1", fn, page_size);
+        REQUIRE(pages_stride >= (most + page_size - 1) / page_size, IDX_EINVAL,
+                "%s: pages_stride=%lld < ceil(%lld / page_size)", fn, (long long)pages_stride, (long long)most);
+        REQUIRE(nseq >= 1 && (seq || nseq >= n), IDX_EINVAL, "%s: nseq=%d page rows; without seq, %lld are used", fn,
+                nseq, (long long)n);
+    }
+    REQUIRE(aligned(kv_base, 8) && aligned(pages, 4) && aligned(seq, 4), IDX_EALIGN, "%s: misaligned pointer", fn);
+    a = Places{rows, kv_base, pages, pages_stride, nseq, seq, division_by(pages ? page_size : 0), division_by(ring), max_n};
+    return ok();
+}
+
+// Validation of a rotation of rows of `dim` values (freq NULL: none)
+idx_status turn_args(const char* fn, int32_t dim, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
+                     int32_t layout, double mscale, int32_t inverse, Turn& a) {
+    a = Turn{nullptr, nullptr, 0, 0, false, false, 1.0};
+    if (!freq) return ok();
+    REQUIRE(layout == IDX_ROPE_HALF || layout == IDX_ROPE_INTERLEAVED, IDX_EUNSUPPORTED, "%s: layout=%d", fn, layout);
+    REQUIRE(rot >= 2 && rot <= dim && rot % 2 == 0 && offset >= 0 && offset <= dim - rot, IDX_EINVAL,
+            "%s: rot=%d must be even, 2 or more, and lie in the row: offset=%d, dim=%d", fn, rot, offset, dim);
+    REQUIRE(isfinite(mscale), IDX_EINVAL, "%s: mscale is not finite", fn);
+    REQUIRE(aligned(pos, 8) && aligned(freq, 8), IDX_EALIGN, "%s: misaligned pointer", fn);
+    a = Turn{pos, freq, rot, offset, layout == IDX_ROPE_HALF, inverse != 0, mscale};
+    return ok();
+}
+
+// Validation shared by the two calls on rows at places; x: the rows written or read into
+idx_status rows_args(const char* fn, int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t stride,
+                     const uint8_t* codes, const uint8_t* scales, const int64_t* at, RowsArgs& a) {
+    REQUIRE(format >= IDX_ROWS_MAIN && format <= IDX_ROWS_KEY, IDX_EUNSUPPORTED, "%s: format=%d", fn, format);
+    REQUIRE(dtype == IDX_BF16 || dtype == IDX_F32, IDX_EUNSUPPORTED, "%s: dtype=%d", fn, dtype);
+    REQUIRE(tokens >= 0 && tokens <= kMaxRopeTokens, IDX_EUNSUPPORTED, "%s: tokens=%lld out of [0, 2^24 - 1]", fn,
+            (long long)tokens);
+    if (tokens == 0) return ok();
+    const size_t size = dtype == IDX_F32 ? 4 : 2;
+    REQUIRE(x && at && (a.places.rows == 0 || (codes && scales)), IDX_EINVAL, "%s: null pointer", fn);
+    REQUIRE(aligned(x, size) && aligned(codes, format == IDX_ROWS_LOCAL ? 8 : 4) && aligned(at, 8), IDX_EALIGN,
+            "%s: misaligned pointer", fn);
+    a.format = format;
+    a.f32 = dtype == IDX_F32;
+    a.wide = aligned(x, 16) && (stride * (int64_t)size) % 16 == 0;
+    a.tokens = tokens;
+    a.stride = stride;
+    a.at = at;
+    a.codes = const_cast<uint8_t*>(codes);
+    a.scales = const_cast<uint8_t*>(scales);
+    return ok();
+}
+constexpr int32_t row_dim(int32_t format) { return format == IDX_ROWS_KEY ? kDim : 512; }
 
 constexpr int kMaxDevices = 64;
 struct DeviceScratch {
@@ -597,6 +657,52 @@ idx_status idx_distill_bwd(const float* scores, int64_t score_stride, const int3
     a.dscores = dscores;
     a.d_stride = d_stride;
     return hip_status(launch_distill_bwd(a, (hipStream_t)stream), "idx_distill_bwd");
+}
+
+idx_status idx_write_rows(int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, int32_t norm,
+                          const float* gamma, double eps, const int64_t* pos, const double* freq, int32_t rot,
+                          int32_t offset, int32_t layout, double mscale, const int8_t* signs, uint8_t* codes,
+                          uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                          int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int64_t* at,
+                          int64_t max_n, int64_t ring, void* stream) {
+    const char* fn = "idx_write_rows";
+    RowsArgs a{};
+    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, tokens, max_n, ring, a.places);
+    if (st == IDX_OK) st = rows_args(fn, format, x, dtype, tokens, x_stride, codes, scales, at, a);
+    if (st == IDX_OK) st = turn_args(fn, row_dim(format), pos, freq, rot, offset, layout, mscale, 0, a.turn);
+    if (st != IDX_OK) return st;
+    REQUIRE(!norm || (isfinite(eps) && eps > 0.0), IDX_EINVAL, "%s: eps must be finite and above 0", fn);
+    REQUIRE(x_stride >= 0, IDX_EINVAL, "%s: x_stride=%lld is negative", fn, (long long)x_stride);
+    if (tokens == 0 || rows == 0) return ok();
+    REQUIRE(format != IDX_ROWS_KEY || signs, IDX_EINVAL, "%s: keys need signs", fn);
+    REQUIRE(aligned(codes, 16) && aligned(gamma, 4) && (format != IDX_ROWS_KEY || aligned(signs, 16)), IDX_EALIGN,
+            "%s: codes and signs must be 16-byte aligned, gamma 4-byte", fn);
+    a.x = x;
+    a.norm = norm != 0;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.signs = signs;
+    return hip_status(launch_write_rows(a, (hipStream_t)stream), fn);
+}
+
+idx_status idx_read_rows(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                         const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,
+                         int32_t page_size, const int32_t* seq, const int64_t* at, int64_t max_n, int64_t ring,
+                         int64_t tokens, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
+                         int32_t layout, double mscale, int32_t inverse, void* out, int32_t dtype, int64_t out_stride,
+                         void* stream) {
+    const char* fn = "idx_read_rows";
+    RowsArgs a{};
+    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, tokens, max_n, ring, a.places);
+    if (st == IDX_OK) st = rows_args(fn, format, out, dtype, tokens, out_stride, codes, scales, at, a);
+    if (st == IDX_OK) st = turn_args(fn, row_dim(format), pos, freq, rot, offset, layout, mscale, inverse, a.turn);
+    if (st != IDX_OK) return st;
+    REQUIRE(!freq || format != IDX_ROWS_KEY, IDX_EINVAL, "%s: keys are stored transformed and cannot be turned", fn);
+    REQUIRE(out_stride >= row_dim(format), IDX_EINVAL, "%s: out_stride=%lld < %d", fn, (long long)out_stride,
+            row_dim(format));
+    if (tokens == 0) return ok();
+    a.out = out;
+    return hip_status(launch_read_rows(a, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

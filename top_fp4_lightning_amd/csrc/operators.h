@@ -1,5 +1,5 @@
 // Internal declarations of the operators beside the indexer: rotary positions, core attention over the
-// main-KV cache, distillation of score rows (not part of the C ABI).
+// main-KV cache, distillation of score rows, cache rows at places of their own (not part of the C ABI).
 #pragma once
 
 #include "internal.h"
@@ -93,5 +93,50 @@ struct DistillArgs {
 size_t distill_workspace_bytes(int32_t nq, int64_t max_n);
 hipError_t launch_distill(const DistillArgs& a, hipStream_t stream);
 hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t stream);
+
+// cache rows at places of their own
+struct Division {  // by a number known to the host (places.h)
+    uint32_t by, mul;
+    int32_t shift;  // -1: none
+};
+struct Places {
+    int64_t rows;           // cache rows; an entry whose row is outside is not there
+    const int64_t* base;    // contiguous form: entry p lies in row base + p
+    const int32_t* pages;   // paged form: row pages[s][p / page] * page + p % page
+    int64_t pages_stride;
+    int32_t nseq;
+    const int32_t* seq;
+    Division page, ring;    // ring: entry p takes the place of entry p % ring
+    int64_t max_n;          // entries 0 .. max_n - 1
+};
+struct Turn {
+    const int64_t* pos;     // null with freq: the entry's number
+    const double* freq;     // null: none
+    int32_t rot;
+    int32_t offset;
+    bool half;
+    bool inverse;
+    double mscale;
+};
+struct RowsArgs {
+    int32_t format;
+    bool f32;               // x, out: else bf16
+    bool wide;              // x, out: rows of whole, aligned 16-byte pieces
+    int64_t tokens;
+    Places places;
+    const int64_t* at;      // [tokens]
+    Turn turn;
+    uint8_t* codes;
+    uint8_t* scales;
+    const void* x;          // write: rows, stride elements apart
+    bool norm;
+    const float* gamma;     // may be null
+    double eps;
+    const int8_t* signs;    // keys
+    void* out;              // read
+    int64_t stride;         // of x or out
+};
+hipError_t launch_write_rows(const RowsArgs& a, hipStream_t stream);
+hipError_t launch_read_rows(const RowsArgs& a, hipStream_t stream);
 
 }  // namespace fp4idx

@@ -1,0 +1,49 @@
+// Where the entries of a cache lie, and the rotary angle of a position: shared by the kernels that write, read and
+// attend to cache rows at places of their own (not part of the C ABI).
+#pragma once
+
+#include "operators.h"
+
+namespace fp4idx {
+
+// p / d for 0 <= p < 2^30 as a product: with d <= 2^b < 2 d, mul = floor(2^(31+b) / d) + 1 is below 2^32 and exceeds
+// 2^(31+b) / d by at most 1, so 2 p mul / 2^(32+b) exceeds p / d by at most p / 2^(31+b) < 1 / (2 d): the floors agree.
+inline Division division_by(int64_t d) {
+    Division v{1, 0, -1};
+    if (d <= 0) return v;
+    int b = 0;
+    while (((int64_t)1 << b) < d) ++b;
+    v.by = (uint32_t)d;
+    v.mul = (uint32_t)(((uint64_t)1 << (31 + b)) / (uint64_t)d + 1);
+    v.shift = b;
+    return v;
+}
+__device__ __forceinline__ uint32_t divided(const Division& d, uint32_t p) { return __umulhi(2 * p, d.mul) >> d.shift; }
+
+// The cache row of entry `at` (any value) of row s of the page table, or from `base` on; -1 where it has none.
+__device__ __forceinline__ int64_t row_at(const Places& a, int64_t s, int64_t base, int64_t at) {
+    if (at < 0 || at >= a.max_n) return -1;
+    uint32_t p = (uint32_t)at;
+    if (a.ring.shift >= 0) p -= divided(a.ring, p) * a.ring.by;
+    int64_t row;
+    if (a.pages) {
+        if (s < 0 || s >= a.nseq) return -1;
+        const uint32_t column = divided(a.page, p);
+        const int32_t page = a.pages[s * a.pages_stride + column];
+        if (page < 0) return -1;
+        row = (int64_t)page * a.page.by + (p - column * a.page.by);
+    } else {
+        row = (int64_t)((uint64_t)base + p);  // (a base near the type's ends wraps below 0)
+    }
+    return row >= 0 && row < a.rows ? row : -1;
+}
+
+// pos * freq / 2 pi without its whole turns, in 64 bits: freq / 2 pi with what its rounding leaves, and the product
+// with pos without one
+__device__ __forceinline__ double turns_of(int64_t pos, double freq) {
+    constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const double p = (double)pos, per = freq * kInv2Pi, low = fma(freq, kInv2Pi, -per) + freq * kInv2PiLow;
+    return fma(p, per, -rint(p * per)) + p * low;
+}
+
+}  // namespace fp4idx
