@@ -52,6 +52,7 @@ typedef int32_t idx_status;
 #define IDX_OP_TOPK 2
 #define IDX_OP_ATTEND 3   /* nq queries, max_n list slots or positions attended to, k = heads; see idx_attend */
 #define IDX_OP_DISTILL 4  /* nq rows of at most max_n scores; any valid k */
+#define IDX_OP_ATTEND_LOCAL 5  /* nq queries, max_n entries attended to, k = heads; see idx_attend_local */
 
 /* formats of idx_write_rows and idx_read_rows */
 #define IDX_ROWS_MAIN 0   /* 512 values: E2M1 codes [256], an E4M3 scale per 16 [32] (idx_quantize_kv's) */
@@ -594,6 +595,45 @@ idx_status idx_read_rows(int32_t format, const uint8_t* codes, const uint8_t* sc
                          int64_t tokens, const int64_t* pos, const double* freq, int32_t rot, int32_t offset,
                          int32_t layout, double mscale, int32_t inverse, void* out, int32_t dtype, int64_t out_stride,
                          void* stream);
+
+/*
+ * idx_attend_local: attention over the FP8 cache of local positions (IDX_ROWS_LOCAL; a row is key and value at once,
+ * shared by the heads), the other part of a layer's attention beside the selection's, joined with it and turned back:
+ *
+ *   s_{h,p} = scale * q_h . kv_p,   l_h = log sum_p exp(s_{h,p}),   o_h = sum_p exp(s_{h,p} - l_h) kv_p
+ *   lse_h = log(exp(l_h) + exp(l'_h)),   out_h = exp(l_h - lse_h) o_h + exp(l'_h - lse_h) o'_h      (with other = o', l')
+ *
+ * over the entries p that query t sees: the last min(window, n_t), or all n_t with window 0, n_t = n_vis[t] clamped to
+ * 0 .. max_n. With freq, the values offset .. offset + rot - 1 of out are then turned back by pos[t] * freq and multiplied
+ * by mscale, as idx_rope with inverse does (mscale = 1 / m takes out a factor m that the rows carry).
+ *
+ *   q       : device bf16 [nq][heads][512], 16-byte aligned; nq 0 .. 65535, heads 1 .. 128.
+ *   group   : queries t, t + 1, .. come in runs of `group` of one sequence (1, the draft positions, a chunk); divides nq.
+ *   codes, scales : device uint8 [rows][512] (16-byte aligned), [rows][16] (4-byte aligned).
+ *   kv_base : device int64 [nq / group], or pages, pages_stride, nseq, page_size and seq int32 [nq / group], and ring, as
+ *             for idx_write_rows, by runs (NULL seq: run i is of sequence i). With a ring, window is at least 1 and ring
+ *             at least window + group - 1.
+ *   n_vis, max_n, scale : as for idx_attend.
+ *   other   : device bf16 [nq][heads][512] (16-byte aligned) and other_lse fp32 [nq][heads] (natural logarithm, finite or
+ *             -inf: what other holds there has no effect), or both NULL. out may be other, and lse other_lse.
+ *   pos     : device int64 [nq] (with freq).   freq, rot, offset, layout, mscale : as for idx_write_rows.
+ *   out     : device bf16 [nq][heads][512], 16-byte aligned (written).
+ *   lse     : device fp32 [nq][heads] or NULL (written).
+ *   ws, ws_bytes : as for idx_attend: idx_workspace_size(IDX_OP_ATTEND_LOCAL, nq, entries, heads) bytes, entries = window
+ *             + group - 1 or max_n, let the call run fastest, 16 bytes are enough.
+ *
+ * An entry that is not there (as for idx_write_rows) is left out; what the cache holds there, or at entries that a query
+ * does not see, has no effect on it. A query without entries and other part gets out = 0 and lse = -inf. Products are
+ * exact in fp16 operands as for idx_attend, sums and the join fp32, probabilities have 11 bits; out is rounded once. A
+ * non-finite value in a q row makes that head's results NaN and no other's (where the query has entries).
+ */
+idx_status idx_attend_local(const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
+                            const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                            int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq,
+                            const int32_t* n_vis, int64_t max_n, int64_t window, int64_t ring, float scale,
+                            const uint16_t* other, const float* other_lse, const int64_t* pos, const double* freq,
+                            int32_t rot, int32_t offset, int32_t layout, double mscale, uint16_t* out, float* lse,
+                            void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

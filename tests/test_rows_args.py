@@ -105,3 +105,66 @@ def test_the_reference_against_the_formats():
         smaller = ref.attn_ref.e4m3(scales - 1) if format == "main" else s / 2
         at_least = (scales == 112) if format == "local" else np.zeros_like(scales, bool)
         assert ((table[-1] * smaller < top) | at_least).all()
+
+
+# idx_attend_local: q, nq, heads, group, codes, scales, rows, kv_base, pages, pages_stride, nseq, page_size, seq, n_vis,
+# max_n, window, ring, scale, other, other_lse, pos, freq, rot, offset, layout, mscale, out, lse, ws, ws_bytes, stream
+LOCAL = [FAKE, 6, 8, 3, FAKE, FAKE, 100, FAKE, None, 0, 0, 0, None, FAKE, 100, 20, 0, 0.05, FAKE, FAKE, FAKE, FAKE, 64, 448, 1,
+         1.0, FAKE, FAKE, FAKE, 16, None]
+L = dict(q=0, nq=1, heads=2, group=3, codes=4, scales=5, rows=6, base=7, pages=8, pstride=9, nseq=10, psize=11, seq=12, n_vis=13,
+         max_n=14, window=15, ring=16, scale=17, other=18, other_lse=19, pos=20, freq=21, rot=22, offset=23, layout=24, mscale=25,
+         out=26, lse=27, ws=28, ws_bytes=29)
+
+
+def test_local_attention_refusals(fx):
+    name, a = "idx_attend_local", L
+    none = list(LOCAL)
+    none[a["nq"]] = 0
+    for x in ("q", "codes", "n_vis", "out", "ws", "base"):
+        none[a[x]] = None
+    assert call(fx, name, *none)[0] == fx.IDX_OK
+    paged = (a["base"], a["pages"], a["psize"], a["pstride"], a["nseq"])
+    refuse(fx, name, LOCAL, [(a[x], None, fx.IDX_EINVAL) for x in
+                             ("q", "codes", "scales", "n_vis", "out", "other", "other_lse", "pos", "base")])
+    refuse(fx, name, LOCAL, [
+        (a["pages"], FAKE, fx.IDX_EINVAL), (a["nq"], -1, fx.IDX_EUNSUPPORTED), (a["nq"], 65538, fx.IDX_EUNSUPPORTED),
+        (a["heads"], 0, fx.IDX_EUNSUPPORTED), (a["heads"], 129, fx.IDX_EUNSUPPORTED), (a["group"], 0, fx.IDX_EINVAL),
+        (a["group"], 4, fx.IDX_EINVAL), (a["group"], -3, fx.IDX_EINVAL), (a["rows"], -1, fx.IDX_EUNSUPPORTED),
+        (a["max_n"], -1, fx.IDX_EUNSUPPORTED), (a["max_n"], (1 << 30) + 1, fx.IDX_EUNSUPPORTED),
+        (a["window"], -1, fx.IDX_EINVAL), (a["ring"], -1, fx.IDX_EUNSUPPORTED), (a["ring"], 21, fx.IDX_EINVAL),
+        ((a["ring"], a["window"]), (22, 0), fx.IDX_EINVAL), ((a["ring"], a["window"]), (22, 1 << 62), fx.IDX_EINVAL),
+        (a["scale"], NAN, fx.IDX_EINVAL), (a["scale"], INF, fx.IDX_EINVAL),
+        (paged, (None, FAKE, 0, 100, 2), fx.IDX_EINVAL), (paged, (None, FAKE, 16, 6, 2), fx.IDX_EINVAL),
+        (paged, (None, FAKE, 16, 7, 1), fx.IDX_EINVAL), ((*paged, a["ring"]), (None, FAKE, 11, 1, 2, 22), fx.IDX_EINVAL),
+        (a["rot"], 63, fx.IDX_EINVAL), (a["rot"], 514, fx.IDX_EINVAL), (a["offset"], 449, fx.IDX_EINVAL),
+        (a["layout"], 2, fx.IDX_EUNSUPPORTED), (a["mscale"], NAN, fx.IDX_EINVAL),
+        (a["ws"], None, fx.IDX_EWORKSPACE), (a["ws_bytes"], 15, fx.IDX_EWORKSPACE),
+        (a["q"], FAKE + 8, fx.IDX_EALIGN), (a["codes"], FAKE + 8, fx.IDX_EALIGN), (a["scales"], FAKE + 2, fx.IDX_EALIGN),
+        (a["n_vis"], FAKE + 2, fx.IDX_EALIGN), (a["other"], FAKE + 8, fx.IDX_EALIGN), (a["other_lse"], FAKE + 2, fx.IDX_EALIGN),
+        (a["out"], FAKE + 8, fx.IDX_EALIGN), (a["lse"], FAKE + 2, fx.IDX_EALIGN), (a["ws"], FAKE + 8, fx.IDX_EALIGN),
+        (a["base"], FAKE + 4, fx.IDX_EALIGN), (a["seq"], FAKE + 2, fx.IDX_EALIGN), (a["pos"], FAKE + 4, fx.IDX_EALIGN),
+        (a["freq"], FAKE + 4, fx.IDX_EALIGN)])
+
+
+def test_local_workspace_sizes(fx):
+    op = fx.IDX_OP_ATTEND_LOCAL
+    assert fx.workspace_size(op, 4096, 128, 64) == 16
+    assert fx.workspace_size(op, 1, 1 << 30, 128) > 16
+    assert fx.workspace_size(op, 0, 100, 1) == 16 and fx.workspace_size(op, 5, 0, 1) == 16
+    assert fx.workspace_size(op, 5, 100, 129) == 0 and fx.workspace_size(op, -1, 100, 1) == 0
+
+
+def test_local_attention_binding_refuses_on_the_host(fx):
+    q, codes = torch.zeros(4, 2, 512, dtype=torch.bfloat16), torch.zeros(10, 512, dtype=torch.uint8)
+    good = dict(q=q, codes=codes, scales=torch.zeros(10, 16, dtype=torch.uint8), n_vis=torch.zeros(4, dtype=torch.int32), max_n=10,
+                scale=1.0, out=q.clone(), ws=torch.zeros(16, dtype=torch.uint8), group=2, kv_base=torch.zeros(2, dtype=torch.int64))
+    for change, error in [
+            (dict(q=q[..., :256]), ValueError), (dict(q=q.float()), TypeError), (dict(group=3), ValueError),
+            (dict(group=0), ValueError), (dict(n_vis=good["n_vis"][:2]), ValueError), (dict(codes=codes[:9]), ValueError),
+            (dict(kv_base=torch.zeros(4, dtype=torch.int64)), ValueError), (dict(out=q[:, :1]), ValueError),
+            (dict(other=q.float(), other_lse=torch.zeros(4, 2)), TypeError),
+            (dict(other=q, other_lse=torch.zeros(4)), ValueError), (dict(lse=torch.zeros(2, 4)), ValueError),
+            (dict(freq=torch.zeros(32, dtype=torch.float64), pos=torch.zeros(2, dtype=torch.int64)), ValueError),
+            (dict(), ValueError)]:  # the last: not on a GPU
+        with pytest.raises(error):
+            fx.idx_attend_local(**{**good, **change})

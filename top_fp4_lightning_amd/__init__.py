@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4idx.so")
 
 IDX_OK, IDX_EINVAL, IDX_EALIGN, IDX_EUNSUPPORTED, IDX_EHIP, IDX_EWORKSPACE = 0, -1, -2, -3, -4, -5
-IDX_OP_BUILD_POOL, IDX_OP_TOPK, IDX_OP_ATTEND, IDX_OP_DISTILL = 1, 2, 3, 4
+IDX_OP_BUILD_POOL, IDX_OP_TOPK, IDX_OP_ATTEND, IDX_OP_DISTILL, IDX_OP_ATTEND_LOCAL = 1, 2, 3, 4, 5
 HEADS, DIM, BLOCK = 32, 128, 8
 
 if not os.path.exists(LIB_PATH):
@@ -54,17 +54,20 @@ lib.idx_write_rows.argtypes = [_i32, _P, _i32, _i64, _i64, _i32, _P, _f64, _P, _
                                _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _P]
 lib.idx_read_rows.argtypes = [_i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _P, _P, _i32, _i32,
                               _i32, _f64, _i32, _P, _i32, _i64, _P]
+lib.idx_attend_local.argtypes = [_P, _i32, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _f32,
+                                 _P, _P, _P, _P, _i32, _i32, _i32, _f64, _P, _P, _P, _sz, _P]
 for _f in ("idx_quantize_q", "idx_score_full", "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks",
            "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope",
-           "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows"):
+           "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows",
+           "idx_attend_local"):
     getattr(lib, _f).restype = _i32
 
 EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quantize_q", "idx_score_full",
            "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks", "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv",
            "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope", "idx_attend",
-           "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows")
+           "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows", "idx_attend_local")
 MKV_DIM = 512
 
 
@@ -612,3 +615,33 @@ def idx_read_rows(format: str, codes, scales, at, max_n: int, kv_base=None, page
     _call(lib.idx_read_rows, number, codes_ptr, scales_ptr, rows, *where, at_ptr, max_n, ring, tokens, *turn, mscale,
           int(inverse), out_ptr, number_out, stride, _stream(stream))
     return out
+
+
+def idx_attend_local(q, codes, scales, n_vis, max_n: int, scale: float, out, ws, lse=None, window: int = 0, ring: int = 0,
+                     group: int = 1, kv_base=None, pages=None, page_size: int = 0, seq=None, other=None, other_lse=None,
+                     pos=None, freq=None, offset: int | None = None, layout: str = "half", mscale: float = 1.0,
+                     stream=None):
+    """Attention of q [nq, heads, 512] over the FP8 cache of local positions (IDX_ROWS_LOCAL rows): the last `window`
+    visible entries or all of them, joined with `other` (out and lse of the attention over other entries) and, with freq,
+    turned back by pos [nq]. Runs of `group` queries are of one sequence; kv_base or seq [nq / group] names its rows, as for
+    idx_write_rows. ws: workspace(IDX_OP_ATTEND_LOCAL, nq, entries, heads), or another call's."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != MKV_DIM:
+        raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(shape)}")
+    nq, heads, _ = shape
+    if group < 1 or nq % group:
+        raise ValueError(f"group={group} must divide nq={nq}")
+    q_ptr = _arg(q, torch.bfloat16, None, "q")
+    _, _, codes_ptr, scales_ptr, rows = _row_format("local", codes, scales)
+    nv_ptr = _arg(n_vis, torch.int32, (nq,), "n_vis")
+    where = _places(nq // group, max_n, ring, kv_base, pages, page_size, seq)
+    other_ptr = None if other is None else _arg(other, torch.bfloat16, shape, "other")
+    other_lse_ptr = None if other_lse is None else _arg(other_lse, torch.float32, shape[:2], "other_lse")
+    turn = _turn(pos, freq, nq, MKV_DIM, offset, layout)
+    out_ptr = _arg(out, torch.bfloat16, shape, "out")
+    lse_ptr = None if lse is None else _arg(lse, torch.float32, shape[:2], "lse")
+    ws_ptr = _arg(ws, torch.uint8, None, "ws")
+    _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, other, other_lse, pos, freq, out, lse, ws)
+    _call(lib.idx_attend_local, q_ptr, nq, heads, group, codes_ptr, scales_ptr, rows, *where, nv_ptr, max_n, window, ring,
+          scale, other_ptr, other_lse_ptr, *turn, mscale, out_ptr, lse_ptr, ws_ptr, ws.numel(), _stream(stream))
+    return out, lse

@@ -95,9 +95,9 @@ hipError_t launch_distill(const DistillArgs& a, hipStream_t stream);
 hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t stream);
 
 // cache rows at places of their own
-struct Division {  // by a number known to the host (places.h)
+struct Division {  // by a number known to the host (places.h), 0: none
     uint32_t by, mul;
-    int32_t shift;  // -1: none
+    int32_t shift;
 };
 struct Places {
     int64_t rows;           // cache rows; an entry whose row is outside is not there
@@ -136,6 +136,28 @@ struct RowsArgs {
     void* out;              // read
     int64_t stride;         // of x or out
 };
+// attention over the cache of local positions, joined with another part
+struct LocalArgs {
+    const uint16_t* q;      // bf16 [nq][heads][512]
+    int32_t nq;
+    int32_t heads;
+    int32_t group;          // consecutive queries of one sequence
+    const uint8_t* codes;
+    const uint8_t* scales;
+    Places places;          // base and seq by run of `group` queries
+    const int32_t* n_vis;
+    int64_t window;         // the last `window` visible entries; 0 is all
+    float scale;
+    const uint16_t* other;  // bf16 [nq][heads][512] or null: another part of the softmax, normalised by itself
+    const float* other_lse; // [nq][heads]
+    Turn turn;              // of the result
+    uint16_t* out;
+    float* lse;             // or null
+    float* part_o;          // set by the launch
+    float* part_ml;
+};
+size_t local_workspace_bytes(int32_t nq, int32_t heads, int64_t entries);
+hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream_t stream);
 hipError_t launch_write_rows(const RowsArgs& a, hipStream_t stream);
 hipError_t launch_read_rows(const RowsArgs& a, hipStream_t stream);
 

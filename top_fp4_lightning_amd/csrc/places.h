@@ -9,8 +9,8 @@ namespace fp4idx {
 // p / d for 0 <= p < 2^30 as a product: with d <= 2^b < 2 d, mul = floor(2^(31+b) / d) + 1 is below 2^32 and exceeds
 // 2^(31+b) / d by at most 1, so 2 p mul / 2^(32+b) exceeds p / d by at most p / 2^(31+b) < 1 / (2 d): the floors agree.
 inline Division division_by(int64_t d) {
-    Division v{1, 0, -1};
-    if (d <= 0) return v;
+    Division v{0, 0, 0};
+    if (d <= 0) return v;  // none: every quotient is 0
     int b = 0;
     while (((int64_t)1 << b) < d) ++b;
     v.by = (uint32_t)d;
@@ -20,11 +20,13 @@ inline Division division_by(int64_t d) {
 }
 __device__ __forceinline__ uint32_t divided(const Division& d, uint32_t p) { return __umulhi(2 * p, d.mul) >> d.shift; }
 
+// the place of an entry below max_n
+__device__ __forceinline__ uint32_t place_of(const Places& a, uint32_t p) { return p - divided(a.ring, p) * a.ring.by; }
+
 // The cache row of entry `at` (any value) of row s of the page table, or from `base` on; -1 where it has none.
 __device__ __forceinline__ int64_t row_at(const Places& a, int64_t s, int64_t base, int64_t at) {
     if (at < 0 || at >= a.max_n) return -1;
-    uint32_t p = (uint32_t)at;
-    if (a.ring.shift >= 0) p -= divided(a.ring, p) * a.ring.by;
+    const uint32_t p = place_of(a, (uint32_t)at);
     int64_t row;
     if (a.pages) {
         if (s < 0 || s >= a.nseq) return -1;
