@@ -31,6 +31,7 @@ struct Span {
     int32_t first;  // the first entry that a row sees
     int32_t count;  // up to the last one
     bool mixed;     // not every row sees the same
+    int32_t each;   // above 0: the queries' windows lie far apart and are gone through one by one, `each` places for each
 };
 
 // entries lo .. hi - 1 that a query sees
@@ -71,76 +72,72 @@ struct LocalCut {
     uint32_t parts, tiles;  // tiles of a run
 };
 
-// The result of one row, by a wavefront: its sums (get(p, v): values 8p .. 8p + 7 of o 2^R, and L 2^R of the
-// probabilities), normalised, joined with the other part and turned.
-template <typename Get>
-__device__ __forceinline__ void finish_row(const LocalArgs& a, int64_t pair, int64_t t, float R, float L, const Get& get) {
-    const int lane = threadIdx.x & 63;
-    float w1 = L == 0.0f ? 0.0f : 1.0f / L, w2 = 0.0f;
-    float lse = L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) + R) * kLn2;
+// Weights of a row's sums o and of its other part, and the joined logarithm: L = sum 2^(s2 - R).
+struct Weights {
+    float mine, other, lse;
+};
+__device__ __forceinline__ Weights join_weights(const LocalArgs& a, int64_t pair, float R, float L) {
+    Weights w{L == 0.0f ? 0.0f : 1.0f / L, 0.0f, L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) + R) * kLn2};
     if (a.other) {
-        const float l2 = a.other_lse[pair], top = fmaxf(lse, l2);
+        const float l2 = a.other_lse[pair], top = fmaxf(w.lse, l2);
         if (top > ninf()) {
-            const float e1 = __builtin_amdgcn_exp2f((lse - top) * kLog2e), e2 = __builtin_amdgcn_exp2f((l2 - top) * kLog2e);
+            const float e1 = __builtin_amdgcn_exp2f((w.lse - top) * kLog2e), e2 = __builtin_amdgcn_exp2f((l2 - top) * kLog2e);
             const float inv = 1.0f / (e1 + e2);
-            w1 *= e1 * inv;
-            w2 = e2 * inv;
-            lse = top + __builtin_amdgcn_logf(e1 + e2) * kLn2;
+            w.mine *= e1 * inv;
+            w.other = e2 * inv;
+            w.lse = top + __builtin_amdgcn_logf(e1 + e2) * kLn2;
         }
     }
-    const bool both = !(w2 == 0.0f);  // (what lies in a part of no weight has no effect)
-    const uint16_t* other = a.other + pair * kD;
-    float v[8];
-    get(lane, v);
+    return w;
+}
+// values 8 lane .. + 7 of the other part added (what lies in one of no weight has no effect)
+__device__ __forceinline__ void add_other(const uint4& u, float weight, float (&v)[8]) {
+    if (weight == 0.0f) return;
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= w1;
-    if (both) {
-        const uint4 u = *reinterpret_cast<const uint4*>(other + 8 * lane);
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = fmaf(weight, __uint_as_float(x[i] << 16), v[2 * i]);
+        v[2 * i + 1] = fmaf(weight, __uint_as_float(x[i] & 0xffff0000u), v[2 * i + 1]);
+    }
+}
+// (cos, sin) of a pair, times the factor
+__device__ __forceinline__ float2 angle_of(const LocalArgs& a, int64_t t, int pair) {
+    float s, c;
+    sincospif(2.0f * (float)turns_of(a.turn.pos[t], a.turn.freq[pair]), &s, &c);
+    const float m = (float)a.turn.mscale;
+    return float2{c * m, (a.turn.inverse ? -s : s) * m};
+}
+// A row's values 8 lane .. + 7, turned by angles cs; row: LDS of its 512 values for pairs that lanes do not hold together
+__device__ __forceinline__ void turn_row(const LocalArgs& a, const float2* cs, float* row, float (&v)[8]) {
+    const int lane = threadIdx.x & 63, rot = a.turn.rot, pairs = rot / 2, j0 = 8 * lane - a.turn.offset;
+    if (!a.turn.half && !(a.turn.offset & 1)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = fmaf(w2, __uint_as_float(x[i] << 16), v[2 * i]);
-            v[2 * i + 1] = fmaf(w2, __uint_as_float(x[i] & 0xffff0000u), v[2 * i + 1]);
+            if (j0 + 2 * i < 0 || j0 + 2 * i >= rot) continue;
+            const float2 z = cs[(j0 >> 1) + i];
+            const float x0 = v[2 * i], x1 = v[2 * i + 1];
+            v[2 * i] = x0 * z.x - x1 * z.y;
+            v[2 * i + 1] = x1 * z.x + x0 * z.y;
         }
+        return;
     }
-    if (a.turn.freq) {
-        const int rot = a.turn.rot, pairs = rot / 2, offset = a.turn.offset;
-        const float m = (float)a.turn.mscale;
-        const int64_t pos = a.turn.pos[t];
-        float y[8];
+    *reinterpret_cast<v4f*>(row + 8 * lane) = v4f{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<v4f*>(row + 8 * lane + 4) = v4f{v[4], v[5], v[6], v[7]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = v[i];
-            const int j = 8 * lane + i - offset;
-            if (j < 0 || j >= rot) continue;
-            const bool second = a.turn.half ? j >= pairs : j & 1;
-            const int pair_of = a.turn.half ? (second ? j - pairs : j) : j >> 1;
-            const int at = offset + (a.turn.half ? (second ? j - pairs : j + pairs) : j ^ 1);
-            float s, c;
-            sincospif(2.0f * (float)turns_of(pos, a.turn.freq[pair_of]), &s, &c);
-            if (a.turn.inverse) s = -s;
-            float z;
-            if (at >> 3 == lane) {
-                z = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z = (at & 7) == k ? v[k] : z;
-            } else {
-                float f[8];
-                get(at >> 3, f);
-                z = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z = (at & 7) == k ? f[k] : z;
-                z *= w1;
-                if (both) z = fmaf(w2, __uint_as_float((uint32_t)other[at] << 16), z);
-            }
-            y[i] = m * (second ? v[i] * c + z * s : v[i] * c - z * s);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = y[i];
+    for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i;
+        if (j < 0 || j >= rot) continue;
+        const bool second = a.turn.half ? j >= pairs : j & 1;
+        const float2 z = cs[a.turn.half ? (second ? j - pairs : j) : j >> 1];
+        const float x = row[a.turn.offset + (a.turn.half ? (second ? j - pairs : j + pairs) : j ^ 1)];
+        v[i] = second ? v[i] * z.x + x * z.y : v[i] * z.x - x * z.y;
     }
-    *reinterpret_cast<uint4*>(a.out + pair * kD + 8 * lane) =
+}
+__device__ __forceinline__ void store_row(const LocalArgs& a, int64_t pair, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(a.out + pair * kD + 8 * (threadIdx.x & 63)) =
         uint4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-    if (a.lse && lane == 0) a.lse[pair] = lse;
 }
 
 // NH: rows of a block in sixteens
@@ -181,7 +178,7 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
     int2 mine;
     if (ta == tb) {
         mine = seen_by(a, t0 + ta);
-        sp = Span{mine.x, mine.y - mine.x, false};
+        sp = Span{mine.x, mine.y - mine.x, false, 0};
     } else {
         const int row = min(r0 + (lane & (kRows - 1)), a.group * a.heads - 1);
         mine = seen_by(a, t0 + row / a.heads);
@@ -195,13 +192,18 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
             lo_most = max(lo_most, __shfl_xor(lo_most, d));
             hi_least = min(hi_least, __shfl_xor(hi_least, d));
         }
-        sp = Span{lo, hi - lo, lo != lo_most || hi != hi_least};
-        if (hi == 0) sp = Span{0, 0, false};
-        sp.first = __builtin_amdgcn_readfirstlane(sp.first);
-        sp.count = __builtin_amdgcn_readfirstlane(sp.count);
-        sp.mixed = __builtin_amdgcn_readfirstlane((int)sp.mixed);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        hi = __builtin_amdgcn_readfirstlane(hi);
+        sp = Span{lo, hi - lo, __builtin_amdgcn_readfirstlane((int)(lo != lo_most || hi != hi_least)) != 0, 0};
+        if (hi == 0) sp = Span{0, 0, false, 0};
+        const int64_t each = (a.window + kTile - 1) / kTile * kTile;
+        if (a.window > 0 && each * (tb - ta + 1) < sp.count) {
+            sp.each = (int32_t)each;
+            sp.count = (int32_t)each * (tb - ta + 1);
+        }
     }
     if (w == 0 && lane < kRows) sh.sees[lane] = int2{mine.x - sp.first, mine.y - sp.first};
+    if (sp.each) __syncthreads();
     // where they lie
     int64_t base = 0;
     const int32_t* pages = nullptr;
@@ -223,7 +225,18 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
     const int i0 = step0 * kTile + w * 16 + c;      // this lane's entry of the first step
 
     // an entry's row in three stages, so that the loads of each are in flight: its place, its page, its row
-    const auto place = [&](int i) { return i < end ? (int)place_of(a.places, (uint32_t)(sp.first + i)) : -1; };
+    const auto row_in_block = [&](int query) { return max((ta + query) * a.heads - r0, 0); };
+    const auto place = [&](int i) {
+        int p = sp.first + i;
+        bool there = i < end;
+        if (sp.each) {
+            const int query = min(i, end - 1) / sp.each;
+            const int2 see = sh.sees[row_in_block(query)];
+            there &= i - query * sp.each < see.y - see.x;
+            p = sp.first + see.x + i - query * sp.each;
+        }
+        return there ? (int)place_of(a.places, (uint32_t)p) : -1;
+    };
     const auto page = [&](int p) { return PAGED ? pages[divided(a.places.page, (uint32_t)max(p, 0))] : 0; };
     const auto row_of = [&](int p, int32_t pg) {
         int64_t r;
@@ -379,10 +392,12 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
             const uint32_t seen = (uint32_t)all >> (g * 4);
             const int e = (step0 + i) * kTile + w * 16 + g * 4;
             bool odd = false;
+            const int query = sp.each ? (step0 + i) * kTile / sp.each : 0;  // of the step, where they go one by one
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
                 const float hole = fr[n].x < 0.0f ? __builtin_inff() : ninf();
-                const int2 see = sh.sees[n * 16 + c];
+                int2 see = sh.sees[n * 16 + c];
+                if (sp.each) see = (r0 + n * 16 + c) / a.heads == ta + query ? int2{INT32_MIN, INT32_MAX} : int2{0, 0};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const bool mine = ((seen >> y) & 1) && e + y >= see.x && e + y < see.y;
@@ -499,33 +514,51 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
             *reinterpret_cast<v4f*>(rows + hl * kD + (((at >> 2) ^ (hl & 31)) << 2)) = x;
         }
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int i = 0; i < kRows / 4; ++i) {
-        const int hl = w * (kRows / 4) + i;
-        if (hl >= left) break;
-        const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
-        const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]), R = -sh.fr[hl].y;
-        const auto piece = [&](int p) { return *reinterpret_cast<const v4f*>(rows + hl * kD + ((p ^ (hl & 31)) << 2)); };
-        const int64_t pair = pair0 + hl;
-        if (cut.parts > 1) {
-            const int64_t at = pair * cut.parts + part;
-            *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = piece(2 * lane);
-            *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = piece(2 * lane + 1);
-            if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
-            continue;
+    // angles of the block's queries, as many at a time as fit where the probabilities were
+    float2* cs = reinterpret_cast<float2*>(sh.p);
+    const bool finish = cut.parts == 1;
+    const int pairs = finish && a.turn.freq ? a.turn.rot / 2 : 0;
+    const int queries = tb - ta + 1, batch = pairs ? min(queries, (int)(sizeof(sh.p) / sizeof(float2)) / pairs) : queries;
+    for (int first_query = 0; first_query < queries; first_query += batch) {
+        const int some = min(batch, queries - first_query);
+        for (int i = threadIdx.x; i < some * pairs; i += 256)
+            cs[i] = angle_of(a, t0 + ta + first_query + i / pairs, i % pairs);
+        __syncthreads();
+        const int begin = max((ta + first_query) * a.heads - r0, 0);
+        const int stop = min((ta + first_query + some) * a.heads - r0, min(kRows, left));
+#pragma unroll 2
+        for (int hl = begin + ((w - begin) & 3); hl < stop; hl += 4) {
+            const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
+            const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]), R = -sh.fr[hl].y;
+            float* row = rows + hl * kD;
+            const v4f x = *reinterpret_cast<const v4f*>(row + (((2 * lane) ^ (hl & 31)) << 2));
+            const v4f y = *reinterpret_cast<const v4f*>(row + (((2 * lane + 1) ^ (hl & 31)) << 2));
+            const int64_t pair = pair0 + hl;
+            if (!finish) {
+                const int64_t at = pair * cut.parts + part;
+                *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = x;
+                *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = y;
+                if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
+                continue;
+            }
+            uint4 u{};
+            if (a.other) u = *reinterpret_cast<const uint4*>(a.other + pair * kD + 8 * lane);
+            const Weights wt = join_weights(a, pair, R, L);
+            float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
+                          y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
+            add_other(u, wt.other, v);
+            if (pairs) turn_row(a, cs + ((r0 + hl) / a.heads - ta - first_query) * pairs, row, v);
+            store_row(a, pair, v);
+            if (a.lse && lane == 0) a.lse[pair] = wt.lse;
         }
-        finish_row(a, pair, t0 + (r0 + hl) / a.heads, R, L, [&](int p, float (&v)[8]) {
-            const v4f x = piece(2 * p), y = piece(2 * p + 1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
-        });
+        if (first_query + batch < queries) __syncthreads();  // before the next angles
     }
 }
 
 // The parts of a row, a wavefront each: o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i, then as above.
 __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int parts) {
-    __shared__ float s_o[4][kD];
+    __shared__ __align__(16) float s_o[4][kD];
+    __shared__ float2 s_cs[4][kD / 2];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t pair = (int64_t)blockIdx.x * 4 + w;
     if (pair >= (int64_t)a.nq * a.heads) return;  // (no barrier below)
@@ -546,15 +579,20 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int 
         x += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[0];
         y += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[1];
     }
-    *reinterpret_cast<v4f*>(s_o[w] + 8 * lane) = x;
-    *reinterpret_cast<v4f*>(s_o[w] + 8 * lane + 4) = y;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    finish_row(a, pair, pair / a.heads, R, L, [&](int p, float (&v)[8]) {
-        const v4f u = *reinterpret_cast<const v4f*>(s_o[w] + 8 * p), t = *reinterpret_cast<const v4f*>(s_o[w] + 8 * p + 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = u[k], v[4 + k] = t[k];
-    });
+    uint4 u{};
+    if (a.other) u = *reinterpret_cast<const uint4*>(a.other + pair * kD + 8 * lane);
+    const Weights wt = join_weights(a, pair, R, L);
+    float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
+                  y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
+    add_other(u, wt.other, v);
+    if (a.turn.freq) {
+        for (int i = lane; i < a.turn.rot / 2; i += 64) s_cs[w][i] = angle_of(a, pair / a.heads, i);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        turn_row(a, s_cs[w], s_o[w], v);
+    }
+    store_row(a, pair, v);
+    if (a.lse && lane == 0) a.lse[pair] = wt.lse;
 }
 
 // Parts of a run's entries: two blocks for each of the 256 compute units, with two steps each at least.
