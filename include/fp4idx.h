@@ -609,7 +609,7 @@ idx_status idx_read_rows(int32_t format, const uint8_t* codes, const uint8_t* sc
  *
  *   q       : device bf16 [nq][heads][512], 16-byte aligned; nq 0 .. 65535, heads 1 .. 128.
  *   group   : queries t, t + 1, .. come in runs of `group` of one sequence (1, the draft positions, a chunk); divides nq.
- *   codes, scales : device uint8 [rows][512] (16-byte aligned), [rows][16] (4-byte aligned).
+ *   codes, scales : device uint8 [rows][512] (16-byte aligned), [rows][16] (4-byte aligned); rows up to 2^31 - 1.
  *   kv_base : device int64 [nq / group], or pages, pages_stride, nseq, page_size and seq int32 [nq / group], and ring, as
  *             for idx_write_rows, by runs (NULL seq: run i is of sequence i). With a ring, window is at least 1 and ring
  *             at least window + group - 1.

@@ -130,6 +130,7 @@ def test_local_attention_refusals(fx):
         (a["pages"], FAKE, fx.IDX_EINVAL), (a["nq"], -1, fx.IDX_EUNSUPPORTED), (a["nq"], 65538, fx.IDX_EUNSUPPORTED),
         (a["heads"], 0, fx.IDX_EUNSUPPORTED), (a["heads"], 129, fx.IDX_EUNSUPPORTED), (a["group"], 0, fx.IDX_EINVAL),
         (a["group"], 4, fx.IDX_EINVAL), (a["group"], -3, fx.IDX_EINVAL), (a["rows"], -1, fx.IDX_EUNSUPPORTED),
+        (a["rows"], 1 << 31, fx.IDX_EUNSUPPORTED),
         (a["max_n"], -1, fx.IDX_EUNSUPPORTED), (a["max_n"], (1 << 30) + 1, fx.IDX_EUNSUPPORTED),
         (a["window"], -1, fx.IDX_EINVAL), (a["ring"], -1, fx.IDX_EUNSUPPORTED), (a["ring"], 21, fx.IDX_EINVAL),
         ((a["ring"], a["window"]), (22, 0), fx.IDX_EINVAL), ((a["ring"], a["window"]), (22, 1 << 62), fx.IDX_EINVAL),

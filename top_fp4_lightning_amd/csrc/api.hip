@@ -722,6 +722,7 @@ idx_status idx_attend_local(const uint16_t* q, int32_t nq, int32_t heads, int32_
                                 a.places);
     if (st == IDX_OK) st = turn_args(fn, row_dim(IDX_ROWS_LOCAL), pos, freq, rot, offset, layout, mscale, 1, a.turn);
     if (st != IDX_OK) return st;
+    REQUIRE(rows <= INT32_MAX, IDX_EUNSUPPORTED, "%s: rows=%lld out of [0, 2^31 - 1]", fn, (long long)rows);
     REQUIRE(window >= 0, IDX_EINVAL, "%s: window=%lld is negative", fn, (long long)window);
     REQUIRE(!ring || (window >= 1 && window <= ring - (group - 1)), IDX_EINVAL,
             "%s: ring=%lld must hold window=%lld + group - 1=%d entries", fn, (long long)ring, (long long)window, group - 1);

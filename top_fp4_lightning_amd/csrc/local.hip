@@ -16,6 +16,7 @@
 // 7 below the largest logit that moves when one comes to lie 15 above it (both base 2). The join and the rotation are
 // fp32, rounded once.
 #include <algorithm>
+#include <string.h>
 #include <type_traits>
 
 #include "attend_common.h"
@@ -24,7 +25,7 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kMostParts = 64;  // of a run's entries
+constexpr int kMostParts = 64;  // of a run's entries (a lane each when they are joined)
 
 // what a block's rows see
 struct Span {
@@ -42,16 +43,18 @@ __device__ __forceinline__ int2 seen_by(const LocalArgs& a, int64_t t) {
     return int2{(int32_t)lo, (int32_t)n};
 }
 
-// One lane's share of a cache row: lane group g (of 4) holds values 128g .. 128g + 127 and their four scales.
+// One lane's share of a cache row: lane group g (of 4) holds values 128g .. 128g + 127 and their four scales. (Reading 64
+// bytes of a row by four neighbouring lanes, and exchanging the pieces between them, would free the address unit, but the 64
+// more instructions of a step cost more: 514 queries over 16384 entries 1248 -> 1356 us.)
 struct LocalPart {
     uint4 code[8];
     uint32_t scale;
 };
-__device__ __forceinline__ void load_piece(const LocalArgs& a, int64_t row, int g, int j, LocalPart& r) {
-    r.code[j] = *reinterpret_cast<const uint4*>(a.codes + (row < 0 ? 0 : row) * kD + g * 128 + 16 * j);
+__device__ __forceinline__ void load_piece(const LocalArgs& a, int32_t row, int g, int j, LocalPart& r) {
+    r.code[j] = *reinterpret_cast<const uint4*>(a.codes + (int64_t)max(row, 0) * kD + g * 128 + 16 * j);
 }
-__device__ __forceinline__ uint32_t load_scale(const LocalArgs& a, int64_t row, int g) {
-    return *reinterpret_cast<const uint32_t*>(a.scales + (row < 0 ? 0 : row) * 16 + g * 4);
+__device__ __forceinline__ uint32_t load_scale(const LocalArgs& a, int32_t row, int g) {
+    return *reinterpret_cast<const uint32_t*>(a.scales + (int64_t)max(row, 0) * 16 + g * 4);
 }
 // values 8x .. 8x + 7 of the part as fp16 (exact); keep: all ones, or zero for a row that is not there
 __device__ __forceinline__ h8 local_values8(const LocalPart& r, int x, uint32_t keep) {
@@ -65,21 +68,22 @@ __device__ __forceinline__ h8 local_values8(const LocalPart& r, int x, uint32_t 
     return h8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
-// How a call is cut: blocks take `rows` rows (16 or 32) of a run's heads x queries, and one of `parts` parts of the
-// entries.
+// How a call is cut: blocks of 16 nh rows of a run's heads x queries, each over one of `parts` parts of the entries; or,
+// with `queries` above 0, blocks of the window kernel over so many queries.
 struct LocalCut {
     int nh;
     uint32_t parts, tiles;  // tiles of a run
+    int queries;
 };
 
 // Weights of a row's sums o and of its other part, and the joined logarithm: L = sum 2^(s2 - R).
 struct Weights {
     float mine, other, lse;
 };
-__device__ __forceinline__ Weights join_weights(const LocalArgs& a, int64_t pair, float R, float L) {
+__device__ __forceinline__ Weights join_weights(const LocalArgs& a, float l2, float R, float L) {
     Weights w{L == 0.0f ? 0.0f : 1.0f / L, 0.0f, L == 0.0f ? ninf() : (__builtin_amdgcn_logf(L) + R) * kLn2};
     if (a.other) {
-        const float l2 = a.other_lse[pair], top = fmaxf(w.lse, l2);
+        const float top = fmaxf(w.lse, l2);
         if (top > ninf()) {
             const float e1 = __builtin_amdgcn_exp2f((w.lse - top) * kLog2e), e2 = __builtin_amdgcn_exp2f((l2 - top) * kLog2e);
             const float inv = 1.0f / (e1 + e2);
@@ -140,10 +144,16 @@ __device__ __forceinline__ void store_row(const LocalArgs& a, int64_t pair, cons
         uint4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
 }
 
-// NH: rows of a block in sixteens
+// NH: rows of a block in sixteens. Blocks of 16 rows come in pairs on a compute unit, half its registers each and one
+// step's rows in LDS: the two products of a block take turns, and the blocks cover each other's waits. The others have it
+// to themselves, and two steps' rows. (Pairs of 32 rows spill registers: 3.4 ms for 514 queries over 16384 entries.)
+template <int NH>
+constexpr bool kLocalPair = NH == 1;
+
 template <int NH>
 struct LocalShared {
-    _Float16 kv[kTile * kD];  // a step's rows; queries and outputs on their ways
+    static constexpr bool PAIR = kLocalPair<NH>;
+    _Float16 kv[(PAIR ? 1 : 2) * kTile * kD];  // rows; queries and outputs on their ways
     _Float16 p[2][NH * 16 * kPRow];
     float m[NH * 16][4];
     float l[NH * 16][4];
@@ -154,8 +164,9 @@ struct LocalShared {
 };
 
 template <int NH, bool PAGED>
-__global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a, const LocalCut cut, uint32_t units) {
+__global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kernel(const LocalArgs a, const LocalCut cut, uint32_t units) {
     __shared__ __align__(16) LocalShared<NH> sh;
+    constexpr bool PAIR = kLocalPair<NH>;
     constexpr int kRows = NH * 16;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -215,6 +226,7 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
             pages = a.places.pages + s * a.places.pages_stride;
     } else if (a.places.base) {
         base = a.places.base[run];
+        if (base <= -a.places.max_n || base >= a.places.rows) sp.count = 0;  // no entry lies in the cache
     }
     if (a.places.rows == 0) sp.count = 0;
     const int steps_all = (sp.count + kTile - 1) / kTile;
@@ -239,19 +251,24 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
     };
     const auto page = [&](int p) { return PAGED ? pages[divided(a.places.page, (uint32_t)max(p, 0))] : 0; };
     const auto row_of = [&](int p, int32_t pg) {
-        int64_t r;
+        uint32_t r;
+        bool there = p >= 0;
         if (PAGED) {
             const uint32_t in_page = (uint32_t)p - divided(a.places.page, (uint32_t)max(p, 0)) * a.places.page.by;
-            r = pg < 0 ? -1 : (int64_t)pg * a.places.page.by + in_page;
+            const uint64_t at = (uint64_t)(uint32_t)pg * a.places.page.by + in_page;
+            there &= pg >= 0 && at < (uint64_t)a.places.rows;
+            r = (uint32_t)at;
         } else {
-            r = (int64_t)((uint64_t)base + (uint32_t)p);
+            // the base lies in (-2^30, rows) and p in [0, 2^30): a sum below zero wraps above any row
+            r = (uint32_t)base + (uint32_t)p;
+            there &= r < (uint32_t)a.places.rows;
         }
-        return p >= 0 && r >= 0 && r < a.places.rows ? r : (int64_t)-1;
+        return there ? (int32_t)r : -1;
     };
 
     LocalPart kv;
     uint32_t scale1 = 0;
-    int64_t row = -1;
+    int32_t row = -1;
     int place1 = -1, place2 = -1;
     int32_t page1 = 0;
     if (steps > 0) {
@@ -265,6 +282,12 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
         for (int j = 0; j < 8; ++j) load_piece(a, row, g, j, kv);
         kv.scale = load_scale(a, row, g);
     }
+    // angles of the result, while the rows are on their way: one a thread, where they are so few
+    const int queries = tb - ta + 1, pairs = cut.parts == 1 && a.turn.freq ? a.turn.rot / 2 : 0;
+    const bool early = queries * pairs <= 256;
+    float2 angle{};
+    if (early && (int)threadIdx.x < queries * pairs)
+        angle = angle_of(a, t0 + ta + (int)threadIdx.x / pairs, (int)threadIdx.x % pairs);
     stage_query<kRows>(a.scale, left, qr, sh.kv, sh.fr);
     __syncthreads();
     h8 q[NH][15];
@@ -275,6 +298,11 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
         for (int x = 0; x < 15; ++x) q[n][x] = *reinterpret_cast<const h8*>(at + x * 8);
         const h8 ql = *reinterpret_cast<const h8*>(at + 15 * 8);
         if (w == 0) *reinterpret_cast<h8*>(sh.q + (n * 16 + c) * kQRow + g * 8) = ql;
+        if constexpr (!PAIR) {
+            // in the accumulation half of the register file: matrix operands only
+#pragma unroll
+            for (int x = 0; x < 15; ++x) asm volatile("" : "+a"(q[n][x]));
+        }
     }
     __syncthreads();  // before kv takes rows
 
@@ -357,100 +385,57 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
         __syncthreads();
     };
 
-    // The first product of step i: rows widened, multiplied, left in LDS; then their probabilities.
-    const auto first_product = [&](int i, auto first_step) {
-        constexpr bool kFirst = decltype(first_step)::value;
-        const uint32_t keep = row >= 0 ? ~0u : 0u;
-        const bool there = row >= 0;
-        const int64_t row1 = row_of(place1, page1);
-        place1 = place2;
-        page1 = page(place2);
-        place2 = place(i0 + (i + 3) * kTile);
-        h8 k = local_values8(kv, 0, keep), ql[NH];
+    // The logits of step i at entries that a row does not see; seen: which of this lane's four have a row; at: where the
+    // step's rows lie.
+    const auto mask_step = [&](int i, uint32_t seen, const float2 (&fr)[NH], int at_rows) {
+        const int e = (step0 + i) * kTile + w * 16 + g * 4;
+        const int query = sp.each ? (step0 + i) * kTile / sp.each : 0;  // of the step, where they go one by one
+        bool odd = false;
 #pragma unroll
-        for (int n = 0; n < NH; ++n) s[n] = v4f{};
+        for (int n = 0; n < NH; ++n) {
+            const float hole = fr[n].x < 0.0f ? __builtin_inff() : ninf();
+            int2 see = sh.sees[n * 16 + c];
+            if (sp.each) see = (r0 + n * 16 + c) / a.heads == ta + query ? int2{INT32_MIN, INT32_MAX} : int2{0, 0};
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const h8 kx = k;
-            *reinterpret_cast<h8*>(sh.kv + (at_in ^ ((x & 7) * 8)) + (x >> 3) * 64) = kx;
-            if (x < 15) k = local_values8(kv, x + 1, keep);
-            if (x == 3) scale1 = load_scale(a, row1, g);
-            if (x & 1) load_piece(a, row1, g, x >> 1, kv);
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                if (x == 14) ql[n] = *reinterpret_cast<const h8*>(sh.q + (n * 16 + c) * kQRow + g * 8);
-                s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, x < 15 ? q[n][x < 15 ? x : 0] : ql[n], s[n], 0, 0, 0);
+            for (int y = 0; y < 4; ++y) {
+                const bool mine = ((seen >> y) & 1) && e + y >= see.x && e + y < see.y;
+                odd |= !mine && !(fabsf(s[n][y]) < __builtin_inff());
+                s[n][y] = mine ? s[n][y] : hole;
             }
         }
-        row = row1;
-        kv.scale = scale1;
-        float2 fr[NH];
-#pragma unroll
-        for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
-        const uint64_t all = __ballot(there);
-        if (all != ~0ull || sp.mixed) {
-            const uint32_t seen = (uint32_t)all >> (g * 4);
-            const int e = (step0 + i) * kTile + w * 16 + g * 4;
-            bool odd = false;
-            const int query = sp.each ? (step0 + i) * kTile / sp.each : 0;  // of the step, where they go one by one
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                const float hole = fr[n].x < 0.0f ? __builtin_inff() : ninf();
-                int2 see = sh.sees[n * 16 + c];
-                if (sp.each) see = (r0 + n * 16 + c) / a.heads == ta + query ? int2{INT32_MIN, INT32_MAX} : int2{0, 0};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const bool mine = ((seen >> y) & 1) && e + y >= see.x && e + y < see.y;
-                    odd |= !mine && !(fabsf(s[n][y]) < __builtin_inff());
-                    s[n][y] = mine ? s[n][y] : hole;
-                }
-            }
-            // A row that holds NaN codes and that some of the block's queries do not see: for the second product it is
-            // zeros (those that see it have a NaN probability). A query's own NaN or infinity looks the same; then
-            // nothing is found here.
-            if (__any(odd)) {
+        // A row that holds NaN codes and that some of the block's queries do not see: for the second product it is
+        // zeros (those that see it have a NaN probability). A query's own NaN or infinity looks the same; then
+        // nothing is found here.
+        if (__any(odd)) {
 #pragma unroll 1
-                for (int j = 0; j < 16; ++j) {
-                    h8* at = reinterpret_cast<h8*>(sh.kv + (w * 16 + j) * kD + lane * 8);
-                    const h8 v = *at;
-                    bool bad = false;
+            for (int j = 0; j < 16; ++j) {
+                h8* at = reinterpret_cast<h8*>(sh.kv + at_rows + (w * 16 + j) * kD + lane * 8);
+                const h8 v = *at;
+                bool bad = false;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) bad |= !(fabsf((float)v[y]) < __builtin_inff());
-                    if (__any(bad)) *at = h8{};
-                }
+                for (int y = 0; y < 8; ++y) bad |= !(fabsf((float)v[y]) < __builtin_inff());
+                if (__any(bad)) *at = h8{};
             }
         }
-        bool over = false;
-        if constexpr (kFirst) {
-            // the first step sets R
-            float r[NH];
-            new_reference(fr, r);
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                fr[n].y = -r[n];
-                if (w == 0 && g == 0) sh.fr[n * 16 + c].y = -r[n];
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NH; ++n) over |= probabilities(n, fr[n], i);
-        const int any = __any(over);
-        sh.over[i & 1][w] = any;
-        __syncthreads();
     };
-    const auto second_product = [&](int i) {
-        const int4 ov = *reinterpret_cast<const int4*>(sh.over[i & 1]);
-        if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) rebase(i);
-#pragma unroll
-        for (int n = 0; n < NH; ++n) l[n] += sum[n];
-        const _Float16* prob = sh.p[i & 1] + oc * kPRow + og * 8;
-        // a transposed read of unit y's eight entries of this lane's value
+
+    // Turn i of the pipe, after a barrier: the first product of step i + 1 (its rows widened, multiplied, left in LDS) and
+    // the second product of step i, then the probabilities of step i + 1 under the rest of the second product. Widening,
+    // exponentials, LDS and loads run under the matrix instructions.
+    const auto turn = [&](auto pv, auto qk, auto first_step, int i) {
+        constexpr bool kPv = decltype(pv)::value, kQk = decltype(qk)::value, kFirst = decltype(first_step)::value;
+        const int buf = i & 1;
+        const int in = at_in ^ (PAIR || buf ? 0 : kTile * kD);
+        const int out = at_out ^ (!PAIR && buf ? kTile * kD : 0);
+        const _Float16* prob = sh.p[buf] + oc * kPRow + og * 8;
+        // a transposed read of unit y's eight entries (below) of this lane's value
         const auto rows8 = [&](int y) {
             int lo, hi, at;
             if constexpr (kWide) {
-                lo = at_out ^ ((y & 1) * 32), hi = at_out ^ ((y & 1) * 32 + 4 * kD + 8);
+                lo = out ^ ((y & 1) * 32), hi = out ^ ((y & 1) * 32 + 4 * kD + 8);
                 at = (y >> 2) * 16 * kD + ((y >> 1) & 1) * 64;
             } else {
-                lo = at_out ^ ((y & 3) * 16), hi = at_out ^ ((y & 3) * 16 + 4 * kD + 8);
+                lo = out ^ ((y & 3) * 16), hi = out ^ ((y & 3) * 16 + 4 * kD + 8);
                 at = (y >> 3) * 32 * kD + ((y >> 2) & 1) * 64;
             }
             const hv4 l4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(sh.kv + lo + at));
@@ -460,30 +445,136 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
             __builtin_memcpy((char*)&v + 8, &h4, 8);
             return v;
         };
+        h8 k, v[4], p[kOh], ql[NH];
+        int4 ov{0, 0, 0, 0};
+        if constexpr (kPv) {
+            ov = *reinterpret_cast<const int4*>(sh.over[buf]);
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            const h8 v = rows8(y);
+            for (int n = 0; n < kOh; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow);
+            v[0] = rows8(0);
+        }
+        const bool there = row >= 0;
+        const uint32_t keep = there ? ~0u : 0u;
+        int32_t row1 = -1;
+        if constexpr (kQk) {
+            row1 = row_of(place1, page1);
+            place1 = place2;
+            page1 = page(place2);
+            place2 = place(i0 + (i + 4) * kTile);
+            k = local_values8(kv, 0, keep);
+        }
+        if constexpr (kPv) {
+            if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
+                rebase(i);
+#pragma unroll
+                for (int n = 0; n < kOh; ++n) p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow);
+            }
+#pragma unroll
+            for (int n = 0; n < NH; ++n) l[n] += sum[n];
+        }
+        // y-th unit of the second product: entries 32 (y / 8) .. + 31 of values 16 (y % 8) .. + 15, or, wide, entries
+        // 16 (y / 4) .. + 15 of values 32 (y % 4) .. + 31
+        const auto unit = [&](int y) {
+            // operands are read one unit ahead, three where units follow each other closely
+            const auto ahead = [](int u) { return u < 0 ? 0 : u + 1 + (u >= 4) + (u >= 6); };
+#pragma unroll
+            for (int r = 1; r < 16; ++r)
+                if (r > ahead(y - 1) && r <= ahead(y)) v[r & 3] = rows8(r);
 #pragma unroll
             for (int n = 0; n < kOh; ++n) {
                 if constexpr (kWide) {
-                    const h8 p = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow + (y >> 2) * 16);
-                    o[n][y & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p, o[n][y & 3], 0, 0, 0);
+                    o[n][y & 3] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[y & 3], p[n], o[n][y & 3], 0, 0, 0);
+                    if ((y & 3) == 3 && y < 15)
+                        p[n] = *reinterpret_cast<const h8*>(prob + n * 32 * kPRow + ((y >> 2) + 1) * 16);
                 } else {
-                    const h8 p = *reinterpret_cast<const h8*>(prob + (y >> 3) * 32);
-                    o[n][y & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o[n][y & 7], 0, 0, 0);
+                    o[n][y & 7] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[y & 3], p[n], o[n][y & 7], 0, 0, 0);
+                    if (y == 7) p[n] = *reinterpret_cast<const h8*>(prob + 32);
                 }
             }
+        };
+        if constexpr (kQk) {
+#pragma unroll
+            for (int n = 0; n < NH; ++n) s[n] = v4f{};
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            if constexpr (kPv) {
+                if (!kQk || (x & 1)) unit(kQk ? x >> 1 : x);
+            }
+            if constexpr (kQk) {
+                const h8 kx = k;
+                *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 7) * 8)) + (x >> 3) * 64) = kx;
+                if (x < 15) k = local_values8(kv, x + 1, keep);
+                if (x == 3) scale1 = load_scale(a, row1, g);
+                if (x & 1) load_piece(a, row1, g, x >> 1, kv);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    if (x == 14) ql[n] = *reinterpret_cast<const h8*>(sh.q + (n * 16 + c) * kQRow + g * 8);
+                    s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kx, x < 15 ? q[n][x < 15 ? x : 0] : ql[n], s[n], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < NH * kQk + kOh * (kPv && (x & 1)); ++y) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kQk) {
+            row = row1;
+            kv.scale = scale1;
+            float2 fr[NH];
+#pragma unroll
+            for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
+            const uint64_t all = __ballot(there);
+            if (all != ~0ull || sp.mixed) mask_step(i + 1, (uint32_t)all >> (g * 4), fr, in - at_in);
+            bool over = false;
+            if constexpr (kFirst) {
+                // the first step sets R
+                float r[NH];
+                new_reference(fr, r);
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    fr[n].y = -r[n];
+                    if (w == 0 && g == 0) sh.fr[n * 16 + c].y = -r[n];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                if constexpr (kPv) {
+#pragma unroll
+                    for (int y = 8 + n * 8 / NH; y < 8 + (n + 1) * 8 / NH; ++y) unit(y);
+                }
+                over |= probabilities(n, fr[n], i + 1);
+                if constexpr (kPv) {
+#pragma unroll
+                    for (int y = 0; y < 8 * kOh / NH; ++y) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, 3 * NH / kOh, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            const int any = __any(over);
+            sh.over[buf ^ 1][w] = any;
+            __syncthreads();
         }
     };
 
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     if (steps > 0) {
-        first_product(0, std::true_type{});
-        for (int i = 0; i + 1 < steps; ++i) {
-            second_product(i);
-            __syncthreads();  // before the next step's rows take the place
-            first_product(i + 1, std::false_type{});
+        turn(no, yes, yes, -1);
+        if constexpr (PAIR) {
+            for (int i = 0; i + 1 < steps; ++i) {
+                turn(yes, no, no, i);
+                __syncthreads();  // before the next step's rows take the place
+                turn(no, yes, no, i);
+            }
+        } else {
+            for (int i = 0; i + 1 < steps; ++i) turn(yes, yes, no, i);
         }
-        second_product(steps - 1);
+        turn(yes, no, no, steps - 1);
     }
 
     // the sum over the four lane groups and the four wavefronts
@@ -517,53 +608,82 @@ __global__ __launch_bounds__(256, 2) void attend_local_kernel(const LocalArgs a,
     // angles of the block's queries, as many at a time as fit where the probabilities were
     float2* cs = reinterpret_cast<float2*>(sh.p);
     const bool finish = cut.parts == 1;
-    const int pairs = finish && a.turn.freq ? a.turn.rot / 2 : 0;
-    const int queries = tb - ta + 1, batch = pairs ? min(queries, (int)(sizeof(sh.p) / sizeof(float2)) / pairs) : queries;
+    const int batch = early ? queries : pairs ? min(queries, (int)(sizeof(sh.p) / sizeof(float2)) / pairs) : queries;
     for (int first_query = 0; first_query < queries; first_query += batch) {
         const int some = min(batch, queries - first_query);
-        for (int i = threadIdx.x; i < some * pairs; i += 256)
-            cs[i] = angle_of(a, t0 + ta + first_query + i / pairs, i % pairs);
+        if (early) {
+            if ((int)threadIdx.x < queries * pairs) cs[threadIdx.x] = angle;
+        } else {
+            for (int i = threadIdx.x; i < some * pairs; i += 256)
+                cs[i] = angle_of(a, t0 + ta + first_query + i / pairs, i % pairs);
+        }
         __syncthreads();
         const int begin = max((ta + first_query) * a.heads - r0, 0);
         const int stop = min((ta + first_query + some) * a.heads - r0, min(kRows, left));
-#pragma unroll 2
-        for (int hl = begin + ((w - begin) & 3); hl < stop; hl += 4) {
-            const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
-            const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]), R = -sh.fr[hl].y;
-            float* row = rows + hl * kD;
-            const v4f x = *reinterpret_cast<const v4f*>(row + (((2 * lane) ^ (hl & 31)) << 2));
-            const v4f y = *reinterpret_cast<const v4f*>(row + (((2 * lane + 1) ^ (hl & 31)) << 2));
-            const int64_t pair = pair0 + hl;
-            if (!finish) {
-                const int64_t at = pair * cut.parts + part;
-                *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = x;
-                *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = y;
-                if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
-                continue;
+        // four rows at a time, the other part's on their way together
+        for (int h0 = begin + ((w - begin) & 3); h0 < stop; h0 += 16) {
+            uint4 u[4] = {};
+            float l2[4] = {};
+            if (finish && a.other) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (h0 + 4 * k >= stop) break;
+                    u[k] = *reinterpret_cast<const uint4*>(a.other + (pair0 + h0 + 4 * k) * kD + 8 * lane);
+                    l2[k] = a.other_lse[pair0 + h0 + 4 * k];
+                }
             }
-            uint4 u{};
-            if (a.other) u = *reinterpret_cast<const uint4*>(a.other + pair * kD + 8 * lane);
-            const Weights wt = join_weights(a, pair, R, L);
-            float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
-                          y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
-            add_other(u, wt.other, v);
-            if (pairs) turn_row(a, cs + ((r0 + hl) / a.heads - ta - first_query) * pairs, row, v);
-            store_row(a, pair, v);
-            if (a.lse && lane == 0) a.lse[pair] = wt.lse;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int hl = h0 + 4 * k;
+                if (hl >= stop) break;
+                const v4f lv = *reinterpret_cast<const v4f*>(sh.l[hl]);
+                const float L = (lv[0] + lv[1]) + (lv[2] + lv[3]), R = -sh.fr[hl].y;
+                float* row = rows + hl * kD;
+                const v4f x = *reinterpret_cast<const v4f*>(row + (((2 * lane) ^ (hl & 31)) << 2));
+                const v4f y = *reinterpret_cast<const v4f*>(row + (((2 * lane + 1) ^ (hl & 31)) << 2));
+                const int64_t pair = pair0 + hl;
+                if (!finish) {
+                    const int64_t at = pair * cut.parts + part;
+                    *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = x;
+                    *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = y;
+                    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
+                    continue;
+                }
+                const Weights wt = join_weights(a, l2[k], R, L);
+                float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
+                              y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
+                add_other(u[k], wt.other, v);
+                if (pairs) turn_row(a, cs + ((r0 + hl) / a.heads - ta - first_query) * pairs, row, v);
+                store_row(a, pair, v);
+                if (a.lse && lane == 0) a.lse[pair] = wt.lse;
+            }
         }
         if (first_query + batch < queries) __syncthreads();  // before the next angles
     }
 }
 
-// The parts of a row, a wavefront each: o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i, then as above.
+// The parts of a row, joined by G wavefronts that take every G-th (o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i), then
+// as above.
+template <int G>
 __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int parts) {
+    constexpr int kRows = 4 / G;  // of a block
     __shared__ __align__(16) float s_o[4][kD];
-    __shared__ float2 s_cs[4][kD / 2];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t pair = (int64_t)blockIdx.x * 4 + w;
-    if (pair >= (int64_t)a.nq * a.heads) return;  // (no barrier below)
+    __shared__ float2 s_cs[kRows][kD / 2];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, own = w / G, take = w % G;
+    const int64_t all = (int64_t)a.nq * a.heads, at_row = (int64_t)blockIdx.x * kRows + own;
+    const bool live = at_row < all;
+    const int64_t pair = live ? at_row : all - 1;
     float2 ml{kNone, 0.0f};
     if (lane < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (pair * parts + lane));
+    uint4 u{};
+    float l2 = 0.0f;
+    if (take == 0 && a.other) {
+        u = *reinterpret_cast<const uint4*>(a.other + pair * kD + 8 * lane);
+        l2 = a.other_lse[pair];
+    }
+    if (a.turn.freq) {
+        for (int i = take * 64 + lane; i < a.turn.rot / 2; i += 64 * G) s_cs[own][i] = angle_of(a, pair / a.heads, i);
+    }
     float R = ml.x;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) R = fmaxf(R, __shfl_xor(R, d));
@@ -574,71 +694,504 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int 
     const float* po = a.part_o + pair * parts * kD + 8 * lane;
     v4f x{}, y{};
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
+    for (int i = take; i < parts; i += G) {
         const float fi = __shfl(f, i);
         x += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[0];
         y += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[1];
     }
-    uint4 u{};
-    if (a.other) u = *reinterpret_cast<const uint4*>(a.other + pair * kD + 8 * lane);
-    const Weights wt = join_weights(a, pair, R, L);
+    if constexpr (G > 1) {
+        *reinterpret_cast<v4f*>(s_o[w] + 8 * lane) = x;
+        *reinterpret_cast<v4f*>(s_o[w] + 8 * lane + 4) = y;
+    }
+    __syncthreads();
+    if (take || !live) return;
+    if constexpr (G > 1) {
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+            x += *reinterpret_cast<const v4f*>(s_o[w + k] + 8 * lane);
+            y += *reinterpret_cast<const v4f*>(s_o[w + k] + 8 * lane + 4);
+        }
+    }
+    const Weights wt = join_weights(a, l2, R, L);
     float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
                   y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
     add_other(u, wt.other, v);
-    if (a.turn.freq) {
-        for (int i = lane; i < a.turn.rot / 2; i += 64) s_cs[w][i] = angle_of(a, pair / a.heads, i);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        turn_row(a, s_cs[w], s_o[w], v);
-    }
+    if (a.turn.freq) turn_row(a, s_cs[own], s_o[w], v);
     store_row(a, pair, v);
     if (a.lse && lane == 0) a.lse[pair] = wt.lse;
 }
 
-// Parts of a run's entries: two blocks for each of the 256 compute units, with two steps each at least.
-int64_t parts_for(int64_t blocks, int64_t entries) {
-    const int64_t steps = (entries + kTile - 1) / kTile;
-    return std::max<int64_t>(1, std::min<int64_t>({(int64_t)kMostParts, 512 / std::max<int64_t>(blocks, 1), steps / 2}));
+// ---- windows of queries that follow each other ----
+// Consecutive queries of a sequence see nearly the same window, so a block takes as many of them as fit: their entries are
+// widened into LDS once, and then its wavefronts take 16 rows at a time, each by itself (no barrier): the products with all
+// entries, an exact softmax, the second product with the probabilities where the first left them, half of the values at a
+// time, and the result. The order in which a product adds up its entries is free, so the probabilities of two tiles of 16
+// entries are the second product's operand as they lie, and the values' transposed reads go by that order.
+constexpr int kWinTiles = 9;                   // of 16 entries
+constexpr int kWinKeys = 16 * kWinTiles;       // 144 rows of 1 KB
+constexpr int kWinWaves = 8;
+constexpr int kWinCuts = 2;                    // of the values, for the second product
+constexpr int kWinAngles = 1536;
+constexpr int kWinQueries = 64;                // at most, a lane each
+
+struct WindowShared {
+    _Float16 kv[kWinKeys * kD];  // a row's 16-byte piece p lies at p ^ win_swap(row)
+    float2 cs[kWinAngles];
+    int2 sees[kWinQueries];
+    uint32_t absent[5], bad[5];  // a bit for each entry: no row, NaN codes
+};
+// Rows of a transposed read (4) and of an ordinary one (16) exchanged so that they lie in different banks.
+__device__ __forceinline__ int win_swap(int row) { return (row & 3) * 2 + ((row >> 2) & 1) * 8 + ((row >> 3) & 1); }
+
+__global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const LocalArgs a, int queries, uint32_t per_run,
+                                                                       uint32_t units) {
+    __shared__ __align__(16) WindowShared sh;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int g = lane >> 4, c = lane & 15;
+    const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= share || unit >= units) return;
+    const int64_t run = unit / per_run;
+    const int q0 = (int)(unit % per_run) * queries, some = min(queries, a.group - q0);
+    const int64_t t0 = run * a.group + q0;
+    int64_t base = 0, s = 0;
+    bool cached = a.places.rows > 0;
+    if (a.places.pages) {
+        s = a.places.seq ? (int64_t)a.places.seq[run] : run;
+        cached &= s >= 0 && s < a.places.nseq;
+    } else if (a.places.base) {
+        base = a.places.base[run];
+    }
+    const int2 mine = lane < some ? seen_by(a, t0 + lane) : int2{0, 0};
+    const bool none = mine.y <= mine.x || !cached;
+    const int pairs = a.turn.freq ? a.turn.rot / 2 : 0;
+
+    // As many queries at a time as see kWinKeys entries together: all of them, unless their lengths do not follow each
+    // other.
+    for (int begin = 0; begin < some;) {
+        int lo = INT32_MAX, hi = 0, stop = begin;
+        {
+            const bool there = lane >= begin && !none;
+            int l = there ? mine.x : INT32_MAX, h = there ? mine.y : 0;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                l = min(l, __shfl_xor(l, d));
+                h = max(h, __shfl_xor(h, d));
+            }
+            lo = __builtin_amdgcn_readfirstlane(l);
+            hi = __builtin_amdgcn_readfirstlane(h);
+        }
+        if (hi == 0 || hi - lo <= kWinKeys) {
+            stop = some;
+        } else {
+            lo = INT32_MAX, hi = 0;
+            for (; stop < some; ++stop) {
+                const int l = __builtin_amdgcn_readlane(none ? INT32_MAX : mine.x, stop);
+                const int h = __builtin_amdgcn_readlane(none ? 0 : mine.y, stop);
+                const int l2 = min(lo, l), h2 = max(hi, h);
+                if (h2 > 0 && h2 - l2 > kWinKeys) break;
+                lo = l2, hi = h2;
+            }
+        }
+        const int first = hi ? lo : 0, count = hi ? hi - lo : 0;
+        if (threadIdx.x < 5) sh.absent[threadIdx.x] = sh.bad[threadIdx.x] = 0;
+        if (w == 0) sh.sees[lane] = none ? int2{0, 0} : int2{mine.x - first, mine.y - first};
+        __syncthreads();
+
+        // the entries: 16 values a lane, two rows a wavefront
+        constexpr int kReads = (kWinKeys + 2 * kWinWaves - 1) / (2 * kWinWaves);
+        {
+            const int part = lane & 31;
+            int64_t row[kReads];
+            uint4 code[kReads];
+            uint32_t scale[kReads];
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) {
+                const int e = (i * kWinWaves + w) * 2 + (lane >> 5);
+                row[i] = e < count ? row_at(a.places, s, base, (int64_t)first + e) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) {
+                code[i] = uint4{0, 0, 0, 0};
+                scale[i] = 0;
+                if (row[i] >= 0) {
+                    code[i] = *reinterpret_cast<const uint4*>(a.codes + row[i] * kD + 16 * part);
+                    scale[i] = a.scales[row[i] * 16 + (part >> 1)];
+                }
+            }
+            for (int i = threadIdx.x; i < (stop - begin) * pairs; i += 64 * kWinWaves)
+                sh.cs[i] = angle_of(a, t0 + begin + i / pairs, i % pairs);
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) {
+                const int e = (i * kWinWaves + w) * 2 + (lane >> 5);
+                if (kWinKeys % (2 * kWinWaves) && (i * kWinWaves + w) * 2 >= kWinKeys) continue;
+                const float by = __uint_as_float(scale[i] << 23);
+                const uint32_t word[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+                h8 v[2];
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const h2 x = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[j], by, false);
+                    const h2 y = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word[j], by, true);
+                    v[j >> 1][(j & 1) * 4] = x[0], v[j >> 1][(j & 1) * 4 + 1] = x[1];
+                    v[j >> 1][(j & 1) * 4 + 2] = y[0], v[j >> 1][(j & 1) * 4 + 3] = y[1];
+                    odd |= !(fabsf((float)x[0]) < __builtin_inff()) | !(fabsf((float)x[1]) < __builtin_inff()) |
+                           !(fabsf((float)y[0]) < __builtin_inff()) | !(fabsf((float)y[1]) < __builtin_inff());
+                }
+                const uint64_t odd_lanes = __ballot(odd);
+                const bool bad = (uint32_t)(lane >> 5 ? odd_lanes >> 32 : odd_lanes) != 0;
+                if (bad) v[0] = v[1] = h8{};
+                if (part == 0 && e < count) {
+                    if (row[i] < 0) atomicOr(&sh.absent[e >> 5], 1u << (e & 31));
+                    if (bad) atomicOr(&sh.bad[e >> 5], 1u << (e & 31));
+                }
+                _Float16* at = sh.kv + e * kD;
+                *reinterpret_cast<h8*>(at + ((2 * part) ^ win_swap(e)) * 8) = v[0];
+                *reinterpret_cast<h8*>(at + ((2 * part + 1) ^ win_swap(e)) * 8) = v[1];
+            }
+        }
+        __syncthreads();
+        uint32_t flags = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) flags |= sh.absent[i] | sh.bad[i];
+        flags = __builtin_amdgcn_readfirstlane(flags);
+
+        const int rows = (stop - begin) * a.heads;
+        const int64_t pair0 = (t0 + begin) * a.heads;
+        for (int tile = w; tile * 16 < rows; tile += kWinWaves) {
+            const int r = min(tile * 16 + c, rows - 1), query = r / a.heads;
+            const bool live = tile * 16 + c < rows;
+            const int64_t pair = pair0 + r;
+            // the rows' queries, as scaled fp16 (as stage_query)
+            h8 q[16];
+            float fr;
+            {
+                uint4 raw[16];
+                const uint16_t* at = a.q + pair * kD + 8 * g;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) raw[x] = *reinterpret_cast<const uint4*>(at + 32 * x);
+                us2 two = {0, 0};
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    two = __builtin_elementwise_max(two, __builtin_bit_cast(us2, raw[x].x & 0x7fff7fffu));
+                    two = __builtin_elementwise_max(two, __builtin_bit_cast(us2, raw[x].y & 0x7fff7fffu));
+                    two = __builtin_elementwise_max(two, __builtin_bit_cast(us2, raw[x].z & 0x7fff7fffu));
+                    two = __builtin_elementwise_max(two, __builtin_bit_cast(us2, raw[x].w & 0x7fff7fffu));
+                }
+                const uint32_t m = max32(max16(max((uint32_t)two[0], (uint32_t)two[1])));
+                int e = (int)(m >> 7);
+                const bool finite = e < 255;
+                e = e < 15 ? 15 : (e > 254 ? 254 : e);
+                const float mul = finite ? __uint_as_float((uint32_t)(127 + 141 - e) << 23) : __builtin_nanf("");
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const uint32_t v[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        q[x][2 * y] = (_Float16)(__uint_as_float(v[y] << 16) * mul);
+                        q[x][2 * y + 1] = (_Float16)(__uint_as_float(v[y] & 0xffff0000u) * mul);
+                    }
+                    if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
+                fr = a.scale * kLog2e * __uint_as_float((uint32_t)(e - 14) << 23);
+            }
+            const int2 see = sh.sees[begin + query];
+            // the tiles of entries that any of the rows sees, and those that all see whole
+            int from = see.y > see.x ? see.x : INT32_MAX, to = see.y > see.x ? see.y : 0, low = see.x, high = see.y;
+            from = min(from, (int)dpp<0xB1>(from)), to = max(to, (int)dpp<0xB1>(to));  // quad_perm [1,0,3,2]
+            low = max(low, (int)dpp<0xB1>(low)), high = min(high, (int)dpp<0xB1>(high));
+            from = min(from, (int)dpp<0x4E>(from)), to = max(to, (int)dpp<0x4E>(to));  // quad_perm [2,3,0,1]
+            low = max(low, (int)dpp<0x4E>(low)), high = min(high, (int)dpp<0x4E>(high));
+            from = min(from, (int)dpp<0x141>(from)), to = max(to, (int)dpp<0x141>(to));  // row_half_mirror
+            low = max(low, (int)dpp<0x141>(low)), high = min(high, (int)dpp<0x141>(high));
+            from = min(from, (int)dpp<0x140>(from)), to = max(to, (int)dpp<0x140>(to));  // row_mirror
+            low = max(low, (int)dpp<0x140>(low)), high = min(high, (int)dpp<0x140>(high));
+            from = __builtin_amdgcn_readfirstlane(from) / 16;
+            to = (__builtin_amdgcn_readfirstlane(to) + 15) / 16;
+            low = __builtin_amdgcn_readfirstlane(low);
+            high = __builtin_amdgcn_readfirstlane(high);
+
+            v4f y[kWinTiles];
+            // (the lane's place in the first entries' rows; the exchange of pieces makes the others differ in single bits)
+            int at_key = c * kD + (g ^ win_swap(c)) * 8;
+            asm volatile("" : "+v"(at_key));  // not kept for all of them over the rows
+#pragma unroll
+            for (int k3 = 0; k3 < kWinTiles; k3 += 3) {
+                v4f d[3] = {};
+                if (k3 + 3 > from && k3 < to) {
+                    const _Float16* at = sh.kv + k3 * 16 * kD;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const _Float16* piece = at + (at_key ^ ((x & 3) * 32)) + (x >> 2) * 128;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const h8 v = *reinterpret_cast<const h8*>(piece + k * 16 * kD);
+                            d[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, q[x], d[k], 0, 0, 0);
+                        }
+                        if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int e = (k3 + k) * 16;
+                    y[k3 + k] = d[k] * fr;
+                    if (e < low || e + 16 > high) {  // some rows see only some of them
+                        const uint32_t place = (uint32_t)(e + 4 * g - see.x), seen = (uint32_t)max(see.y - see.x, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[k3 + k][i] = place + i < seen ? y[k3 + k][i] : ninf();
+                    }
+                }
+            }
+            if (flags) {
+#pragma unroll
+                for (int k = 0; k < kWinTiles; ++k) {
+                    const int e = k * 16 + 4 * g;
+                    const uint32_t absent = sh.absent[e >> 5] >> (e & 31), bad = sh.bad[e >> 5] >> (e & 31);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((absent >> i) & 1) y[k][i] = ninf();
+                        if (((bad >> i) & 1) && e + i >= see.x && e + i < see.y) y[k][i] = __builtin_nanf("");
+                    }
+                }
+            }
+            float top = ninf();
+#pragma unroll
+            for (int k = 0; k < kWinTiles; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[k][i]);
+            }
+            top = group_max(top);
+            // probabilities up to 2^15: those down to 2^-29 of the largest are normal fp16 numbers
+            const float R = top > ninf() ? ceilf(top) - 15.0f : 0.0f;
+            float L = 0.0f;
+            h8 p[(kWinTiles + 1) / 2];
+#pragma unroll
+            for (int k = 0; k < kWinTiles; ++k) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float ex = __builtin_amdgcn_exp2f(y[k][i] - R);
+                    L += ex;
+                    p[k / 2][(k & 1) * 4 + i] = (_Float16)ex;
+                }
+            }
+            L = group_sum(L);
+            __builtin_amdgcn_sched_barrier(0);
+            const Weights wt = join_weights(a, a.other ? a.other_lse[pair] : 0.0f, R, L);
+            if (a.lse && g == 0 && live) a.lse[pair] = wt.lse;
+
+            // lane (c, g) reads four values' piece of entry 4g + c / 4 of a tile; it gets value c of four entries
+            const int entry = 4 * g + (c >> 2);
+            int at_value = entry * kD + (((c & 3) >> 1) ^ win_swap(entry)) * 8 + (c & 1) * 4;
+            asm volatile("" : "+v"(at_value));
+            const int turn_at = a.turn.freq ? a.turn.offset : kD;
+            const float2* cs = sh.cs + query * pairs;
+#pragma unroll 1
+            for (int half = 0; half < kWinCuts; ++half) {
+                constexpr int kTwos = 8 / kWinCuts, kValues = kD / kWinCuts;  // blocks of 64 values
+                v4f o[4 * kTwos] = {};
+                const int mine8 = (g & 1) * 16 + (g & 2) * 4;  // see below
+                uint4 u[2 * kTwos] = {};
+                if (wt.other != 0.0f) {  // (what lies in a part of no weight has no effect)
+#pragma unroll
+                    for (int b = 0; b < 2 * kTwos; ++b)
+                        u[b] = *reinterpret_cast<const uint4*>(a.other + pair * kD + half * kValues + 32 * b + mine8);
+                }
+#pragma unroll
+                for (int k = 0; k < kWinTiles; k += 2) {
+                    if (k + 2 <= from || k >= to) continue;
+#pragma unroll
+                    for (int d = 0; d < 4 * kTwos; ++d) {
+                        const _Float16* at = sh.kv + half * kValues + k * 16 * kD + (at_value ^ ((d & 7) * 16)) + (d >> 3) * 128;
+                        const hv4 l4 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
+                        if (k + 1 < kWinTiles) {
+                            const hv4 h4v = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 16 * kD));
+                            h8 v;
+                            __builtin_memcpy(&v, &l4, 8);
+                            __builtin_memcpy((char*)&v + 8, &h4v, 8);
+                            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[k / 2], o[d], 0, 0, 0);
+                        } else {
+                            h4 v;
+                            __builtin_memcpy(&v, &l4, 8);
+                            const h4 last = {p[k / 2][0], p[k / 2][1], p[k / 2][2], p[k / 2][3]};
+                            o[d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, last, o[d], 0, 0, 0);
+                        }
+                        if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // Lane groups exchange halves of two tiles: eight values in a row each, of 32 by 32 two at a time.
+#pragma unroll
+                for (int two = 0; two < kTwos; ++two) {
+                    const int at = half * kValues + two * 64 + mine8;
+                    float v[2][8];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const v4f x = o[4 * two + 2 * b], z = o[4 * two + 2 * b + 1];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(z[i]), false, false);
+                            v[b][i] = __uint_as_float(sw[0]) * wt.mine;
+                            v[b][4 + i] = __uint_as_float(sw[1]) * wt.mine;
+                        }
+                        const uint32_t x2[4] = {u[2 * two + b].x, u[2 * two + b].y, u[2 * two + b].z, u[2 * two + b].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[b][2 * i] = fmaf(wt.other, __uint_as_float(x2[i] << 16), v[b][2 * i]);
+                            v[b][2 * i + 1] = fmaf(wt.other, __uint_as_float(x2[i] & 0xffff0000u), v[b][2 * i + 1]);
+                        }
+                    }
+                    const int from_turn = half * kValues + two * 64 - turn_at;  // of the block's first value
+                    if (from_turn > -64 && from_turn < 2 * pairs) {
+                        if (a.turn.half) {  // 64 values at a multiple of 64
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 z = cs[mine8 + i];
+                                const float x0 = v[0][i], x1 = v[1][i];
+                                v[0][i] = x0 * z.x - x1 * z.y;
+                                v[1][i] = x1 * z.x + x0 * z.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int j = at + 32 * b + 2 * i - turn_at;
+                                    if (j < 0 || j >= 2 * pairs) continue;
+                                    const float2 z = cs[j >> 1];
+                                    const float x0 = v[b][2 * i], x1 = v[b][2 * i + 1];
+                                    v[b][2 * i] = x0 * z.x - x1 * z.y;
+                                    v[b][2 * i + 1] = x1 * z.x + x0 * z.y;
+                                }
+                            }
+                        }
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            *reinterpret_cast<uint4*>(a.out + pair * kD + at + 32 * b) =
+                                uint4{bf16_pair(v[b][0], v[b][1]), bf16_pair(v[b][2], v[b][3]), bf16_pair(v[b][4], v[b][5]),
+                                      bf16_pair(v[b][6], v[b][7])};
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        begin = stop;
+        if (begin < some) __syncthreads();  // before other entries take the place
+    }
 }
+
+// The most queries that a block of the window kernel takes; 0: the call is not for it.
+int window_queries(const LocalArgs& a) {
+    if (a.window <= 0 || a.window > kWinKeys) return 0;
+    int64_t most = std::min<int64_t>({kWinKeys - a.window + 1, kWinQueries, a.group});
+    if (a.turn.freq) {
+        if (a.turn.half ? a.turn.rot != 64 || a.turn.offset % 64 != 0 : a.turn.offset % 2 != 0) return 0;
+        most = std::min<int64_t>(most, kWinAngles / (a.turn.rot / 2));
+    }
+    return (int)most;
+}
+
+constexpr int64_t up(int64_t x, int64_t by) { return (x + by - 1) / by; }
 size_t part_bytes(int64_t rows) { return (size_t)rows * (kD + 2) * sizeof(float); }
+
+// The cut that takes the least time on 256 compute units, by what was measured (microseconds): a block of 16, 32 or 64 rows
+// kLocalTiles' apart from its steps and for each step of 64 entries (1 .. 1024 queries of 1 .. 128 heads over 1000 .. 65536
+// entries); a join 4, and its parts at 4 TB/s; a block of the window kernel 12, and 14.5 for each 128 rows (9 for a
+// last 64). `most`: parts that the workspace has room for. most_queries: window_queries().
+constexpr struct {
+    int nh, places;
+    float step, block, step_alone, block_alone;
+} kLocalTiles[] = {{4, 256, 1.8f, 24.0f, 1.8f, 24.0f}, {2, 256, 1.3f, 13.0f, 1.3f, 13.0f}, {1, 512, 2.5f, 9.0f, 1.9f, 7.3f}};
+
+LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries) {
+    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), 0};
+    float least = 0.0f;
+    const auto consider = [&](float time, const LocalCut& cut) {
+        if (least == 0.0f || time < least) least = time, best = cut;
+    };
+    for (const auto& t : kLocalTiles) {
+        const int64_t rows = 16 * t.nh;
+        if (t.nh > 1 && group * heads <= 8 * t.nh) continue;  // half of the tile would be empty
+        const int64_t tiles = up(group * heads, rows), blocks = runs * tiles, steps = std::max<int64_t>(up(entries, kTile), 1);
+        const auto in_parts = [&](int64_t parts) {
+            if (parts < 1 || parts > most || parts > kMostParts || (parts > 1 && parts > steps)) return;
+            const bool alone = blocks * parts <= 256;
+            consider((float)up(blocks * parts, t.places) *
+                             ((float)up(steps, parts) * (alone ? t.step_alone : t.step) + (alone ? t.block_alone : t.block)) +
+                         (parts > 1 ? 6.0f + 5e-4f * (float)(runs * group * heads * parts) : 0.0f),
+                     LocalCut{t.nh, (uint32_t)parts, (uint32_t)tiles, 0});
+        };
+        for (int parts = 1; parts <= 8; ++parts) in_parts(parts);
+        for (int rounds = 1; rounds <= 4; ++rounds) in_parts(std::min<int64_t>(rounds * t.places / blocks, kMostParts));
+        for (int parts = 12; parts <= 64; parts += parts >= 32 ? 16 : parts >= 16 ? 8 : 4) in_parts(parts);
+    }
+    for (int queries = 1; queries <= most_queries; ++queries) {
+        const int64_t tiles = up(queries * heads, 16), last = tiles % 8;
+        const float rows = 14.5f * (float)(tiles / 8) + (last == 0 ? 0.0f : last <= 4 ? 9.0f : 14.5f);
+        consider((float)up(runs * up(group, queries), 256) * (12.0f + rows), LocalCut{0, 1, 0, queries});
+    }
+    return best;
+}
+
+// The same for the sizes asked for last: the next call mostly has the same.
+LocalCut local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries) {
+    thread_local int64_t of[6] = {0, 0, 0, 0, 0, 0};
+    thread_local LocalCut cut{};
+    const int64_t now[6] = {runs, group, heads, entries, most, most_queries};
+    if (memcmp(of, now, sizeof(of))) {
+        cut = best_local_cut(runs, group, heads, entries, most, most_queries);
+        memcpy(of, now, sizeof(of));
+    }
+    return cut;
+}
 
 }  // namespace
 
 size_t local_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
     if (nq <= 0 || entries <= 0) return 16;
-    const int64_t rows = (int64_t)nq * heads, parts = parts_for((rows + 31) / 32, entries);
-    return parts == 1 ? 16 : parts * part_bytes(rows);
+    // (how the queries come in runs is not known here: as one, whose tiles are the fewest and parts the most)
+    const LocalCut cut = best_local_cut(1, nq, heads, entries, kMostParts, 0);
+    return cut.parts == 1 ? 16 : cut.parts * part_bytes((int64_t)nq * heads);
 }
 
 hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream_t stream) {
-    const int64_t rows = (int64_t)a.nq * a.heads, runs = a.nq / a.group, run_rows = (int64_t)a.group * a.heads;
+    const int64_t rows = (int64_t)a.nq * a.heads, runs = a.nq / a.group;
     int64_t entries = a.places.max_n;
-    if (a.window > 0) entries = std::min(entries, a.window + std::min<int64_t>(a.group, 31));
-    LocalCut cut;
-    cut.nh = run_rows > 16 ? 2 : 1;
-    cut.tiles = (uint32_t)((run_rows + 16 * cut.nh - 1) / (16 * cut.nh));
-    const int64_t blocks = runs * cut.tiles;
-    cut.parts = (uint32_t)std::max<int64_t>(1, std::min<int64_t>(parts_for(blocks, entries), ws_bytes / part_bytes(rows)));
+    if (a.window > 0) entries = std::min(entries, a.window + std::min<int64_t>(a.group, 16) - 1);
+    const int64_t room = std::min<int64_t>(kMostParts, ws_bytes / part_bytes(rows));
+    LocalCut cut = local_cut(runs, a.group, a.heads, entries, std::max<int64_t>(room, 1), window_queries(a));
+    if (cut.queries) {
+        const uint32_t per_run = (uint32_t)up(a.group, cut.queries), units = (uint32_t)runs * per_run;
+        hipLaunchKernelGGL(attend_window_kernel, dim3((units + 7) / 8 * 8), dim3(64 * kWinWaves), 0, stream, a, cut.queries,
+                           per_run, units);
+        return hipGetLastError();
+    }
     if (cut.parts > 1) {
         a.part_o = (float*)ws;
         a.part_ml = a.part_o + (size_t)cut.parts * rows * kD;
     }
-    const uint32_t units = (uint32_t)(blocks * cut.parts);
-    const dim3 grid((units + 7) / 8 * 8);
-    if (cut.nh == 2) {
+    const uint32_t units = (uint32_t)(runs * cut.tiles * cut.parts);
+    const auto start = [&](auto nh) {
+        constexpr int kNh = decltype(nh)::value;
+        const dim3 grid((units + 7) / 8 * 8);
         if (a.places.pages)
-            hipLaunchKernelGGL((attend_local_kernel<2, true>), grid, dim3(256), 0, stream, a, cut, units);
+            hipLaunchKernelGGL((attend_local_kernel<kNh, true>), grid, dim3(256), 0, stream, a, cut, units);
         else
-            hipLaunchKernelGGL((attend_local_kernel<2, false>), grid, dim3(256), 0, stream, a, cut, units);
-    } else {
-        if (a.places.pages)
-            hipLaunchKernelGGL((attend_local_kernel<1, true>), grid, dim3(256), 0, stream, a, cut, units);
-        else
-            hipLaunchKernelGGL((attend_local_kernel<1, false>), grid, dim3(256), 0, stream, a, cut, units);
-    }
+            hipLaunchKernelGGL((attend_local_kernel<kNh, false>), grid, dim3(256), 0, stream, a, cut, units);
+    };
+    if (cut.nh == 1)
+        start(std::integral_constant<int, 1>{});
+    else if (cut.nh == 2)
+        start(std::integral_constant<int, 2>{});
+    else
+        start(std::integral_constant<int, 4>{});
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || cut.parts == 1) return err;
-    hipLaunchKernelGGL(local_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, (int)cut.parts);
+    if (cut.parts > 4)
+        hipLaunchKernelGGL(local_join_kernel<4>, dim3((unsigned)rows), dim3(256), 0, stream, a, (int)cut.parts);
+    else
+        hipLaunchKernelGGL(local_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, (int)cut.parts);
     return hipGetLastError();
 }
 
