@@ -56,10 +56,10 @@ __device__ __forceinline__ void load_piece(const LocalArgs& a, int32_t row, int 
 __device__ __forceinline__ uint32_t load_scale(const LocalArgs& a, int32_t row, int g) {
     return *reinterpret_cast<const uint32_t*>(a.scales + (int64_t)max(row, 0) * 16 + g * 4);
 }
-// values 8x .. 8x + 7 of the part as fp16 (exact); keep: all ones, or zero for a row that is not there
-__device__ __forceinline__ h8 local_values8(const LocalPart& r, int x, uint32_t keep) {
+// values 8x .. 8x + 7 of the part as fp16 (exact)
+__device__ __forceinline__ h8 local_values8(const LocalPart& r, int x) {
     const uint4 c = r.code[x >> 1];
-    const uint32_t w0 = (x & 1 ? c.z : c.x) & keep, w1 = (x & 1 ? c.w : c.y) & keep;
+    const uint32_t w0 = x & 1 ? c.z : c.x, w1 = x & 1 ? c.w : c.y;
     const float s = __uint_as_float((r.scale >> (8 * (x >> 2)) & 0xffu) << 23);
     const h2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, s, false);
     const h2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, s, true);
@@ -163,7 +163,9 @@ struct LocalShared {
     _Float16 q[NH * 16 * kQRow];  // the queries' last fragment (the registers hold 15 of 16)
 };
 
-template <int NH, bool PAGED>
+// WINDOW: of a window's entries, perhaps in a ring; else of all visible ones. (A template argument: a branch inside a turn of
+// the pipe costs the blocks of 64 rows a sixth.)
+template <int NH, bool PAGED, bool WINDOW>
 __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kernel(const LocalArgs a, const LocalCut cut, uint32_t units) {
     __shared__ __align__(16) LocalShared<NH> sh;
     constexpr bool PAIR = kLocalPair<NH>;
@@ -208,13 +210,13 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
         sp = Span{lo, hi - lo, __builtin_amdgcn_readfirstlane((int)(lo != lo_most || hi != hi_least)) != 0, 0};
         if (hi == 0) sp = Span{0, 0, false, 0};
         const int64_t each = (a.window + kTile - 1) / kTile * kTile;
-        if (a.window > 0 && each * (tb - ta + 1) < sp.count) {
+        if (WINDOW && each * (tb - ta + 1) < sp.count) {
             sp.each = (int32_t)each;
             sp.count = (int32_t)each * (tb - ta + 1);
         }
     }
     if (w == 0 && lane < kRows) sh.sees[lane] = int2{mine.x - sp.first, mine.y - sp.first};
-    if (sp.each) __syncthreads();
+    if (WINDOW && sp.each) __syncthreads();
     // where they lie
     int64_t base = 0;
     const int32_t* pages = nullptr;
@@ -239,6 +241,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     // an entry's row in three stages, so that the loads of each are in flight: its place, its page, its row
     const auto row_in_block = [&](int query) { return max((ta + query) * a.heads - r0, 0); };
     const auto place = [&](int i) {
+        if (!WINDOW) return i < end ? i : -1;
         int p = sp.first + i;
         bool there = i < end;
         if (sp.each) {
@@ -389,13 +392,13 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     // step's rows lie.
     const auto mask_step = [&](int i, uint32_t seen, const float2 (&fr)[NH], int at_rows) {
         const int e = (step0 + i) * kTile + w * 16 + g * 4;
-        const int query = sp.each ? (step0 + i) * kTile / sp.each : 0;  // of the step, where they go one by one
+        const int query = WINDOW && sp.each ? (step0 + i) * kTile / sp.each : 0;  // of the step, where they go one by one
         bool odd = false;
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             const float hole = fr[n].x < 0.0f ? __builtin_inff() : ninf();
             int2 see = sh.sees[n * 16 + c];
-            if (sp.each) see = (r0 + n * 16 + c) / a.heads == ta + query ? int2{INT32_MIN, INT32_MAX} : int2{0, 0};
+            if (WINDOW && sp.each) see = (r0 + n * 16 + c) / a.heads == ta + query ? int2{INT32_MIN, INT32_MAX} : int2{0, 0};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const bool mine = ((seen >> y) & 1) && e + y >= see.x && e + y < see.y;
@@ -403,9 +406,9 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
                 s[n][y] = mine ? s[n][y] : hole;
             }
         }
-        // A row that holds NaN codes and that some of the block's queries do not see: for the second product it is
-        // zeros (those that see it have a NaN probability). A query's own NaN or infinity looks the same; then
-        // nothing is found here.
+        // A row that holds NaN codes, and that is not there (what was read is another) or that some of the block's queries
+        // do not see: for the second product it is zeros (those that see it have a NaN probability). A query's own NaN or
+        // infinity looks the same; then nothing is found here.
         if (__any(odd)) {
 #pragma unroll 1
             for (int j = 0; j < 16; ++j) {
@@ -454,14 +457,14 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
             v[0] = rows8(0);
         }
         const bool there = row >= 0;
-        const uint32_t keep = there ? ~0u : 0u;
+        const uint64_t all = __ballot(there);
         int32_t row1 = -1;
         if constexpr (kQk) {
             row1 = row_of(place1, page1);
             place1 = place2;
             page1 = page(place2);
             place2 = place(i0 + (i + 4) * kTile);
-            k = local_values8(kv, 0, keep);
+            k = local_values8(kv, 0);
         }
         if constexpr (kPv) {
             if (__builtin_amdgcn_readfirstlane(ov.x | ov.y | ov.z | ov.w)) {
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
             if constexpr (kQk) {
                 const h8 kx = k;
                 *reinterpret_cast<h8*>(sh.kv + (in ^ ((x & 7) * 8)) + (x >> 3) * 64) = kx;
-                if (x < 15) k = local_values8(kv, x + 1, keep);
+                if (x < 15) k = local_values8(kv, x + 1);
                 if (x == 3) scale1 = load_scale(a, row1, g);
                 if (x & 1) load_piece(a, row1, g, x >> 1, kv);
 #pragma unroll
@@ -526,7 +529,6 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
             float2 fr[NH];
 #pragma unroll
             for (int n = 0; n < NH; ++n) fr[n] = sh.fr[n * 16 + c];
-            const uint64_t all = __ballot(there);
             if (all != ~0ull || sp.mixed) mask_step(i + 1, (uint32_t)all >> (g * 4), fr, in - at_in);
             bool over = false;
             if constexpr (kFirst) {
@@ -1175,10 +1177,17 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
     const auto start = [&](auto nh) {
         constexpr int kNh = decltype(nh)::value;
         const dim3 grid((units + 7) / 8 * 8);
-        if (a.places.pages)
-            hipLaunchKernelGGL((attend_local_kernel<kNh, true>), grid, dim3(256), 0, stream, a, cut, units);
-        else
-            hipLaunchKernelGGL((attend_local_kernel<kNh, false>), grid, dim3(256), 0, stream, a, cut, units);
+        if (a.window > 0) {
+            if (a.places.pages)
+                hipLaunchKernelGGL((attend_local_kernel<kNh, true, true>), grid, dim3(256), 0, stream, a, cut, units);
+            else
+                hipLaunchKernelGGL((attend_local_kernel<kNh, false, true>), grid, dim3(256), 0, stream, a, cut, units);
+        } else {
+            if (a.places.pages)
+                hipLaunchKernelGGL((attend_local_kernel<kNh, true, false>), grid, dim3(256), 0, stream, a, cut, units);
+            else
+                hipLaunchKernelGGL((attend_local_kernel<kNh, false, false>), grid, dim3(256), 0, stream, a, cut, units);
+        }
     };
     if (cut.nh == 1)
         start(std::integral_constant<int, 1>{});
