@@ -28,11 +28,15 @@ them); idx_score_pool_gather re-scores those 4096 keys; idx_topk takes the final
 
 Core attention (the consumer of a layer's selection): CoreAttention keeps the FP4 main-KV cache in pages,
 rotates and quantises new rows into them, and attends over the selected positions; layer() gives the result
-with the values turned back to the query's frame. IndexerDistill trains a layer's indexer towards it, on the
+with the values turned back to the query's frame. LayerAttention is the whole of a layer's attention ("DeepSeek-V4.1
+model structure (3)", sections "Reindex layers score a million entries per token", whose count of core attention has 512
+selected and 128 local entries, and "removing the global scale still leaves enough range"): the selection joined with
+the last positions in an FP8 ring, and the writing of a step's rows into all of the layer's caches. IndexerDistill trains a layer's indexer towards it, on the
 score rows of the training form.
 
 All buffers are allocated once in the plan objects, so a step allocates nothing and can be
-captured in a HIP graph. (CoreAttention.write fills its cache between steps: it allocates and is not captured.)
+captured in a HIP graph. (CoreAttention.write fills its cache between steps: it allocates and is not captured;
+LayerAttention.write, into pages that were reserved, is part of a step.)
 """
 from __future__ import annotations
 
@@ -41,10 +45,10 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (BLOCK, IDX_OP_ATTEND, IDX_OP_BUILD_POOL, IDX_OP_DISTILL, IDX_OP_TOPK, MKV_DIM, Recorded, idx_attend,
-               idx_attend_weights, idx_build_pool, idx_distill, idx_distill_bwd, idx_mask_pool, idx_quantize_kv,
+from . import (BLOCK, DIM, IDX_OP_ATTEND, IDX_OP_ATTEND_LOCAL, IDX_OP_BUILD_POOL, IDX_OP_DISTILL, IDX_OP_TOPK, MKV_DIM, Recorded, idx_attend,
+               idx_attend_local, idx_attend_weights, idx_build_pool, idx_distill, idx_distill_bwd, idx_mask_pool, idx_quantize_kv,
                idx_quantize_q, idx_rope, idx_score_full, idx_score_pool_gather, idx_top_blocks, idx_topk, idx_topk_pool,
-               record, rope_freqs, workspace)
+               idx_write_rows, record, rope_freqs, workspace)
 
 
 @dataclass
@@ -365,6 +369,17 @@ class CoreAttention:
         self.weights = torch.empty(nq, k, dtype=torch.float32, device=device)
         self.ws = workspace(IDX_OP_ATTEND, nq, k, heads, device=device)
 
+    def reserve(self, b: int, n: int) -> None:
+        """Pages for sequence b's first n entries (between steps: page numbers come from the host)."""
+        if n > self.n:
+            raise ValueError(f"{n} entries are more than the sequence's {self.n}")
+        need = (n + self.page_size - 1) // self.page_size
+        if need > self.given[b]:
+            new = torch.arange(self.used, self.used + need - self.given[b], dtype=torch.int32)
+            self.pages[b, self.given[b]:need] = new.to(self.pages.device)
+            self.used += need - self.given[b]
+            self.given[b] = need
+
     def write(self, b: int, first: int, x: torch.Tensor, pos: torch.Tensor | None = None) -> None:
         """Rows x [m, 512] (bf16, not rotated) of sequence b's entries first .. first + m - 1. pos [m] (int64): the
         positions that turn them, where an entry does not stand for the one token of its number (a cache compressed
@@ -378,12 +393,7 @@ class CoreAttention:
         at = torch.arange(first, first + m, device=x.device)
         y = idx_rope(x.view(m, 1, MKV_DIM), at if pos is None else pos, self.freq, layout=self.layout, mscale=self.mscale)
         codes, scales = idx_quantize_kv(y.view(m, MKV_DIM))
-        need = (first + m + self.page_size - 1) // self.page_size
-        if need > self.given[b]:
-            new = torch.arange(self.used, self.used + need - self.given[b], dtype=torch.int32)
-            self.pages[b, self.given[b]:need] = new.to(self.pages.device)
-            self.used += need - self.given[b]
-            self.given[b] = need
+        self.reserve(b, first + m)
         rows = self.pages[b].long()[at // self.page_size] * self.page_size + at % self.page_size
         self.codes.index_copy_(0, rows, codes)
         self.scales.index_copy_(0, rows, scales)
@@ -408,6 +418,67 @@ class CoreAttention:
         """The probabilities [nq, k] that the last run gave its selection, mean over the heads."""
         return idx_attend_weights(self.q, self.codes, self.scales, n_vis, self.n, self.scale, self.lse, self.weights,
                                   pages=self.pages, page_size=self.page_size, seq=seq, idx=idx, stream=stream)
+
+
+class LayerAttention:
+    """A layer's attention over its selection (`core`'s cache) and its last `window` positions, which lie in a ring of FP8
+    rows for each sequence, and the layer's caches as a step writes them: main rows, local rows and the indexer's keys.
+    Steps have up to `group` consecutive queries of a sequence (1, or the draft positions). gamma and eps: the norm of the
+    rows before they are turned (none without eps); signs: the indexer's, for its keys.
+
+    Everything here can be captured: a step writes its rows at entries that the device names and attends to them. Pages
+    of the main cache are reserved ahead (core.reserve)."""
+
+    MOST = 1 << 30  # positions a sequence may have: the ring keeps the last
+
+    def __init__(self, core: CoreAttention, window: int = 128, group: int = 1, signs: torch.Tensor | None = None,
+                 gamma: torch.Tensor | None = None, eps: float | None = None):
+        nseq, d = core.pages.shape[0], core.q.device
+        heads = core.q.shape[1]
+        self.core, self.window, self.group, self.ring = core, window, group, window + group - 1
+        self.signs, self.gamma, self.eps = signs, gamma, eps
+        self.codes = torch.zeros(nseq * self.ring, MKV_DIM, dtype=torch.uint8, device=d)
+        self.scales = torch.zeros(nseq * self.ring, MKV_DIM // 32, dtype=torch.uint8, device=d)
+        # sequence s's ring, and its range of keys, as one page each
+        self.own = torch.arange(nseq, dtype=torch.int32, device=d).view(nseq, 1)
+        self.k_codes = self.k_scales = None
+        if signs is not None:
+            self.k_codes = torch.zeros(nseq * core.n, DIM // 2, dtype=torch.uint8, device=d)
+            self.k_scales = torch.zeros(nseq * core.n, DIM // 32, dtype=torch.uint8, device=d)
+        self.out = torch.empty_like(core.q)
+        self.lse = torch.empty_like(core.lse)
+        self.ws = workspace(IDX_OP_ATTEND_LOCAL, core.nq, self.ring, heads, device=d)
+
+    def write(self, seq, at, main=None, local=None, key=None, pos=None, stream=None):
+        """New rows of a step (not normalised, not turned): main and local [tokens, 512], key [tokens, 128], each or
+        None, of sequences seq [tokens] (int32) at entries at [tokens] (int64), turned by pos [tokens] (default: at).
+        Entries of one call's main rows and keys are those of a cache compressed along the sequence where pos is given;
+        local rows are one a position and go by pos then. Tokens at entries below 0 are left out."""
+        core = self.core
+        norm = dict(gamma=self.gamma, eps=self.eps)
+        turn = dict(pos=pos, freq=core.freq, layout=core.layout, mscale=core.mscale)
+        if main is not None:
+            idx_write_rows("main", main, core.codes, core.scales, at, core.n, pages=core.pages, page_size=core.page_size,
+                           seq=seq, stream=stream, **norm, **turn)
+        if local is not None:
+            idx_write_rows("local", local, self.codes, self.scales, at if pos is None else pos, self.MOST, pages=self.own,
+                           page_size=self.ring, seq=seq, ring=self.ring, stream=stream, **norm, **turn)
+        if key is not None:
+            # (the indexer's keys carry their position, too: the rotated part at the end of the row)
+            idx_write_rows("key", key, self.k_codes, self.k_scales, at, core.n, pages=self.own, page_size=core.n, seq=seq,
+                           signs=self.signs, stream=stream, **turn)
+
+    def run(self, q, pos, seq, n_vis, idx, n_local, stream=None):
+        """q [nq, heads, 512] (bf16, not rotated) at positions pos [nq] of sequences seq [nq]: the attention over the
+        selected entries idx [nq, k] below n_vis [nq] and over the last positions before n_local [nq] (pos + 1, where a
+        query sees itself) -> out, lse, the values turned back to the query's frame."""
+        core = self.core
+        core.run(q, pos, seq, n_vis, idx, stream=stream)
+        runs = seq if self.group == 1 else seq.view(-1, self.group)[:, 0].contiguous()
+        return idx_attend_local(core.q, self.codes, self.scales, n_local, self.MOST, core.scale, self.out, self.ws,
+                                lse=self.lse, window=self.window, ring=self.ring, group=self.group, pages=self.own,
+                                page_size=self.ring, seq=runs, other=core.out, other_lse=core.lse, pos=pos, freq=core.freq,
+                                layout=core.layout, mscale=1.0 / core.mscale, stream=stream)
 
 
 class IndexerDistill:
