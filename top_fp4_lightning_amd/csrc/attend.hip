@@ -756,22 +756,6 @@ __global__ __launch_bounds__(256, 1) void attend_weights_kernel(const AttendArgs
 
 namespace {
 
-// Time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first of `places` that is free.
-float time_of(int64_t places, int64_t n1, float t1, int64_t n2, float t2) {
-    const int64_t rest = n1 % places;
-    const float before = (float)(n1 / places) * t1;
-    if (n2 == 0) return before + (rest ? t1 : 0.0f);
-    if (rest == 0) return before + (float)((n2 + places - 1) / places) * t2;
-    // `rest` places end their long block at t1; the others take short ones from the start
-    for (int64_t j = 0;; ++j) {
-        const float end = t1 + (float)j * t2;
-        const int64_t k = (int64_t)(end / t2);
-        if (k * (places - rest) + j * rest < n2) continue;
-        const float sooner = (float)k * t2;  // the other places' last one ends before these places' j-th
-        const bool enough = j > 0 && sooner >= t1 && k * (places - rest) + (j - 1) * rest >= n2;
-        return before + (enough ? sooner : end);
-    }
-}
 // How a call is cut: head sixteens of a block and parts of a query's entries, by the time that the 256 compute
 // units (a block each, or two of 16 heads) would take. Large head tiles widen a row for more heads, small ones and
 // parts give blocks and even rounds. Measured per step of 64 entries and per block apart from its steps, in

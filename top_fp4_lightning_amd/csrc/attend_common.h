@@ -107,4 +107,21 @@ __device__ __forceinline__ void stage_query(float scale, int left, QueryRows<ROW
     }
 }
 
+// (host) time until the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, each taken by the first of `places` that is free.
+inline float time_of(int64_t places, int64_t n1, float t1, int64_t n2, float t2) {
+    const int64_t rest = n1 % places;
+    const float before = (float)(n1 / places) * t1;
+    if (n2 == 0) return before + (rest ? t1 : 0.0f);
+    if (rest == 0) return before + (float)((n2 + places - 1) / places) * t2;
+    // `rest` places end their long block at t1; the others take short ones from the start
+    for (int64_t j = 0;; ++j) {
+        const float end = t1 + (float)j * t2;
+        const int64_t k = (int64_t)(end / t2);
+        if (k * (places - rest) + j * rest < n2) continue;
+        const float sooner = (float)k * t2;  // the other places' last one ends before these places' j-th
+        const bool enough = j > 0 && sooner >= t1 && k * (places - rest) + (j - 1) * rest >= n2;
+        return before + (enough ? sooner : end);
+    }
+}
+
 }  // namespace fp4idx

@@ -68,12 +68,16 @@ __device__ __forceinline__ h8 local_values8(const LocalPart& r, int x) {
     return h8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
 }
 
-// How a call is cut: blocks of 16 nh rows of a run's heads x queries, each over one of `parts` parts of the entries; or,
-// with `queries` above 0, blocks of the window kernel over so many queries.
+// How a call is cut: blocks (tiles) of 16 nh rows of a run's heads x queries, the first `whole` tiles of a run over `parts`
+// parts of its entries, the others over one more, so that blocks come in whole rounds over the compute units; or, with
+// `queries` above 0, blocks of the window kernel over so many queries.
 struct LocalCut {
     int nh;
-    uint32_t parts, tiles;  // tiles of a run
+    uint32_t parts, tiles, whole;
     int queries;
+    __host__ __device__ uint32_t of_run() const { return tiles * (parts + 1) - whole; }
+    __host__ __device__ uint32_t slots() const { return parts + (whole < tiles); }  // of a row's parts
+    __device__ uint32_t parts_of(uint32_t tile) const { return parts + (tile >= whole); }
 };
 
 // Weights of a row's sums o and of its other part, and the joined logarithm: L = sum 2^(s2 - R).
@@ -173,11 +177,27 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int g = lane >> 4, c = lane & 15;
-    // blocks b, b + 8, .. run on one XCD: it takes neighbouring units, whose rows lie together
-    const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= share || unit >= units) return;
-    const uint32_t tile = unit % cut.tiles, part = unit / cut.tiles % cut.parts;
-    const int64_t run = unit / cut.tiles / cut.parts;
+    uint32_t run32, tile, part;
+    if (cut.whole == cut.tiles) {
+        // blocks b, b + 8, .. run on one XCD: it takes neighbouring units, those of a run's part, which read the same entries
+        const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+        if ((blockIdx.x >> 3) >= share || unit >= units) return;
+        tile = unit % cut.tiles, part = unit / cut.tiles % cut.parts, run32 = unit / cut.tiles / cut.parts;
+    } else {
+        // the longer ones of all runs first
+        const uint32_t longer = cut.whole * cut.parts, shorter = cut.tiles - cut.whole, first = units / cut.of_run() * longer;
+        if (blockIdx.x >= units) return;
+        if (blockIdx.x < first) {
+            run32 = blockIdx.x / longer;
+            tile = blockIdx.x % longer % cut.whole, part = blockIdx.x % longer / cut.whole;
+        } else {
+            const uint32_t v = blockIdx.x - first, of_run = shorter * (cut.parts + 1);
+            run32 = v / of_run;
+            tile = cut.whole + v % of_run % shorter, part = v % of_run / shorter;
+        }
+    }
+    const uint32_t parts = cut.parts_of(tile);
+    const int64_t run = run32;
     const int r0 = (int)tile * kRows, left = a.group * a.heads - r0;  // rows of the run from r0 on
     const int64_t t0 = run * a.group;                                 // the run's first query
     const int64_t pair0 = t0 * a.heads + r0;                          // the block's first row
@@ -232,7 +252,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     }
     if (a.places.rows == 0) sp.count = 0;
     const int steps_all = (sp.count + kTile - 1) / kTile;
-    const int per = (steps_all + (int)cut.parts - 1) / (int)cut.parts;
+    const int per = (steps_all + (int)parts - 1) / (int)parts;
     const int step0 = (int)part * per;
     const int steps = min(per, steps_all - step0);  // may be 0 or less
     const int end = steps > 0 ? min((step0 + steps) * kTile, sp.count) : 0;
@@ -286,7 +306,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
         kv.scale = load_scale(a, row, g);
     }
     // angles of the result, while the rows are on their way: one a thread, where they are so few
-    const int queries = tb - ta + 1, pairs = cut.parts == 1 && a.turn.freq ? a.turn.rot / 2 : 0;
+    const int queries = tb - ta + 1, pairs = parts == 1 && a.turn.freq ? a.turn.rot / 2 : 0;
     const bool early = queries * pairs <= 256;
     float2 angle{};
     if (early && (int)threadIdx.x < queries * pairs)
@@ -609,7 +629,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     }
     // angles of the block's queries, as many at a time as fit where the probabilities were
     float2* cs = reinterpret_cast<float2*>(sh.p);
-    const bool finish = cut.parts == 1;
+    const bool finish = parts == 1;
     const int batch = early ? queries : pairs ? min(queries, (int)(sizeof(sh.p) / sizeof(float2)) / pairs) : queries;
     for (int first_query = 0; first_query < queries; first_query += batch) {
         const int some = min(batch, queries - first_query);
@@ -645,7 +665,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
                 const v4f y = *reinterpret_cast<const v4f*>(row + (((2 * lane + 1) ^ (hl & 31)) << 2));
                 const int64_t pair = pair0 + hl;
                 if (!finish) {
-                    const int64_t at = pair * cut.parts + part;
+                    const int64_t at = pair * cut.slots() + part;
                     *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = x;
                     *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = y;
                     if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
@@ -667,16 +687,17 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
 // The parts of a row, joined by G wavefronts that take every G-th (o = sum 2^(R_i - R) o_i over sum 2^(R_i - R) l_i), then
 // as above.
 template <int G>
-__global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int parts) {
+__global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, const LocalCut cut) {
     constexpr int kRows = 4 / G;  // of a block
     __shared__ __align__(16) float s_o[4][kD];
     __shared__ float2 s_cs[kRows][kD / 2];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, own = w / G, take = w % G;
     const int64_t all = (int64_t)a.nq * a.heads, at_row = (int64_t)blockIdx.x * kRows + own;
     const bool live = at_row < all;
-    const int64_t pair = live ? at_row : all - 1;
+    const int64_t pair = live ? at_row : all - 1, slots = cut.slots();
+    const int parts = (int)cut.parts_of((uint32_t)(pair % ((int64_t)a.group * a.heads)) / (16 * cut.nh));
     float2 ml{kNone, 0.0f};
-    if (lane < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (pair * parts + lane));
+    if (lane < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (pair * slots + lane));
     uint4 u{};
     float l2 = 0.0f;
     if (take == 0 && a.other) {
@@ -693,7 +714,7 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int 
     float L = f * ml.y;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
-    const float* po = a.part_o + pair * parts * kD + 8 * lane;
+    const float* po = a.part_o + pair * slots * kD + 8 * lane;
     v4f x{}, y{};
 #pragma unroll 4
     for (int i = take; i < parts; i += G) {
@@ -706,7 +727,7 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, int 
         *reinterpret_cast<v4f*>(s_o[w] + 8 * lane + 4) = y;
     }
     __syncthreads();
-    if (take || !live) return;
+    if (take || !live || parts == 1) return;  // (a row in one part is done)
     if constexpr (G > 1) {
 #pragma unroll
         for (int k = 1; k < G; ++k) {
@@ -1107,7 +1128,7 @@ constexpr struct {
 } kLocalTiles[] = {{4, 256, 1.8f, 24.0f, 1.8f, 24.0f}, {2, 256, 1.3f, 13.0f, 1.3f, 13.0f}, {1, 512, 2.5f, 9.0f, 1.9f, 7.3f}};
 
 LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries) {
-    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), 0};
+    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), (uint32_t)up(group * heads, 16), 0};
     float least = 0.0f;
     const auto consider = [&](float time, const LocalCut& cut) {
         if (least == 0.0f || time < least) least = time, best = cut;
@@ -1115,23 +1136,31 @@ LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entr
     for (const auto& t : kLocalTiles) {
         const int64_t rows = 16 * t.nh;
         if (t.nh > 1 && group * heads <= 8 * t.nh) continue;  // half of the tile would be empty
-        const int64_t tiles = up(group * heads, rows), blocks = runs * tiles, steps = std::max<int64_t>(up(entries, kTile), 1);
-        const auto in_parts = [&](int64_t parts) {
-            if (parts < 1 || parts > most || parts > kMostParts || (parts > 1 && parts > steps)) return;
-            const bool alone = blocks * parts <= 256;
-            consider((float)up(blocks * parts, t.places) *
-                             ((float)up(steps, parts) * (alone ? t.step_alone : t.step) + (alone ? t.block_alone : t.block)) +
-                         (parts > 1 ? 6.0f + 5e-4f * (float)(runs * group * heads * parts) : 0.0f),
-                     LocalCut{t.nh, (uint32_t)parts, (uint32_t)tiles, 0});
+        const int64_t tiles = up(group * heads, rows), steps = std::max<int64_t>(up(entries, kTile), 1);
+        // the first `whole` tiles of a run in `parts` parts, the others in one more
+        const auto in_parts = [&](int64_t parts, int64_t whole) {
+            const LocalCut cut{t.nh, (uint32_t)parts, (uint32_t)tiles, (uint32_t)whole, 0};
+            if (parts < 1 || cut.slots() > kMostParts || (cut.slots() > 1 && (cut.slots() > most || cut.slots() > steps))) return;
+            const int64_t n1 = runs * whole * parts, n2 = runs * (tiles - whole) * (parts + 1);
+            const bool alone = n1 + n2 <= 256;
+            const auto one = [&](int64_t n) {
+                return (float)up(steps, n) * (alone ? t.step_alone : t.step) + (alone ? t.block_alone : t.block);
+            };
+            consider(time_of(t.places, n1, one(parts), n2, n2 ? one(parts + 1) : 0.0f) +
+                         (cut.slots() > 1 ? 6.0f + 5e-4f * (float)((n1 + n2) * rows) : 0.0f),
+                     cut);
         };
-        for (int parts = 1; parts <= 8; ++parts) in_parts(parts);
-        for (int rounds = 1; rounds <= 4; ++rounds) in_parts(std::min<int64_t>(rounds * t.places / blocks, kMostParts));
-        for (int parts = 12; parts <= 64; parts += parts >= 32 ? 16 : parts >= 16 ? 8 : 4) in_parts(parts);
+        for (int parts = 1; parts <= 8; ++parts) in_parts(parts, tiles);
+        for (int parts = 12; parts <= 64; parts += parts >= 32 ? 16 : parts >= 16 ? 8 : 4) in_parts(parts, tiles);
+        for (int rounds = 1; rounds <= 8; ++rounds) {  // whole rounds, as nearly as runs alike allow
+            const int64_t of_run = rounds * t.places / runs, parts = of_run / tiles;
+            if (parts >= 1) in_parts(parts, tiles * (parts + 1) - of_run);
+        }
     }
     for (int queries = 1; queries <= most_queries; ++queries) {
         const int64_t tiles = up(queries * heads, 16), last = tiles % 8;
         const float rows = 14.5f * (float)(tiles / 8) + (last == 0 ? 0.0f : last <= 4 ? 9.0f : 14.5f);
-        consider((float)up(runs * up(group, queries), 256) * (12.0f + rows), LocalCut{0, 1, 0, queries});
+        consider((float)up(runs * up(group, queries), 256) * (12.0f + rows), LocalCut{0, 1, 0, 0, queries});
     }
     return best;
 }
@@ -1154,7 +1183,7 @@ size_t local_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
     if (nq <= 0 || entries <= 0) return 16;
     // (how the queries come in runs is not known here: as one, whose tiles are the fewest and parts the most)
     const LocalCut cut = best_local_cut(1, nq, heads, entries, kMostParts, 0);
-    return cut.parts == 1 ? 16 : cut.parts * part_bytes((int64_t)nq * heads);
+    return cut.slots() == 1 ? 16 : cut.slots() * part_bytes((int64_t)nq * heads);
 }
 
 hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream_t stream) {
@@ -1169,11 +1198,11 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
                            per_run, units);
         return hipGetLastError();
     }
-    if (cut.parts > 1) {
+    const uint32_t slots = cut.slots(), units = (uint32_t)runs * cut.of_run();
+    if (slots > 1) {
         a.part_o = (float*)ws;
-        a.part_ml = a.part_o + (size_t)cut.parts * rows * kD;
+        a.part_ml = a.part_o + (size_t)slots * rows * kD;
     }
-    const uint32_t units = (uint32_t)(runs * cut.tiles * cut.parts);
     const auto start = [&](auto nh) {
         constexpr int kNh = decltype(nh)::value;
         const dim3 grid((units + 7) / 8 * 8);
@@ -1196,11 +1225,11 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
     else
         start(std::integral_constant<int, 4>{});
     const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || cut.parts == 1) return err;
-    if (cut.parts > 4)
-        hipLaunchKernelGGL(local_join_kernel<4>, dim3((unsigned)rows), dim3(256), 0, stream, a, (int)cut.parts);
+    if (err != hipSuccess || slots == 1) return err;
+    if (slots > 4)
+        hipLaunchKernelGGL(local_join_kernel<4>, dim3((unsigned)rows), dim3(256), 0, stream, a, cut);
     else
-        hipLaunchKernelGGL(local_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, (int)cut.parts);
+        hipLaunchKernelGGL(local_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, cut);
     return hipGetLastError();
 }
 
