@@ -118,14 +118,15 @@ __device__ __forceinline__ float2 angle_of(const LocalArgs& a, int64_t t, int pa
 // A row's values 8 lane .. + 7, turned by angles cs; row: LDS of its 512 values for pairs that lanes do not hold together
 __device__ __forceinline__ void turn_row(const LocalArgs& a, const float2* cs, float* row, float (&v)[8]) {
     const int lane = threadIdx.x & 63, rot = a.turn.rot, pairs = rot / 2, j0 = 8 * lane - a.turn.offset;
-    if (!a.turn.half && !(a.turn.offset & 1)) {
+    if (!a.turn.half && !((a.turn.offset | rot) & 7)) {  // whole lanes
+        if (j0 < 0 || j0 >= rot) return;
+        const v4f z[2] = {reinterpret_cast<const v4f*>(cs)[j0 >> 2], reinterpret_cast<const v4f*>(cs)[(j0 >> 2) + 1]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (j0 + 2 * i < 0 || j0 + 2 * i >= rot) continue;
-            const float2 z = cs[(j0 >> 1) + i];
+            const float c = z[i >> 1][(i & 1) * 2], s = z[i >> 1][(i & 1) * 2 + 1];
             const float x0 = v[2 * i], x1 = v[2 * i + 1];
-            v[2 * i] = x0 * z.x - x1 * z.y;
-            v[2 * i + 1] = x1 * z.x + x0 * z.y;
+            v[2 * i] = x0 * c - x1 * s;
+            v[2 * i + 1] = x1 * c + x0 * s;
         }
         return;
     }
@@ -675,7 +676,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
                 float v[8] = {x[0] * wt.mine, x[1] * wt.mine, x[2] * wt.mine, x[3] * wt.mine,
                               y[0] * wt.mine, y[1] * wt.mine, y[2] * wt.mine, y[3] * wt.mine};
                 add_other(u[k], wt.other, v);
-                if (pairs) turn_row(a, cs + ((r0 + hl) / a.heads - ta - first_query) * pairs, row, v);
+                if (pairs) turn_row(a, cs + (queries == 1 ? 0 : (r0 + hl) / a.heads - ta - first_query) * pairs, row, v);
                 store_row(a, pair, v);
                 if (a.lse && lane == 0) a.lse[pair] = wt.lse;
             }
@@ -690,7 +691,7 @@ template <int G>
 __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, const LocalCut cut) {
     constexpr int kRows = 4 / G;  // of a block
     __shared__ __align__(16) float s_o[4][kD];
-    __shared__ float2 s_cs[kRows][kD / 2];
+    __shared__ __align__(16) float2 s_cs[kRows][kD / 2];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, own = w / G, take = w % G;
     const int64_t all = (int64_t)a.nq * a.heads, at_row = (int64_t)blockIdx.x * kRows + own;
     const bool live = at_row < all;
