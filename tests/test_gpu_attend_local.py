@@ -277,6 +277,36 @@ def test_the_last_entries_of_the_largest_ring(fx):
     check(got, q, codes, scales, n_vis, 1 << 30, 0.05, where, which=[0, 1, 2], **kw)
 
 
+def test_a_long_run_of_one_head(fx):
+    rng = np.random.default_rng(8)
+    nq, n = 65535, 65700
+    where = dict(pages=rng.integers(0, 200, (1, -(-n // 7))).astype(np.int32), page_size=7, seq=np.zeros(1, np.int32))
+    codes, scales = cache(rng, 1400)
+    q = bf16(2 * rng.standard_normal((nq, 1, 512), dtype=np.float32))
+    n_vis = (n - nq + 1 + np.arange(nq)).astype(np.int32)
+    kw = dict(window=100, group=nq)
+    got = run(fx, q, codes, scales, n_vis, n, 0.05, where, **kw)
+    check(got, q, codes, scales, n_vis, n, 0.05, where, which=[0, 1, nq - 2, nq - 1, *rng.choice(nq, 40, replace=False)], **kw)
+
+
+@pytest.mark.parametrize("window", [3, 0])
+def test_rows_past_32_bits(fx, window):
+    """65535 queries of 128 heads: more than 2^32 values"""
+    rng = np.random.default_rng(9)
+    nq, heads, n = 65535, 128, 5
+    codes, scales = cache(rng, 60)
+    q = torch.empty(nq, heads, 512, dtype=torch.bfloat16, device="cuda").normal_()
+    base = np.arange(nq, dtype=np.int64) % 56
+    n_vis = np.full(nq, n, np.int32)
+    out, lse = torch.zeros_like(q), torch.zeros(nq, heads, device="cuda")
+    ws = fx.workspace(fx.IDX_OP_ATTEND_LOCAL, nq, n, heads)
+    fx.idx_attend_local(q, dev(codes), dev(scales), dev(n_vis), n, 0.05, out, ws, lse=lse, window=window, kv_base=dev(base))
+    for t in (0, 32767, 32768, nq - 1):
+        few = (slice(t, t + 1),)
+        check((out[few].double().cpu().numpy(), lse[few].double().cpu().numpy()), q[few].float().cpu().numpy(), codes, scales,
+              n_vis[few], n, 0.05, dict(kv_base=base[few]), window=window)
+
+
 def test_in_place_of_the_other_part(fx):
     rng = np.random.default_rng(6)
     where, rows = where_of("base", rng, 40, 140, 0)

@@ -269,6 +269,25 @@ def test_rows_past_32_bits(fx):
     assert torch.equal(got, fx.idx_read_rows("local", small_c, small_s, torch.arange(4, device="cuda"), 4))
 
 
+def test_the_most_tokens(fx):
+    """2^24 - 1 of them, one row of x for all: the first and the last have a place"""
+    tokens = (1 << 24) - 1
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(1, 128, device="cuda", generator=g).bfloat16()
+    signs = torch.ones(128, dtype=torch.int8, device="cuda")
+    at = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    at[0], at[-1] = 3, 1
+    codes, scales = torch.zeros(5, 64, dtype=torch.uint8, device="cuda"), torch.zeros(5, 4, dtype=torch.uint8, device="cuda")
+    fx.idx_write_rows("key", x.expand(tokens, 128), codes, scales, at, 5, signs=signs, kv_base=torch.zeros_like(at))
+    want = fx.idx_quantize_q(x, signs)
+    for row in (1, 3):
+        assert torch.equal(codes[row], want[0][0]) and torch.equal(scales[row], want[1][0])
+    assert not codes[[0, 2, 4]].any() and not scales[[0, 2, 4]].any()
+    out = fx.idx_read_rows("key", codes, scales, at, 5, kv_base=torch.zeros_like(at))
+    few = fx.idx_read_rows("key", codes, scales, at[:1], 5, kv_base=torch.zeros_like(at[:1]))
+    assert few.any() and torch.equal(out[:1], few) and torch.equal(out[-1:], few) and not out[1:-1].any()
+
+
 def test_nothing_to_do(fx):
     none = torch.zeros(0, 512, dtype=torch.uint8, device="cuda")
     x, at = torch.zeros(2, 512, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")

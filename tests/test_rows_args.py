@@ -77,6 +77,7 @@ def test_binding_refuses_on_the_host(fx):
             (dict(pages=torch.zeros(1, 0, dtype=torch.int32), page_size=4, seq=at.int(), max_n=0), ValueError),
             (dict(freq=torch.zeros(32, dtype=torch.float64), layout="pairs"), ValueError),
             (dict(freq=torch.zeros(32)), TypeError), (dict(eps=1e-6, gamma=torch.ones(128)), ValueError),
+            (dict(gamma=torch.ones(512)), ValueError),  # without eps there is no norm for it
             (dict(), ValueError)]:  # the last: not on a GPU
         with pytest.raises(error):
             fx.idx_write_rows(**{**good, **change})

@@ -147,7 +147,7 @@ def _rows_ptr(t: torch.Tensor | None) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object in between (2.7 us of a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -363,7 +363,7 @@ def _same_gpu(*tensors) -> None:
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"fp4idx tensors must live on one GPU, got {tensors[0].device} and {t.device}")
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"fp4idx tensors must live on the current GPU, got {tensors[0].device}")
 
 
@@ -587,7 +587,9 @@ def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, 
     at_ptr = _arg(at, torch.int64, (tokens,), "at")
     where = _places(tokens, max_n, ring, kv_base, pages, page_size, seq)
     turn = _turn(pos, freq, tokens, dim, offset, layout)
-    gamma_ptr = None if gamma is None or eps is None else _arg(gamma, torch.float32, (dim,), "gamma")
+    if gamma is not None and eps is None:
+        raise ValueError("gamma needs eps")
+    gamma_ptr = None if gamma is None else _arg(gamma, torch.float32, (dim,), "gamma")
     signs_ptr = None if signs is None else _arg(signs, torch.int8, (DIM,), "signs")
     _same_gpu(codes, scales, x, at, kv_base, pages, seq, pos, freq, gamma, signs)
     _call(lib.idx_write_rows, number, x_ptr, dtype, tokens, stride, int(eps is not None), gamma_ptr, eps or 0.0, *turn,
