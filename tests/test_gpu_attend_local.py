@@ -92,6 +92,9 @@ CASES = [
     (1, 50, 3, 700, 0, "base", False, False, None),
     (300, 1, 2, 70, 64, "base", False, False, None),
     (1, 1, 8, 700, 600, "pages", True, False, None),
+    (250, 1, 50, 90, 80, "base", False, True, (FREQ, 448, "half", 1.0)),
+    (50, 4, 64, 200, 128, "odd", True, True, (FREQ[:17], 4, "interleaved", 1.5)),
+    (140, 1, 32, 128, 0, "pages", False, True, (10000.0 ** (-np.arange(0, 512, 2) / 512), 0, "interleaved", 0.5)),
 ]
 
 
@@ -234,6 +237,43 @@ def test_extreme_values_and_logits(fx):
     for scale in (0.5, -0.5):
         got = run(fx, q, codes, scales, n_vis, n, scale, where, group=2)
         check(got, q, codes, scales, n_vis, n, scale, where, group=2)
+
+
+@pytest.mark.parametrize("nq, heads", [(5, 37), (240, 64)])
+def test_one_query_of_few_entries(fx, nq, heads):
+    """the single query's ways out: hidden rows and absent ones, queries that are not finite, logits far apart"""
+    rng = np.random.default_rng(heads)
+    n, few = 150, [0, 1, 2, 3, 4, nq - 1]
+    codes, scales = cache(rng, 3 * n)
+    codes[n:2 * n], scales[n:2 * n] = 0xFF, 0xFF  # of no sequence
+    rises = np.abs(rng.standard_normal((1, 512))) * np.linspace(0.01, 1.0, n)[:, None]
+    codes[2 * n:], scales[2 * n:] = rows_ref.quantise("local", rises)
+    pages = np.array([[0, 1, 2], [6, 7, 8], [0, -1, 2], [6, 1, 9], [3, 4, 5]], np.int32)
+    seq = rng.integers(0, 4, nq).astype(np.int32)
+    seq[:5] = [0, 1, 2, 3, 7]
+    n_vis = rng.integers(100, n + 1, nq).astype(np.int32)
+    q = bf16(rng.standard_normal((nq, heads, 512)))
+    q[:, 1] = np.abs(q[:, 1])
+    where = dict(pages=pages, page_size=50, seq=seq)
+    for scale in (0.05, -0.3, 1.0):
+        got = run(fx, q, codes, scales, n_vis, n, scale, where, window=110)
+        check(got, q, codes, scales, n_vis, n, scale, where, window=110, which=few)
+    assert np.isneginf(got[1][4]).all() and (got[0][4] == 0).all()
+    q[0, 2, 100], q[1, 0, 0], q[2, 5, 511], q[3, 36, 17], q[4, 1, 1] = np.nan, np.inf, -np.inf, np.nan, np.nan
+    bad = np.zeros((nq, heads), bool)
+    bad[0, 2] = bad[1, 0] = bad[2, 5] = bad[3, 36] = True
+    again = run(fx, q, codes, scales, n_vis, n, 1.0, where, window=110)
+    assert np.isnan(again[1][bad]).all() and np.isnan(again[0][bad]).all()
+    assert np.array_equal(again[0][~bad], got[0][~bad]) and np.array_equal(again[1][~bad], got[1][~bad])
+    # hidden by the window, by n_vis, and in the middle of what query 1 alone sees
+    n_vis[:], seq[:], n_vis[1], seq[1] = 140, 0, 130, 1
+    want = run(fx, q, codes, scales, n_vis, n, 0.05, where, window=100)
+    codes[[3, 39, 140, 149]], scales[[0, 20, 145]], codes[2 * n + 60, 400] = 0xFF, 0xFF, 0xFF
+    got = run(fx, q, codes, scales, n_vis, n, 0.05, where, window=100)
+    assert np.isnan(got[1][1]).all() and np.isnan(got[0][1]).all()
+    rest = np.arange(nq) != 1
+    assert np.array_equal(got[0][rest], want[0][rest], equal_nan=True)
+    assert np.array_equal(got[1][rest], want[1][rest], equal_nan=True)
 
 
 def test_a_cache_past_32_bits(fx):

@@ -54,28 +54,29 @@ __device__ __forceinline__ float group_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// ROWS query rows, one after another from `at` on (those past the first `left` as zeros): read, a row per wavefront and
-// step, 8 values per lane; then into LDS as scaled fp16, and per head the factor that turns a dot product of theirs into s2.
-template <int ROWS>
+// ROWS query rows, one after another from `at` on (those past the first `left` as zeros): read by WAVES wavefronts, a row
+// per wavefront and step, 8 values per lane; then into LDS as scaled fp16, and per head the factor that turns a dot product
+// of theirs into s2.
+template <int ROWS, int WAVES = 4>
 struct QueryRows {
-    uint4 raw[ROWS / 4];
+    uint4 raw[ROWS / WAVES];
 };
-template <int ROWS>
-__device__ __forceinline__ void load_query(const uint16_t* at, int left, QueryRows<ROWS>& q) {
+template <int ROWS, int WAVES = 4>
+__device__ __forceinline__ void load_query(const uint16_t* at, int left, QueryRows<ROWS, WAVES>& q) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
-    for (int i = 0; i < ROWS / 4; ++i) {
-        const int h = w * (ROWS / 4) + i, hc = h < left ? h : left - 1;
+    for (int i = 0; i < ROWS / WAVES; ++i) {
+        const int h = w * (ROWS / WAVES) + i, hc = h < left ? h : left - 1;
         q.raw[i] = *reinterpret_cast<const uint4*>(at + hc * kD + lane * 8);
     }
 }
-template <int ROWS>
-__device__ __forceinline__ void stage_query(float scale, int left, QueryRows<ROWS>& q, _Float16* lds, float2* factor) {
+template <int ROWS, int WAVES = 4>
+__device__ __forceinline__ void stage_query(float scale, int left, QueryRows<ROWS, WAVES>& q, _Float16* lds, float2* factor) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int i = 0; i < ROWS / 4; ++i) {
-        const int row = w * (ROWS / 4) + i;
+    for (int i = 0; i < ROWS / WAVES; ++i) {
+        const int row = w * (ROWS / WAVES) + i;
         const uint32_t keep = row < left ? 0xffffffffu : 0u;
         const uint32_t v[4] = {q.raw[i].x & keep, q.raw[i].y & keep, q.raw[i].z & keep, q.raw[i].w & keep};
         us2 two = {0, 0};  // the largest magnitude of each half

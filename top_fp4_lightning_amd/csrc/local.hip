@@ -70,11 +70,12 @@ __device__ __forceinline__ h8 local_values8(const LocalPart& r, int x) {
 
 // How a call is cut: blocks (tiles) of 16 nh rows of a run's heads x queries, the first `whole` tiles of a run over `parts`
 // parts of its entries, the others over one more, so that blocks come in whole rounds over the compute units; or, with
-// `queries` above 0, blocks of the window kernel over so many queries.
+// `queries` above 0, blocks of the window kernel over so many queries; or, with `one` above 0, blocks of one query and so many
+// times 16 heads.
 struct LocalCut {
     int nh;
     uint32_t parts, tiles, whole;
-    int queries;
+    int queries, one;
     __host__ __device__ uint32_t of_run() const { return tiles * (parts + 1) - whole; }
     __host__ __device__ uint32_t slots() const { return parts + (whole < tiles); }  // of a row's parts
     __device__ uint32_t parts_of(uint32_t tile) const { return parts + (tile >= whole); }
@@ -767,6 +768,65 @@ struct WindowShared {
 // Rows of a transposed read (4) and of an ordinary one (16) exchanged so that they lie in different banks.
 __device__ __forceinline__ int win_swap(int row) { return (row & 3) * 2 + ((row >> 2) & 1) * 8 + ((row >> 3) & 1); }
 
+// this lane's eight values of finish64
+__device__ __forceinline__ int of_64(int g) { return (g & 1) * 16 + (g & 2) * 4; }
+// Values `from` .. + 63 of a row, in four tiles o of 16 where a lane has four of each (4 g ..), joined with the other part's
+// u, turned and written. Lane groups exchange halves of two tiles: eight values in a row each, of 32 by 32 two at a time.
+__device__ __forceinline__ void finish64(const LocalArgs& a, int64_t pair, bool live, int from, const v4f* o, const uint4* u,
+                                         const Weights& wt, const float2* cs) {
+    const int mine8 = of_64((threadIdx.x & 63) >> 4), at = from + mine8, pairs = a.turn.freq ? a.turn.rot / 2 : 0;
+    const int turn_at = a.turn.freq ? a.turn.offset : kD;
+    float v[2][8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const v4f x = o[2 * b], z = o[2 * b + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(z[i]), false, false);
+            v[b][i] = __uint_as_float(sw[0]) * wt.mine;
+            v[b][4 + i] = __uint_as_float(sw[1]) * wt.mine;
+        }
+        const uint32_t x2[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[b][2 * i] = fmaf(wt.other, __uint_as_float(x2[i] << 16), v[b][2 * i]);
+            v[b][2 * i + 1] = fmaf(wt.other, __uint_as_float(x2[i] & 0xffff0000u), v[b][2 * i + 1]);
+        }
+    }
+    const int from_turn = from - turn_at;  // of the block's first value
+    if (from_turn > -64 && from_turn < 2 * pairs) {
+        if (a.turn.half) {  // 64 values at a multiple of 64
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 z = cs[mine8 + i];
+                const float x0 = v[0][i], x1 = v[1][i];
+                v[0][i] = x0 * z.x - x1 * z.y;
+                v[1][i] = x1 * z.x + x0 * z.y;
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = at + 32 * b + 2 * i - turn_at;
+                    if (j < 0 || j >= 2 * pairs) continue;
+                    const float2 z = cs[j >> 1];
+                    const float x0 = v[b][2 * i], x1 = v[b][2 * i + 1];
+                    v[b][2 * i] = x0 * z.x - x1 * z.y;
+                    v[b][2 * i + 1] = x1 * z.x + x0 * z.y;
+                }
+            }
+        }
+    }
+    if (live) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            *reinterpret_cast<uint4*>(a.out + pair * kD + at + 32 * b) =
+                uint4{bf16_pair(v[b][0], v[b][1]), bf16_pair(v[b][2], v[b][3]), bf16_pair(v[b][4], v[b][5]),
+                      bf16_pair(v[b][6], v[b][7])};
+    }
+}
+
 __global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const LocalArgs a, int queries, uint32_t per_run,
                                                                        uint32_t units) {
     __shared__ __align__(16) WindowShared sh;
@@ -1007,13 +1067,12 @@ __global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const Loc
             const int entry = 4 * g + (c >> 2);
             int at_value = entry * kD + (((c & 3) >> 1) ^ win_swap(entry)) * 8 + (c & 1) * 4;
             asm volatile("" : "+v"(at_value));
-            const int turn_at = a.turn.freq ? a.turn.offset : kD;
             const float2* cs = sh.cs + query * pairs;
 #pragma unroll 1
             for (int half = 0; half < kWinCuts; ++half) {
                 constexpr int kTwos = 8 / kWinCuts, kValues = kD / kWinCuts;  // blocks of 64 values
                 v4f o[4 * kTwos] = {};
-                const int mine8 = (g & 1) * 16 + (g & 2) * 4;  // see below
+                const int mine8 = of_64(g);
                 uint4 u[2 * kTwos] = {};
                 if (wt.other != 0.0f) {  // (what lies in a part of no weight has no effect)
 #pragma unroll
@@ -1043,59 +1102,9 @@ __global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const Loc
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                // Lane groups exchange halves of two tiles: eight values in a row each, of 32 by 32 two at a time.
 #pragma unroll
                 for (int two = 0; two < kTwos; ++two) {
-                    const int at = half * kValues + two * 64 + mine8;
-                    float v[2][8];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const v4f x = o[4 * two + 2 * b], z = o[4 * two + 2 * b + 1];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(z[i]), false, false);
-                            v[b][i] = __uint_as_float(sw[0]) * wt.mine;
-                            v[b][4 + i] = __uint_as_float(sw[1]) * wt.mine;
-                        }
-                        const uint32_t x2[4] = {u[2 * two + b].x, u[2 * two + b].y, u[2 * two + b].z, u[2 * two + b].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[b][2 * i] = fmaf(wt.other, __uint_as_float(x2[i] << 16), v[b][2 * i]);
-                            v[b][2 * i + 1] = fmaf(wt.other, __uint_as_float(x2[i] & 0xffff0000u), v[b][2 * i + 1]);
-                        }
-                    }
-                    const int from_turn = half * kValues + two * 64 - turn_at;  // of the block's first value
-                    if (from_turn > -64 && from_turn < 2 * pairs) {
-                        if (a.turn.half) {  // 64 values at a multiple of 64
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 z = cs[mine8 + i];
-                                const float x0 = v[0][i], x1 = v[1][i];
-                                v[0][i] = x0 * z.x - x1 * z.y;
-                                v[1][i] = x1 * z.x + x0 * z.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int j = at + 32 * b + 2 * i - turn_at;
-                                    if (j < 0 || j >= 2 * pairs) continue;
-                                    const float2 z = cs[j >> 1];
-                                    const float x0 = v[b][2 * i], x1 = v[b][2 * i + 1];
-                                    v[b][2 * i] = x0 * z.x - x1 * z.y;
-                                    v[b][2 * i + 1] = x1 * z.x + x0 * z.y;
-                                }
-                            }
-                        }
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-                            *reinterpret_cast<uint4*>(a.out + pair * kD + at + 32 * b) =
-                                uint4{bf16_pair(v[b][0], v[b][1]), bf16_pair(v[b][2], v[b][3]), bf16_pair(v[b][4], v[b][5]),
-                                      bf16_pair(v[b][6], v[b][7])};
-                    }
+                    finish64(a, pair, live, half * kValues + two * 64, o + 4 * two, u + 2 * two, wt, cs);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -1105,15 +1114,190 @@ __global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const Loc
     }
 }
 
+// ---- one query, few entries ----
+// One query that sees at most 128 entries, a decode step's window: eight wavefronts read and widen 16 entries each and keep
+// them in registers and LDS. Then 16 heads at a time: each wavefront multiplies its entries with them and leaves the
+// probabilities in LDS, against a reference of its own; behind a barrier each multiplies 64 values of all the entries with
+// the probabilities, brought to the largest of the references (powers of two), and finishes them. A wavefront reads two
+// whole rows at once: of 16 rows a piece each, its lanes' addresses alone take 64 cycles (128 rows 1.7 us). One query of 64
+// heads over 128 entries, joined and turned: 7.6 us in four blocks, 10.25 by the kernel above, in two steps of 64 entries.
+// What bounds it is one wavefront's way through: five loads one behind the other, LDS, two barriers.
+constexpr int kOneKeys = 128;
+struct OneShared {
+    _Float16 kv[kOneKeys * kD];  // a row's first half holds its codes before
+    _Float16 q[16 * kRow];
+    _Float16 p[8][16][16];  // by wavefront, head and entry
+    float m[16][8], l[16][8];
+    float2 fr[16];
+    float2 cs[kD / 2];
+};
+
+__global__ __launch_bounds__(512) void attend_one_kernel(const LocalArgs a, int tiles, uint32_t per_query, uint32_t units) {
+    __shared__ __align__(16) OneShared sh;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int g = lane >> 4, c = lane & 15;
+    const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= share || unit >= units) return;
+    const int64_t t = unit / per_query, run = t / a.group;
+    const int first = (int)(unit % per_query) * tiles * 16, stop = min(first + tiles * 16, a.heads);
+
+    QueryRows<16, 8> qr;
+    load_query<16, 8>(a.q + (t * a.heads + first) * kD, stop - first, qr);
+    const int2 see = seen_by(a, t);
+    const int count = see.y - see.x;
+    int32_t row = -1;  // of entry 16 w + c
+    if (16 * w + c < count && a.places.rows > 0)
+        row = (int32_t)row_at(a.places, a.places.seq ? (int64_t)a.places.seq[run] : run, a.places.base ? a.places.base[run] : 0,
+                              (int64_t)see.x + 16 * w + c);
+    // two rows at a time, whole
+    uint4 code[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int even = __builtin_amdgcn_readlane(row, 2 * i), odd = __builtin_amdgcn_readlane(row, 2 * i + 1);
+        const int r = lane < 32 ? even : odd;
+        code[i] = uint4{0, 0, 0, 0};
+        if (r >= 0) code[i] = *reinterpret_cast<const uint4*>(a.codes + (int64_t)r * kD + 16 * (lane & 31));
+    }
+    LocalPart kv;
+    kv.scale = row >= 0 ? load_scale(a, row, g) : 0;
+    const uint32_t seen = (uint32_t)__ballot(row >= 0) >> (4 * g);
+    uint4 u[2] = {};
+    float l2 = 0.0f;
+    const auto load_other = [&](int head) {
+        if (!a.other) return;
+        const int64_t pair = t * a.heads + min(head + c, stop - 1);
+        l2 = a.other_lse[pair];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) u[b] = *reinterpret_cast<const uint4*>(a.other + pair * kD + 64 * w + 32 * b + of_64(g));
+    };
+    load_other(first);
+    if (a.turn.freq && (int)threadIdx.x < a.turn.rot / 2) sh.cs[threadIdx.x] = angle_of(a, t, threadIdx.x);
+    stage_query<16, 8>(a.scale, stop - first, qr, sh.q, sh.fr);
+    // A row's codes through its place in LDS, from two rows a wavefront to this lane's part of one (piece p of entry e at
+    // p ^ e: sixteen entries' same pieces, and a row's, in different banks)
+    uint4* raw = reinterpret_cast<uint4*>(sh.kv) + 16 * w * 64;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = 2 * i + (lane >> 5);
+        raw[e * 64 + ((lane & 31) ^ e)] = code[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) kv.code[j] = raw[c * 64 + ((8 * g + j) ^ c)];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    h8 keys[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+        keys[x] = local_values8(kv, x);
+        *reinterpret_cast<h8*>(sh.kv + (16 * w + c) * kD + ((16 * g + x) ^ win_swap(c)) * 8) = keys[x];
+    }
+
+    for (int head = first;;) {
+        const int left = min(stop - head, 16);
+        const int64_t pair = t * a.heads + head + min(c, left - 1);
+        __syncthreads();  // the queries are there; the tile before is done with the probabilities
+        v4f s[2] = {};
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            const h8 q = *reinterpret_cast<const h8*>(sh.q + c * kRow + g * 128 + x * 8);
+            s[x & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(keys[x], q, s[x & 1], 0, 0, 0);
+        }
+        const bool more = head + 16 < stop;
+        if (more) load_query<16, 8>(a.q + (t * a.heads + head + 16) * kD, stop - head - 16, qr);
+        {
+            const float fr = sh.fr[c].x;
+            float y[4], top = ninf(), l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = seen >> i & 1 ? (s[0][i] + s[1][i]) * fr : ninf();
+                top = fmaxf(top, y[i]);
+            }
+            top = group_max(top);
+            const float R = top > ninf() ? ceilf(top) - 15.0f : 0.0f;  // probabilities as the window kernel's
+            h4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float ex = __builtin_amdgcn_exp2f(y[i] - R);
+                l += ex;
+                p[i] = (_Float16)ex;
+            }
+            l = group_sum(l);
+            *reinterpret_cast<h4*>(&sh.p[w][c][4 * g]) = p;
+            if (g == 0) sh.m[c][w] = top > ninf() ? R : kNone, sh.l[c][w] = l;
+        }
+        __syncthreads();
+
+        // The wavefronts' references below the largest (none: far enough below). Their probabilities are brought to it in
+        // fp16, rounded where they leave its normal numbers: below 2^-28 of the largest.
+        int down[8];
+        float R = kNone, L = 0.0f;
+        {
+            const v4f m[2] = {*reinterpret_cast<const v4f*>(sh.m[c]), *reinterpret_cast<const v4f*>(sh.m[c] + 4)};
+            const v4f l[2] = {*reinterpret_cast<const v4f*>(sh.l[c]), *reinterpret_cast<const v4f*>(sh.l[c] + 4)};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) R = fmaxf(R, m[k >> 2][k & 3]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float d = fmaxf(m[k >> 2][k & 3] - R, -128.0f);
+                down[k] = (int)d;
+                L = fmaf(l[k >> 2][k & 3], __builtin_amdgcn_exp2f(d), L);
+            }
+        }
+        const Weights wt = join_weights(a, l2, R, L);
+        if (wt.other == 0.0f) u[0] = u[1] = uint4{0, 0, 0, 0};  // (what lies in a part of no weight has no effect)
+        // the values' transposed reads go by the order in which the probabilities lie (as in the window kernel)
+        const int entry = 4 * g + (c >> 2);
+        const int at_value = entry * kD + (((c & 3) >> 1) ^ win_swap(entry)) * 8 + (c & 1) * 4;
+        v4f o[4] = {};
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            if (16 * k >= count) continue;
+            h8 p;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const h4 x = *reinterpret_cast<const h4*>(&sh.p[k + half][c][4 * g]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[4 * half + i] = __builtin_ldexpf16(x[i], down[k + half]);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int tile = 4 * w + d;
+                const _Float16* at = sh.kv + k * 16 * kD + (at_value ^ ((tile & 7) * 16)) + (tile >> 3) * 128;
+                const hv4 low = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)at);
+                const hv4 high = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_hv4*)(at + 16 * kD));
+                h8 v;
+                __builtin_memcpy(&v, &low, 8);
+                __builtin_memcpy((char*)&v + 8, &high, 8);
+                o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, o[d], 0, 0, 0);
+            }
+        }
+        if (more) stage_query<16, 8>(a.scale, stop - head - 16, qr, sh.q, sh.fr);
+        finish64(a, pair, c < left, 64 * w, o, u, wt, sh.cs);
+        if (a.lse && w == 0 && lane < left) a.lse[pair] = wt.lse;
+        if (!more) break;
+        head += 16;
+        load_other(head);
+    }
+}
+
+// whether the pairs of a rotation lie as finish64 takes them
+bool turned_by_64(const LocalArgs& a) {
+    return !a.turn.freq || (a.turn.half ? a.turn.rot == 64 && a.turn.offset % 64 == 0 : a.turn.offset % 2 == 0);
+}
 // The most queries that a block of the window kernel takes; 0: the call is not for it.
 int window_queries(const LocalArgs& a) {
-    if (a.window <= 0 || a.window > kWinKeys) return 0;
+    if (a.window <= 0 || a.window > kWinKeys || !turned_by_64(a)) return 0;
     int64_t most = std::min<int64_t>({kWinKeys - a.window + 1, kWinQueries, a.group});
-    if (a.turn.freq) {
-        if (a.turn.half ? a.turn.rot != 64 || a.turn.offset % 64 != 0 : a.turn.offset % 2 != 0) return 0;
-        most = std::min<int64_t>(most, kWinAngles / (a.turn.rot / 2));
-    }
+    if (a.turn.freq) most = std::min<int64_t>(most, kWinAngles / (a.turn.rot / 2));
     return (int)most;
+}
+// whether the kernel of one query and few entries can take the call
+bool one_query(const LocalArgs& a) {
+    const int64_t entries = a.window > 0 ? std::min(a.window, a.places.max_n) : a.places.max_n;
+    return entries <= kOneKeys && (a.group == 1 || a.heads % 16 == 0) && turned_by_64(a);
 }
 
 constexpr int64_t up(int64_t x, int64_t by) { return (x + by - 1) / by; }
@@ -1121,15 +1305,17 @@ size_t part_bytes(int64_t rows) { return (size_t)rows * (kD + 2) * sizeof(float)
 
 // The cut that takes the least time on 256 compute units, by what was measured (microseconds): a block of 16, 32 or 64 rows
 // kLocalTiles' apart from its steps and for each step of 64 entries (1 .. 1024 queries of 1 .. 128 heads over 1000 .. 65536
-// entries); a join 4, and its parts at 4 TB/s; a block of the window kernel 12, and 14.5 for each 128 rows (9 for a
-// last 64). `most`: parts that the workspace has room for. most_queries: window_queries().
+// entries); a join 4, and its parts at 4 TB/s; a block of the window kernel 17, and 14.5 for each 128 rows (9 for a
+// last 64); one of one query 3.6, 3.5 for each 16 heads, and 2 shared by the blocks that read the same entries (16 .. 2048
+// queries of 16 .. 128 heads; 64 heads over 128 entries: 64 queries 8.6 us and 11.1 without, 256 21.0 and 27.2, 1024 78 and
+// 110). `most`: parts that the workspace has room for. most_queries: window_queries(). one: one_query().
 constexpr struct {
     int nh, places;
     float step, block, step_alone, block_alone;
 } kLocalTiles[] = {{4, 256, 1.8f, 24.0f, 1.8f, 24.0f}, {2, 256, 1.3f, 13.0f, 1.3f, 13.0f}, {1, 512, 2.5f, 9.0f, 1.9f, 7.3f}};
 
-LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries) {
-    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), (uint32_t)up(group * heads, 16), 0};
+LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries, bool one) {
+    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), (uint32_t)up(group * heads, 16), 0, 0};
     float least = 0.0f;
     const auto consider = [&](float time, const LocalCut& cut) {
         if (least == 0.0f || time < least) least = time, best = cut;
@@ -1140,7 +1326,7 @@ LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entr
         const int64_t tiles = up(group * heads, rows), steps = std::max<int64_t>(up(entries, kTile), 1);
         // the first `whole` tiles of a run in `parts` parts, the others in one more
         const auto in_parts = [&](int64_t parts, int64_t whole) {
-            const LocalCut cut{t.nh, (uint32_t)parts, (uint32_t)tiles, (uint32_t)whole, 0};
+            const LocalCut cut{t.nh, (uint32_t)parts, (uint32_t)tiles, (uint32_t)whole, 0, 0};
             if (parts < 1 || cut.slots() > kMostParts || (cut.slots() > 1 && (cut.slots() > most || cut.slots() > steps))) return;
             const int64_t n1 = runs * whole * parts, n2 = runs * (tiles - whole) * (parts + 1);
             const bool alone = n1 + n2 <= 256;
@@ -1161,18 +1347,24 @@ LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entr
     for (int queries = 1; queries <= most_queries; ++queries) {
         const int64_t tiles = up(queries * heads, 16), last = tiles % 8;
         const float rows = 14.5f * (float)(tiles / 8) + (last == 0 ? 0.0f : last <= 4 ? 9.0f : 14.5f);
-        consider((float)up(runs * up(group, queries), 256) * (12.0f + rows), LocalCut{0, 1, 0, 0, queries});
+        consider((float)up(runs * up(group, queries), 256) * (17.0f + rows), LocalCut{0, 1, 0, 0, queries, 0});
+    }
+    const int64_t all = up(heads, 16);
+    for (int tiles = 1; one && tiles <= all; ++tiles) {
+        const int64_t blocks = up(all, tiles);
+        consider((float)up(runs * group * blocks, 256) * (3.6f + 3.5f * (float)tiles + 2.0f / (float)blocks),
+                 LocalCut{0, 1, 0, 0, 0, tiles});
     }
     return best;
 }
 
 // The same for the sizes asked for last: the next call mostly has the same.
-LocalCut local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries) {
-    thread_local int64_t of[6] = {0, 0, 0, 0, 0, 0};
+LocalCut local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries, bool one) {
+    thread_local int64_t of[7] = {0, 0, 0, 0, 0, 0, 0};
     thread_local LocalCut cut{};
-    const int64_t now[6] = {runs, group, heads, entries, most, most_queries};
+    const int64_t now[7] = {runs, group, heads, entries, most, most_queries, one};
     if (memcmp(of, now, sizeof(of))) {
-        cut = best_local_cut(runs, group, heads, entries, most, most_queries);
+        cut = best_local_cut(runs, group, heads, entries, most, most_queries, one);
         memcpy(of, now, sizeof(of));
     }
     return cut;
@@ -1183,7 +1375,7 @@ LocalCut local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, 
 size_t local_workspace_bytes(int32_t nq, int32_t heads, int64_t entries) {
     if (nq <= 0 || entries <= 0) return 16;
     // (how the queries come in runs is not known here: as one, whose tiles are the fewest and parts the most)
-    const LocalCut cut = best_local_cut(1, nq, heads, entries, kMostParts, 0);
+    const LocalCut cut = best_local_cut(1, nq, heads, entries, kMostParts, 0, false);
     return cut.slots() == 1 ? 16 : cut.slots() * part_bytes((int64_t)nq * heads);
 }
 
@@ -1192,7 +1384,13 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
     int64_t entries = a.places.max_n;
     if (a.window > 0) entries = std::min(entries, a.window + std::min<int64_t>(a.group, 16) - 1);
     const int64_t room = std::min<int64_t>(kMostParts, ws_bytes / part_bytes(rows));
-    LocalCut cut = local_cut(runs, a.group, a.heads, entries, std::max<int64_t>(room, 1), window_queries(a));
+    LocalCut cut = local_cut(runs, a.group, a.heads, entries, std::max<int64_t>(room, 1), window_queries(a),
+                             one_query(a));
+    if (cut.one) {
+        const uint32_t per_query = (uint32_t)up(up(a.heads, 16), cut.one), units = (uint32_t)a.nq * per_query;
+        hipLaunchKernelGGL(attend_one_kernel, dim3((units + 7) / 8 * 8), dim3(512), 0, stream, a, cut.one, per_query, units);
+        return hipGetLastError();
+    }
     if (cut.queries) {
         const uint32_t per_run = (uint32_t)up(a.group, cut.queries), units = (uint32_t)runs * per_run;
         hipLaunchKernelGGL(attend_window_kernel, dim3((units + 7) / 8 * 8), dim3(64 * kWinWaves), 0, stream, a, cut.queries,
