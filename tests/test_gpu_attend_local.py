@@ -160,6 +160,47 @@ def test_parts_of_long_ranges(fx, runs, group, heads, n):
         check(got, q, codes, scales, n_vis, n, 0.04, where, group=group, which=some)
 
 
+@pytest.mark.parametrize("runs, group, heads, n, kind", [(64, 1, 16, 8000, "base"), (5, 2, 64, 20000, "pages"),
+                                                         (33, 3, 20, 8192, "odd"), (2, 8, 128, 4097, "base")])
+def test_runs_of_different_lengths(fx, runs, group, heads, n, kind):
+    """long ranges whose lengths differ from run to run and within one: steps marked as above, one cache for all"""
+    rng = np.random.default_rng(runs)
+    page = {"base": 1, "pages": 64, "odd": 7}[kind]
+    rows = n + 64 * runs + page
+    v = 0.01 * rng.standard_normal((rows, 512))
+    i = np.arange(rows)
+    v[i, i // 64 % 400] = 6.0
+    v[i, 400 + i % 64] = 6.0
+    codes, scales = rows_ref.quantise("local", v)
+    if kind == "base":
+        where = dict(kv_base=64 * np.arange(runs, dtype=np.int64))
+    else:
+        pages = np.arange(runs)[:, None] * 64 // page + np.arange(-(-n // page))
+        where = dict(pages=pages.astype(np.int32), page_size=page, seq=rng.permutation(runs).astype(np.int32))
+    q = bf16(0.05 * rng.standard_normal((runs * group, heads, 512)))
+    ws = torch.full((fx.workspace_size(fx.IDX_OP_ATTEND_LOCAL, runs * group, n, heads) + 4096,), 255, dtype=torch.uint8,
+                    device="cuda")
+    for lengths in ("any", "few", "alike", "none"):
+        last = {"any": rng.integers(0, n + 1, runs), "few": np.full(runs, 70), "alike": np.full(runs, n),
+                "none": np.zeros(runs)}[lengths].astype(np.int64)
+        if lengths == "few":
+            last[-1], last[0] = n, -3
+        n_vis = (last[:, None] - np.arange(group)[::-1]).reshape(-1).astype(np.int32)
+        if group > 2:
+            n_vis[1] = n + 5
+            n_vis[-2] = 0
+        got = run(fx, q, codes, scales, n_vis, n, 0.04, where, group=group, ws=ws)
+        some = sorted({0, 1, 2, runs * group // 2, runs * group - 2, runs * group - 1})
+        check(got, q, codes, scales, n_vis, n, 0.04, where, group=group, which=some)
+        again = run(fx, q, codes, scales, n_vis, n, 0.04, where, group=group, ws=ws)
+        assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+        # the parts' borders lie elsewhere, and every run's results within the bounds of both
+        whole = run(fx, q, codes, scales, n_vis, n, 0.04, where, group=group,
+                    ws=torch.full((16,), 255, dtype=torch.uint8, device="cuda"))
+        assert np.abs(got[0] - whole[0]).max() <= 2.0 ** -8 * max(np.abs(whole[0]).max(), 1.0)
+        assert np.array_equal(np.isneginf(got[1]), np.isneginf(whole[1]))
+
+
 def test_what_lies_behind_masks(fx):
     """rows that no query sees, and rows that only some queries of a block see, may hold NaN codes"""
     rng = np.random.default_rng(0)

@@ -26,6 +26,8 @@ namespace fp4idx {
 namespace {
 
 constexpr int kMostParts = 64;  // of a run's entries (a lane each when they are joined)
+constexpr int kShares = 64;     // runs (a lane each) whose blocks are shared out on the device,
+constexpr int kShareGroup = 8;  // and queries of one
 
 // what a block's rows see
 struct Span {
@@ -71,11 +73,12 @@ __device__ __forceinline__ h8 local_values8(const LocalPart& r, int x) {
 // How a call is cut: blocks (tiles) of 16 nh rows of a run's heads x queries, the first `whole` tiles of a run over `parts`
 // parts of its entries, the others over one more, so that blocks come in whole rounds over the compute units; or, with
 // `queries` above 0, blocks of the window kernel over so many queries; or, with `one` above 0, blocks of one query and so many
-// times 16 heads.
+// times 16 heads. With `shared` the blocks are shared out on the device, by what the runs see (see share_of).
 struct LocalCut {
     int nh;
     uint32_t parts, tiles, whole;
     int queries, one;
+    bool shared;
     __host__ __device__ uint32_t of_run() const { return tiles * (parts + 1) - whole; }
     __host__ __device__ uint32_t slots() const { return parts + (whole < tiles); }  // of a row's parts
     __device__ uint32_t parts_of(uint32_t tile) const { return parts + (tile >= whole); }
@@ -150,6 +153,53 @@ __device__ __forceinline__ void store_row(const LocalArgs& a, int64_t pair, cons
         uint4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
 }
 
+// The sum over a wavefront
+__device__ __forceinline__ int wave_sum(int v) {
+    v += (int)dpp<0xB1>((uint32_t)v);   // quad_perm [1,0,3,2]
+    v += (int)dpp<0x4E>((uint32_t)v);   // quad_perm [2,3,0,1]
+    v += (int)dpp<0x141>((uint32_t)v);  // row_half_mirror
+    v += (int)dpp<0x140>((uint32_t)v);  // row_mirror
+    const auto s = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+    v = (int)(s[0] + s[1]);
+    const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+    return __builtin_amdgcn_readfirstlane((int)(r[0] + r[1]));
+}
+// Blocks for runs of different lengths (at most 64, a lane each): parts of as few steps as the blocks suffice for, so that
+// the blocks end together; every run has one at least. A lane gets its run's first block and number of parts.
+__device__ __forceinline__ int2 share_of(const LocalArgs& a, int tiles, int blocks) {
+    const int lane = threadIdx.x & 63, runs = a.nq / a.group;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kShareGroup; ++j)
+        n = max(n, seen_by(a, (int64_t)min(lane, runs - 1) * a.group + min(j, a.group - 1)).y);
+    if (lane >= runs) n = 0;
+    const int steps = (n + kTile - 1) / kTile, all = wave_sum(steps);
+    int most = steps;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+    const auto parts_at = [&](int per) { return lane < runs ? max((steps + per - 1) / per, 1) : 0; };
+    // The smallest number of steps whose parts the blocks suffice for lies in low .. high: a part has at most that many, and
+    // parts come to at most all / steps + runs.
+    const int64_t total = (int64_t)all * tiles;
+    int low = max(max((int)((total + blocks - 1) / blocks), (most + kMostParts - 1) / kMostParts), 1), high = max(most, low);
+    if (blocks > runs * tiles) high = max((int)min((int64_t)high, total / (blocks - runs * tiles) + 1), low);
+    while (low < high) {
+        const int per = (low + high) / 2;
+        if (wave_sum(parts_at(per)) * tiles <= blocks)
+            high = per;
+        else
+            low = per + 1;
+    }
+    const int parts = parts_at(low);
+    int first = parts * tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int before = __shfl_up(first, d);
+        if (lane >= d) first += before;
+    }
+    return int2{first - parts * tiles, parts};
+}
+
 // NH: rows of a block in sixteens. Blocks of 16 rows come in pairs on a compute unit, half its registers each and one
 // step's rows in LDS: the two products of a block take turns, and the blocks cover each other's waits. The others have it
 // to themselves, and two steps' rows. (Pairs of 32 rows spill registers: 3.4 ms for 514 queries over 16384 entries.)
@@ -169,18 +219,31 @@ struct LocalShared {
     _Float16 q[NH * 16 * kQRow];  // the queries' last fragment (the registers hold 15 of 16)
 };
 
-// WINDOW: of a window's entries, perhaps in a ring; else of all visible ones. (A template argument: a branch inside a turn of
-// the pipe costs the blocks of 64 rows a sixth.)
-template <int NH, bool PAGED, bool WINDOW>
+// Of a window's entries, perhaps in a ring, or of all visible ones, these in blocks shared out on the device or not. (Template
+// arguments: a branch inside a turn of the pipe costs the blocks of 64 rows a sixth, and the few more values that the shared
+// blocks keep cost the others a twentieth, in spilled registers.)
+enum Entries { kAll, kShared, kWindow };
+template <int NH, bool PAGED, Entries ENTRIES>
 __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kernel(const LocalArgs a, const LocalCut cut, uint32_t units) {
     __shared__ __align__(16) LocalShared<NH> sh;
-    constexpr bool PAIR = kLocalPair<NH>;
+    constexpr bool PAIR = kLocalPair<NH>, WINDOW = ENTRIES == kWindow;
     constexpr int kRows = NH * 16;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int g = lane >> 4, c = lane & 15;
-    uint32_t run32, tile, part;
-    if (cut.whole == cut.tiles) {
+    uint32_t run32, tile, part, parts, unit_of = 0;
+    if constexpr (ENTRIES == kShared) {
+        const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+        if ((blockIdx.x >> 3) >= share || unit >= units) return;
+        const int2 own = share_of(a, (int)cut.tiles, (int)units);
+        if (unit == 0 && w == 0 && lane < a.nq / a.group) a.shares[lane] = own;
+        run32 = (uint32_t)__builtin_popcountll(__ballot(own.y > 0 && own.x <= (int)unit)) - 1;
+        const uint32_t v = unit - (uint32_t)__builtin_amdgcn_readlane(own.x, (int)run32);
+        parts = (uint32_t)__builtin_amdgcn_readlane(own.y, (int)run32);
+        tile = v % cut.tiles, part = v / cut.tiles;
+        if (part >= parts) return;  // behind the last run's
+        unit_of = unit;
+    } else if (cut.whole == cut.tiles) {
         // blocks b, b + 8, .. run on one XCD: it takes neighbouring units, those of a run's part, which read the same entries
         const uint32_t share = (units + 7) / 8, unit = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
         if ((blockIdx.x >> 3) >= share || unit >= units) return;
@@ -198,7 +261,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
             tile = cut.whole + v % of_run % shorter, part = v % of_run / shorter;
         }
     }
-    const uint32_t parts = cut.parts_of(tile);
+    if constexpr (ENTRIES != kShared) parts = cut.parts_of(tile);
     const int64_t run = run32;
     const int r0 = (int)tile * kRows, left = a.group * a.heads - r0;  // rows of the run from r0 on
     const int64_t t0 = run * a.group;                                 // the run's first query
@@ -667,7 +730,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
                 const v4f y = *reinterpret_cast<const v4f*>(row + (((2 * lane + 1) ^ (hl & 31)) << 2));
                 const int64_t pair = pair0 + hl;
                 if (!finish) {
-                    const int64_t at = pair * cut.slots() + part;
+                    const int64_t at = ENTRIES == kShared ? (int64_t)unit_of * kRows + hl : pair * cut.slots() + part;
                     *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane) = x;
                     *reinterpret_cast<v4f*>(a.part_o + at * kD + 8 * lane + 4) = y;
                     if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = float2{R, L};
@@ -696,10 +759,17 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, cons
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, own = w / G, take = w % G;
     const int64_t all = (int64_t)a.nq * a.heads, at_row = (int64_t)blockIdx.x * kRows + own;
     const bool live = at_row < all;
-    const int64_t pair = live ? at_row : all - 1, slots = cut.slots();
-    const int parts = (int)cut.parts_of((uint32_t)(pair % ((int64_t)a.group * a.heads)) / (16 * cut.nh));
+    const int64_t pair = live ? at_row : all - 1, of_run = (int64_t)a.group * a.heads;
+    const int rows = 16 * cut.nh, in_run = (int)(pair % of_run), tile = in_run / rows;
+    int parts = (int)cut.parts_of(tile);
+    int64_t slot = pair * cut.slots(), next = 1;  // the row's first part, and the next one from it
+    if (cut.shared) {
+        const int2 own = a.shares[pair / of_run];
+        parts = own.y;
+        slot = (int64_t)(own.x + tile) * rows + in_run % rows, next = (int64_t)cut.tiles * rows;
+    }
     float2 ml{kNone, 0.0f};
-    if (lane < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (pair * slots + lane));
+    if (lane < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (slot + lane * next));
     uint4 u{};
     float l2 = 0.0f;
     if (take == 0 && a.other) {
@@ -716,13 +786,13 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, cons
     float L = f * ml.y;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
-    const float* po = a.part_o + pair * slots * kD + 8 * lane;
+    const float* po = a.part_o + slot * kD + 8 * lane;
     v4f x{}, y{};
 #pragma unroll 4
     for (int i = take; i < parts; i += G) {
         const float fi = __shfl(f, i);
-        x += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[0];
-        y += fi * reinterpret_cast<const v4f*>(po + (int64_t)i * kD)[1];
+        x += fi * reinterpret_cast<const v4f*>(po + i * next * kD)[0];
+        y += fi * reinterpret_cast<const v4f*>(po + i * next * kD)[1];
     }
     if constexpr (G > 1) {
         *reinterpret_cast<v4f*>(s_o[w] + 8 * lane) = x;
@@ -1315,7 +1385,7 @@ constexpr struct {
 } kLocalTiles[] = {{4, 256, 1.8f, 24.0f, 1.8f, 24.0f}, {2, 256, 1.3f, 13.0f, 1.3f, 13.0f}, {1, 512, 2.5f, 9.0f, 1.9f, 7.3f}};
 
 LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entries, int64_t most, int most_queries, bool one) {
-    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), (uint32_t)up(group * heads, 16), 0, 0};
+    LocalCut best{1, 1, (uint32_t)up(group * heads, 16), (uint32_t)up(group * heads, 16), 0, 0, false};
     float least = 0.0f;
     const auto consider = [&](float time, const LocalCut& cut) {
         if (least == 0.0f || time < least) least = time, best = cut;
@@ -1326,7 +1396,7 @@ LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entr
         const int64_t tiles = up(group * heads, rows), steps = std::max<int64_t>(up(entries, kTile), 1);
         // the first `whole` tiles of a run in `parts` parts, the others in one more
         const auto in_parts = [&](int64_t parts, int64_t whole) {
-            const LocalCut cut{t.nh, (uint32_t)parts, (uint32_t)tiles, (uint32_t)whole, 0, 0};
+            const LocalCut cut{t.nh, (uint32_t)parts, (uint32_t)tiles, (uint32_t)whole, 0, 0, false};
             if (parts < 1 || cut.slots() > kMostParts || (cut.slots() > 1 && (cut.slots() > most || cut.slots() > steps))) return;
             const int64_t n1 = runs * whole * parts, n2 = runs * (tiles - whole) * (parts + 1);
             const bool alone = n1 + n2 <= 256;
@@ -1347,13 +1417,13 @@ LocalCut best_local_cut(int64_t runs, int64_t group, int64_t heads, int64_t entr
     for (int queries = 1; queries <= most_queries; ++queries) {
         const int64_t tiles = up(queries * heads, 16), last = tiles % 8;
         const float rows = 14.5f * (float)(tiles / 8) + (last == 0 ? 0.0f : last <= 4 ? 9.0f : 14.5f);
-        consider((float)up(runs * up(group, queries), 256) * (17.0f + rows), LocalCut{0, 1, 0, 0, queries, 0});
+        consider((float)up(runs * up(group, queries), 256) * (17.0f + rows), LocalCut{0, 1, 0, 0, queries, 0, false});
     }
     const int64_t all = up(heads, 16);
     for (int tiles = 1; one && tiles <= all; ++tiles) {
         const int64_t blocks = up(all, tiles);
         consider((float)up(runs * group * blocks, 256) * (3.6f + 3.5f * (float)tiles + 2.0f / (float)blocks),
-                 LocalCut{0, 1, 0, 0, 0, tiles});
+                 LocalCut{0, 1, 0, 0, 0, tiles, false});
     }
     return best;
 }
@@ -1397,25 +1467,40 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
                            per_run, units);
         return hipGetLastError();
     }
-    const uint32_t slots = cut.slots(), units = (uint32_t)runs * cut.of_run();
+    uint32_t slots = cut.slots(), units = (uint32_t)runs * cut.of_run();
     if (slots > 1) {
         a.part_o = (float*)ws;
         a.part_ml = a.part_o + (size_t)slots * rows * kD;
     }
+    // As many blocks for all runs together, in whole rounds: where blocks have eight steps or more (16 of 16 rows; 8 runs of 3 queries of 64
+    // heads over up to 65537 entries: of lengths alike 241 -> 225 us, spread evenly 179 -> 113, one long and seven short
+    // 169 -> 60; 8 runs of one query over 4096, two steps a block: 22 -> 26).
+    const int64_t places = cut.nh == 1 ? 512 : 256, blocks = up(units, places) * places;
+    if (slots > 1 && a.window == 0 && runs > 1 && runs <= kShares && a.group <= kShareGroup &&
+        runs * cut.tiles * up(entries, kTile) >= (cut.nh == 1 ? 16 : 8) * blocks &&
+        kShares * sizeof(int2) + part_bytes(blocks * 16 * cut.nh) <= ws_bytes) {
+        cut.shared = true;
+        units = (uint32_t)blocks;
+        a.shares = (int2*)ws;
+        a.part_o = (float*)(a.shares + kShares);
+        a.part_ml = a.part_o + (size_t)blocks * 16 * cut.nh * kD;
+    }
     const auto start = [&](auto nh) {
         constexpr int kNh = decltype(nh)::value;
         const dim3 grid((units + 7) / 8 * 8);
-        if (a.window > 0) {
+        const auto go = [&](auto entries) {
+            constexpr Entries kEntries = decltype(entries)::value;
             if (a.places.pages)
-                hipLaunchKernelGGL((attend_local_kernel<kNh, true, true>), grid, dim3(256), 0, stream, a, cut, units);
+                hipLaunchKernelGGL((attend_local_kernel<kNh, true, kEntries>), grid, dim3(256), 0, stream, a, cut, units);
             else
-                hipLaunchKernelGGL((attend_local_kernel<kNh, false, true>), grid, dim3(256), 0, stream, a, cut, units);
-        } else {
-            if (a.places.pages)
-                hipLaunchKernelGGL((attend_local_kernel<kNh, true, false>), grid, dim3(256), 0, stream, a, cut, units);
-            else
-                hipLaunchKernelGGL((attend_local_kernel<kNh, false, false>), grid, dim3(256), 0, stream, a, cut, units);
-        }
+                hipLaunchKernelGGL((attend_local_kernel<kNh, false, kEntries>), grid, dim3(256), 0, stream, a, cut, units);
+        };
+        if (a.window > 0)
+            go(std::integral_constant<Entries, kWindow>{});
+        else if (cut.shared)
+            go(std::integral_constant<Entries, kShared>{});
+        else
+            go(std::integral_constant<Entries, kAll>{});
     };
     if (cut.nh == 1)
         start(std::integral_constant<int, 1>{});
@@ -1425,7 +1510,7 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
         start(std::integral_constant<int, 4>{});
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || slots == 1) return err;
-    if (slots > 4)
+    if (slots > 4 || cut.shared)
         hipLaunchKernelGGL(local_join_kernel<4>, dim3((unsigned)rows), dim3(256), 0, stream, a, cut);
     else
         hipLaunchKernelGGL(local_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, cut);

@@ -155,6 +155,7 @@ struct LocalArgs {
     float* lse;             // or null
     float* part_o;          // set by the launch
     float* part_ml;
+    int2* shares;
 };
 size_t local_workspace_bytes(int32_t nq, int32_t heads, int64_t entries);
 hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream_t stream);
