@@ -42,6 +42,13 @@ __device__ __forceinline__ double xor_lane(double v, int li) {
     const uint32_t lo = xor_lane32<M>((uint32_t)b, li), hi = xor_lane32<M>((uint32_t)(b >> 32), li);
     return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
+// the value of lane li ^ 7 (row_half_mirror)
+__device__ __forceinline__ double mirror8(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = dpp32<0x141>((uint32_t)b), hi = dpp32<0x141>((uint32_t)(b >> 32));
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ float mirror8f(float v) { return __uint_as_float(dpp32<0x141>(__float_as_uint(v))); }
 template <int M>
 __device__ __forceinline__ float xor_lanef(float v, int li) {
     return __uint_as_float(xor_lane32<M>(__float_as_uint(v), li));

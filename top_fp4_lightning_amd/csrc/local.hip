@@ -5,11 +5,19 @@
 //   s_p = scale * q . kv_p,  l = log sum e^{s_p},  o = sum e^{s_p - l} kv_p
 //   with another part (o', l'):  L = log(e^l + e^{l'}),  out = e^{l - L} o + e^{l' - L} o'
 //
-// A block of four wavefronts takes 16 or 32 rows, a row being one head of one query: rows of consecutive queries of a
-// sequence share the cache rows they see, so that few heads fill a block too; which entries a row sees is masked where
-// the block's queries differ. 64 entries a step: wavefront w reads those 16w .. 16w + 15 straight into registers, widens
-// them to fp16, multiplies them with the block's rows and leaves them in LDS; after a barrier it multiplies values
-// 128w .. 128w + 127 of all 64 entries with the probabilities. Two blocks on a compute unit cover each other's waits.
+// Three kernels. Long ranges, and whatever the others do not take: a block of four wavefronts takes 16, 32 or 64 rows, a row
+// being one head of one query; rows of consecutive queries of a sequence share the cache rows they see, so that few heads
+// fill a block too, and which entries a row sees is masked where the block's queries differ. 64 entries a step: wavefront w
+// reads those 16w .. 16w + 15 straight into registers, widens them to fp16, multiplies them with the block's rows and leaves
+// them in LDS; after a barrier it multiplies values 128w .. 128w + 127 of all 64 entries with the probabilities. Two blocks of
+// 16 rows on a compute unit cover each other's waits; larger ones have it to themselves. Windows of queries that follow each
+// other, and single queries of at most 128 entries, have kernels of their own below. A run's entries are split where its rows
+// do not fill the card, and the parts joined by another launch.
+//
+// 64 heads: 514 queries over 16384 entries in pages 1.03 to 1.07 ms (0.9 PFLOP/s of the 1.36 that a large product reaches:
+// one wavefront per SIMD, whose issue and waits leave the matrix units busy half of the time); 24 queries over about 57400
+// 218 us (0.83 PFLOP/s: 84 steps of 2.2 us a block, and 33 MB of parts, written and read); 4096 over windows of 128, joined,
+// 184 us (805 MB at 4.4 TB/s, nine tenths of a copy's rate).
 //
 // Arithmetic. A stored value is an fp16 number; queries are scaled by a power of two per row and exact down to 2^-28 of
 // the row's largest; products and sums are fp32. Probabilities enter the second product in 11 bits, against a reference
@@ -821,7 +829,9 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, cons
 // widened into LDS once, and then its wavefronts take 16 rows at a time, each by itself (no barrier): the products with all
 // entries, an exact softmax, the second product with the probabilities where the first left them, half of the values at a
 // time, and the result. The order in which a product adds up its entries is free, so the probabilities of two tiles of 16
-// entries are the second product's operand as they lie, and the values' transposed reads go by that order.
+// entries are the second product's operand as they lie, and the values' transposed reads go by that order. 4096 queries of 64
+// heads over 128 entries, joined and turned: 184 us (573 by the kernel above, which widens every query's entries again);
+// without the other part's 268 MB and the turn it is bound by vector instructions.
 constexpr int kWinTiles = 9;                   // of 16 entries
 constexpr int kWinKeys = 16 * kWinTiles;       // 144 rows of 1 KB
 constexpr int kWinWaves = 8;

@@ -453,7 +453,8 @@ class LayerAttention:
         """New rows of a step (not normalised, not turned): main and local [tokens, 512], key [tokens, 128], each or
         None, of sequences seq [tokens] (int32) at entries at [tokens] (int64), turned by pos [tokens] (default: at).
         Entries of one call's main rows and keys are those of a cache compressed along the sequence where pos is given;
-        local rows are one a position and go by pos then. Tokens at entries below 0 are left out."""
+        local rows are one a position and go by pos then, of each sequence at most `ring` a call (the last of a prefill).
+        Tokens at entries below 0 are left out."""
         core = self.core
         norm = dict(gamma=self.gamma, eps=self.eps)
         turn = dict(pos=pos, freq=core.freq, layout=core.layout, mscale=core.mscale)
