@@ -123,7 +123,7 @@ __device__ __forceinline__ void add_other(const uint4& u, float weight, float (&
 // (cos, sin) of a pair, times the factor
 __device__ __forceinline__ float2 angle_of(const LocalArgs& a, int64_t t, int pair) {
     float s, c;
-    sincospif(2.0f * (float)turns_of(a.turn.pos[t], a.turn.freq[pair]), &s, &c);
+    sincos_turns((float)turns_of(a.turn.pos[t], a.turn.freq[pair]), s, c);
     const float m = (float)a.turn.mscale;
     return float2{c * m, (a.turn.inverse ? -s : s) * m};
 }

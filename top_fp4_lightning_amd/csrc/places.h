@@ -68,4 +68,19 @@ __device__ __forceinline__ void sincos_turns(double t, double& s, double& c) {
     if ((n + 1) & 2) c = -c;
 }
 
+// The same in fp32, to 2^-23: the series to the 9th and 10th power (the next terms are below 2^-26)
+__device__ __forceinline__ void sincos_turns(float t, float& s, float& c) {
+    const float k = rintf(4.0f * t), x = fmaf(k, -0.25f, t) * 6.283185307f, z = x * x;
+    float p = fmaf(1.0f / 362880.0f, z, -1.0f / 5040.0f), q = fmaf(-1.0f / 3628800.0f, z, 1.0f / 40320.0f);
+    p = fmaf(p, z, 1.0f / 120.0f), q = fmaf(q, z, -1.0f / 720.0f);
+    p = fmaf(p, z, -1.0f / 6.0f), q = fmaf(q, z, 1.0f / 24.0f);
+    q = fmaf(q, z, -0.5f);
+    const float sx = fmaf(p * z, x, x), cx = fmaf(q, z, 1.0f);
+    const int n = (int)k;  // quarter turns
+    s = n & 1 ? cx : sx;
+    c = n & 1 ? sx : cx;
+    s = __uint_as_float(__float_as_uint(s) ^ ((uint32_t)n << 30 & 0x80000000u));
+    c = __uint_as_float(__float_as_uint(c) ^ ((uint32_t)(n + 1) << 30 & 0x80000000u));
+}
+
 }  // namespace fp4idx

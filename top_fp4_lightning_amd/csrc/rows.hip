@@ -367,7 +367,7 @@ __global__ __launch_bounds__(256) void read_rows_kernel(const RowsArgs a) {
     constexpr bool kKey = FMT == IDX_ROWS_KEY;
     constexpr int kLanes = F::kDim / 8, kSide = 64 / kLanes;  // of a row; rows side by side in a wavefront
     constexpr int kGroupLanes = F::kGroup / 8, kScales = F::kDim / F::kGroup;
-    __shared__ float2 s_cs[kKey ? 1 : 4][kReadAngles];
+    __shared__ __align__(16) float2 s_cs[kKey ? 1 : 4][kReadAngles];
     __shared__ __align__(16) float s_y[kKey ? 1 : 4][F::kDim];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane % kLanes;
     const int64_t t0 = ((int64_t)blockIdx.x * 4 + w) * (kSide * kReads) + lane / kLanes;
@@ -398,15 +398,18 @@ __global__ __launch_bounds__(256) void read_rows_kernel(const RowsArgs a) {
     const float m = (float)a.turn.mscale;
     const auto angle = [&](int64_t t, int64_t entry, int p) {
         float s, c;
-        sincospif(2.0f * (float)turns_of(a.turn.pos ? a.turn.pos[t] : entry, a.turn.freq[p]), &s, &c);
+        sincos_turns((float)turns_of(a.turn.pos ? a.turn.pos[t] : entry, a.turn.freq[p]), s, c);
         return float2{c * m, (a.turn.inverse ? -s : s) * m};
     };
     // angles of all the rows at once where they are few
     const bool all = kReads * pairs <= kReadAngles;
     if (pairs && all) {
-        for (int i = lane; i < kReads * pairs; i += 64) {
-            const int64_t t = min(t0 + i / pairs, a.tokens - 1);
-            s_cs[kKey ? 0 : w][i] = angle(t, a.at[t], i % pairs);
+        // i / pairs as a product: i below 256, the factor above 2^16 / pairs by at most 1
+        const uint32_t by = (1u << 16) / (uint32_t)pairs + 1;
+        for (uint32_t i = lane; i < (uint32_t)(kReads * pairs); i += 64) {
+            const uint32_t k = i * by >> 16;
+            const int64_t t = min(t0 + k, a.tokens - 1);
+            s_cs[kKey ? 0 : w][i] = angle(t, a.at[t], (int)(i - k * pairs));
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -457,7 +460,17 @@ __global__ __launch_bounds__(256) void read_rows_kernel(const RowsArgs a) {
                 }
                 const int j0 = 8 * li - offset;
                 if (j0 > -8 && j0 < rot) {
-                    if (!apart) {
+                    if (!apart && !((offset | rot) & 7)) {  // whole lanes
+                        const float4 z[2] = {reinterpret_cast<const float4*>(cs)[j0 >> 2],
+                                             reinterpret_cast<const float4*>(cs)[(j0 >> 2) + 1]};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float c = i & 1 ? z[i >> 1].z : z[i >> 1].x, d = i & 1 ? z[i >> 1].w : z[i >> 1].y;
+                            const float x0 = y[2 * i], x1 = y[2 * i + 1];
+                            y[2 * i] = x0 * c - x1 * d;
+                            y[2 * i + 1] = x1 * c + x0 * d;
+                        }
+                    } else if (!apart) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int j = j0 + 2 * i;
@@ -536,7 +549,7 @@ hipError_t launch_write_rows(const RowsArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_read_rows(const RowsArgs& a, hipStream_t stream) {
-    // Four rows a lane where the wavefronts still fill the card twice: 32768 rows of the main KV, turned, 25 -> 17 us; 64 rows
+    // Four rows a lane where the wavefronts still fill the card twice: 32768 rows of the main KV, turned, 23 -> 15 us; 64 rows
     // 3.4 us with one and 4.8 with four.
     const int64_t lanes = a.tokens * (a.format == IDX_ROWS_KEY ? kDim : 512) / 8;
     if (lanes >= (int64_t)4 * 64 * 4096) {
