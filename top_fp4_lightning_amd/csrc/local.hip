@@ -16,8 +16,8 @@
 //
 // 64 heads: 514 queries over 16384 entries in pages 1.03 to 1.07 ms (0.9 PFLOP/s of the 1.36 that a large product reaches:
 // one wavefront per SIMD, whose issue and waits leave the matrix units busy half of the time); 24 queries over about 57400
-// 218 us (0.83 PFLOP/s: 84 steps of 2.2 us a block, and 33 MB of parts, written and read); 4096 over windows of 128, joined,
-// 184 us (805 MB at 4.4 TB/s, nine tenths of a copy's rate).
+// 218 us (0.83 PFLOP/s: 84 steps of about 2 us a block, and 33 MB of parts, written and read); 4096 over windows of 128,
+// joined, 183 us (805 MB at 4.4 TB/s, nine tenths of a copy's rate).
 //
 // Arithmetic. A stored value is an fp16 number; queries are scaled by a power of two per row and exact down to 2^-28 of
 // the row's largest; products and sums are fp32. Probabilities enter the second product in 11 bits, against a reference
@@ -830,8 +830,8 @@ __global__ __launch_bounds__(256) void local_join_kernel(const LocalArgs a, cons
 // entries, an exact softmax, the second product with the probabilities where the first left them, half of the values at a
 // time, and the result. The order in which a product adds up its entries is free, so the probabilities of two tiles of 16
 // entries are the second product's operand as they lie, and the values' transposed reads go by that order. 4096 queries of 64
-// heads over 128 entries, joined and turned: 184 us (573 by the kernel above, which widens every query's entries again);
-// without the other part's 268 MB and the turn it is bound by vector instructions.
+// heads over 128 entries, joined and turned: 183 us (573 by the kernel above, which widens every query's entries again),
+// 805 MB at 4.4 TB/s.
 constexpr int kWinTiles = 9;                   // of 16 entries
 constexpr int kWinKeys = 16 * kWinTiles;       // 144 rows of 1 KB
 constexpr int kWinWaves = 8;
@@ -1482,9 +1482,9 @@ hipError_t launch_attend_local(LocalArgs a, void* ws, size_t ws_bytes, hipStream
         a.part_o = (float*)ws;
         a.part_ml = a.part_o + (size_t)slots * rows * kD;
     }
-    // As many blocks for all runs together, in whole rounds: where blocks have eight steps or more (16 of 16 rows; 8 runs of 3 queries of 64
-    // heads over up to 65537 entries: of lengths alike 241 -> 225 us, spread evenly 179 -> 113, one long and seven short
-    // 169 -> 60; 8 runs of one query over 4096, two steps a block: 22 -> 26).
+    // As many blocks for all runs together, in whole rounds: where blocks have eight steps or more (16, of 16 rows). 8 runs of
+    // 3 queries of 64 heads over up to 65537 entries: of lengths alike 241 -> 225 us, spread evenly 179 -> 113, one long and
+    // seven short 169 -> 60; 8 runs of one query over 4096, two steps a block: 22 -> 26.
     const int64_t places = cut.nh == 1 ? 512 : 256, blocks = up(units, places) * places;
     if (slots > 1 && a.window == 0 && runs > 1 && runs <= kShares && a.group <= kShareGroup &&
         runs * cut.tiles * up(entries, kTile) >= (cut.nh == 1 ? 16 : 8) * blocks &&

@@ -31,8 +31,8 @@ rotates and quantises new rows into them, and attends over the selected position
 with the values turned back to the query's frame. LayerAttention is the whole of a layer's attention ("DeepSeek-V4.1
 model structure (3)", sections "Reindex layers score a million entries per token", whose count of core attention has 512
 selected and 128 local entries, and "removing the global scale still leaves enough range"): the selection joined with
-the last positions in an FP8 ring, and the writing of a step's rows into all of the layer's caches. IndexerDistill trains a layer's indexer towards it, on the
-score rows of the training form.
+the last positions in an FP8 ring, and the writing of a step's rows into all of the layer's caches. IndexerDistill trains
+a layer's indexer towards the core attention, on the score rows of the training form.
 
 All buffers are allocated once in the plan objects, so a step allocates nothing and can be
 captured in a HIP graph. (CoreAttention.write fills its cache between steps: it allocates and is not captured;
@@ -45,8 +45,8 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (BLOCK, DIM, IDX_OP_ATTEND, IDX_OP_ATTEND_LOCAL, IDX_OP_BUILD_POOL, IDX_OP_DISTILL, IDX_OP_TOPK, MKV_DIM, Recorded, idx_attend,
-               idx_attend_local, idx_attend_weights, idx_build_pool, idx_distill, idx_distill_bwd, idx_mask_pool, idx_quantize_kv,
+from . import (BLOCK, DIM, IDX_OP_ATTEND, IDX_OP_ATTEND_LOCAL, IDX_OP_BUILD_POOL, IDX_OP_DISTILL, IDX_OP_TOPK, MKV_DIM,
+               Recorded, idx_attend, idx_attend_local, idx_attend_weights, idx_build_pool, idx_distill, idx_distill_bwd, idx_mask_pool, idx_quantize_kv,
                idx_quantize_q, idx_rope, idx_score_full, idx_score_pool_gather, idx_top_blocks, idx_topk, idx_topk_pool,
                idx_write_rows, record, rope_freqs, workspace)
 
