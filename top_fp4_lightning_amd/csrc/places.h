@@ -48,12 +48,11 @@ __device__ __forceinline__ double turns_of(int64_t pos, double freq) {
     return fma(p, per, -rint(p * per)) + p * low;
 }
 
-// sin and cos of t turns, |t| at most about 1/2, to 2^-50: t's quarter turns taken off, then the Taylor series to the 17th
-// and 16th power of an angle of at most pi / 4 (the next terms are below 2^-56)
+// sin and cos of t turns, |t| at most about 1/2, to 2^-49: t's quarter turns taken off, then the Taylor series to the 15th
+// and 14th power of an angle of at most pi / 4 (the next terms are below 2^-53 and 2^-49)
 __device__ __forceinline__ void sincos_turns(double t, double& s, double& c) {
     const double k = rint(4.0 * t), x = fma(k, -0.25, t) * 6.283185307179586477, z = x * x;
-    double p = 1.0 / 355687428096000.0, q = 1.0 / 20922789888000.0;  // 1 / 17!, 1 / 16!
-    p = fma(p, z, -1.0 / 1307674368000.0), q = fma(q, z, -1.0 / 87178291200.0);
+    double p = -1.0 / 1307674368000.0, q = -1.0 / 87178291200.0;  // 1 / 15!, 1 / 14!
     p = fma(p, z, 1.0 / 6227020800.0), q = fma(q, z, 1.0 / 479001600.0);
     p = fma(p, z, -1.0 / 39916800.0), q = fma(q, z, -1.0 / 3628800.0);
     p = fma(p, z, 1.0 / 362880.0), q = fma(q, z, 1.0 / 40320.0);

@@ -202,15 +202,29 @@ __global__ __launch_bounds__(256) void write_rows_kernel(const RowsArgs a) {
             sum += xor_lane<8>(sum, li);
             sum += xor_lane<16>(sum, li);
         }
-        by = 1.0 / sqrt(sum / F::kDim + a.eps);
+        // 1 / sqrt by the instruction's approximation (2^-23 or better) and two of Newton's steps
+        const double mean = fmax(fma(sum, 1.0 / F::kDim, a.eps), 0x1p-1020);
+        by = __builtin_amdgcn_rsq(mean);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) by = fma(by * 0.5, fma(-mean * by, by, 1.0), by);
     }
     const auto normal = [&](int i) {
         return (double)f[i] * by * (double)gamma[i];
     };
+    double y[kKey ? 16 : 1];
+    if constexpr (kKey) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = NORM ? normal(i) : (double)f[i];
+    }
     if (pairs) {
         if (first < last) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s_part[r][(16 + kPad) * li + i] = (Part)f[i];
+            for (int i = 0; i < 16; ++i) {
+                if constexpr (kKey)
+                    s_part[r][(16 + kPad) * li + i] = y[i];
+                else
+                    s_part[r][(16 + kPad) * li + i] = f[i];
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (a row is one wavefront's)
         __builtin_amdgcn_wave_barrier();
@@ -218,12 +232,12 @@ __global__ __launch_bounds__(256) void write_rows_kernel(const RowsArgs a) {
         const auto turned = [&](int p, double per) {
             double s, c;
             sincos_turns(turns_of(pos, per), s, c);
-            s *= a.turn.mscale, c *= a.turn.mscale;
+            if (a.turn.mscale != 1.0) s *= a.turn.mscale, c *= a.turn.mscale;
             const int i0 = offset + (a.turn.half ? p : 2 * p), i1 = i0 + (a.turn.half ? pairs : 1);
             Part& at0 = s_part[r][part(i0)];
             Part& at1 = s_part[r][part(i1)];
             double x0 = at0, x1 = at1;
-            if (NORM) {
+            if (NORM && !kKey) {
                 x0 *= by, x1 *= by;
                 if (a.gamma) x0 *= (double)a.gamma[i0], x1 *= (double)a.gamma[i1];
             }
@@ -246,9 +260,6 @@ __global__ __launch_bounds__(256) void write_rows_kernel(const RowsArgs a) {
 
     int place = li;  // which sixteen of the row this lane holds in the end
     if constexpr (kKey) {
-        double y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = NORM ? normal(i) : (double)f[i];
         if (first == 0 && last == 16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = s_part[r][(16 + kPad) * li + i];
