@@ -10,10 +10,10 @@
 //
 // Reading: the stored values (a code times a scale is exact in fp32 and bf16), turned in fp32, rounded once.
 //
-// Under the tracer, writing takes 18 us for 32770 fp32 rows of the main KV, turned (76 MB at 4.2 TB/s), 16 for 16384 bf16 rows
-// of local positions, normalised and turned, 21 for 65537 keys: vector instructions fill 73, 70 and 88% of the time (24, 35 and
-// 63 a value; of a key's, 25 are its pairs' sines and cosines). A fifth block on a compute unit changes nothing. Reading them
-// takes 13, 8 and 7 us. One row 3.4 and 2.0 us: launch, three loads one behind the other.
+// Under the tracer, writing takes 18 us for 32770 fp32 rows of the main KV, turned (76 MB at 4.3 TB/s), 13 for 16384 bf16 rows
+// of local positions, normalised and turned, 18 for 65537 keys: vector instructions fill two thirds to nine tenths of the time,
+// 24, 32 and 58 a value, a third of a key's for its pairs' sines and cosines. A fifth block on a compute unit changes nothing.
+// Reading them takes 12, 7 and 6 us. One row 3.2 and 2.2 us: launch, three loads one behind the other.
 #include "../../include/fp4idx.h"
 #include <type_traits>
 
@@ -560,17 +560,17 @@ hipError_t launch_write_rows(const RowsArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_read_rows(const RowsArgs& a, hipStream_t stream) {
-    // Four rows a lane where the wavefronts still fill the card twice: 32768 rows of the main KV, turned, 23 -> 15 us; 64 rows
-    // 3.4 us with one and 4.8 with four.
+    // Two rows a lane where the wavefronts fill the card four times: 32768 rows of the main KV, turned, 13.8 -> 11.9 us (four
+    // rows 13.3, eight 14), 65536 23.5 -> 19.7; 8192 rows of local positions in fp32 7.0 us with one and 7.4 with two.
     const int64_t lanes = a.tokens * (a.format == IDX_ROWS_KEY ? kDim : 512) / 8;
     if (lanes >= (int64_t)4 * 64 * 4096) {
-        const dim3 grid((unsigned)((lanes + 1023) / 1024));
+        const dim3 grid((unsigned)((lanes + 511) / 512));
         if (a.format == IDX_ROWS_KEY)
-            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_KEY, 4>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_KEY, 2>), grid, dim3(256), 0, stream, a);
         else if (a.format == IDX_ROWS_MAIN)
-            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_MAIN, 4>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_MAIN, 2>), grid, dim3(256), 0, stream, a);
         else
-            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_LOCAL, 4>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((read_rows_kernel<IDX_ROWS_LOCAL, 2>), grid, dim3(256), 0, stream, a);
     } else {
         const dim3 grid((unsigned)((lanes + 255) / 256));
         if (a.format == IDX_ROWS_KEY)
