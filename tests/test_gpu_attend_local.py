@@ -444,3 +444,36 @@ def test_two_graphs_with_one_workspace(fx):
             call(s, out, lse)
             torch.cuda.synchronize()
             assert torch.equal(out, s[1]) and torch.equal(lse, s[2])
+
+
+def test_a_graph_whose_lengths_change(fx):
+    """blocks shared out anew at each replay, other calls on the same workspace between"""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    n, runs, group, heads = 16384, 16, 2, 64
+    codes = torch.randint(0, 127, (n, 512), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.full((n, 16), 119, dtype=torch.uint8, device="cuda")
+    q = torch.randn(runs * group, heads, 512, device="cuda", generator=g).bfloat16()
+    n_vis = torch.full((runs * group,), n, dtype=torch.int32, device="cuda")
+    base = torch.zeros(runs, dtype=torch.int64, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(runs * group, heads, device="cuda")
+    ws = fx.workspace(fx.IDX_OP_ATTEND_LOCAL, runs * group, n, heads)
+
+    def call(out, lse, ws):
+        fx.idx_attend_local(q, codes, scales, n_vis, n, 0.02, out, ws, lse=lse, group=group, kv_base=base)
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call(out, lse, ws)
+    want, want_lse, own = torch.empty_like(q), torch.empty_like(lse), torch.full_like(ws, 255)
+    one = torch.empty_like(q[:2]), torch.empty(2, heads, device="cuda")
+    for _ in range(5):
+        last = torch.randint(-1, n + 1, (runs, 1), device="cuda", generator=g)
+        n_vis.copy_((last + torch.arange(group, device="cuda")).reshape(-1))
+        q.normal_(generator=g)
+        graph.replay()
+        fx.idx_attend_local(q[:2], codes, scales, n_vis[:2], n, 0.02, one[0], ws, lse=one[1], group=2, kv_base=base[:1])
+        call(want, want_lse, own)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        own.fill_(255)
