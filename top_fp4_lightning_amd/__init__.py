@@ -521,16 +521,24 @@ ROW_FORMATS = {"main": (0, MKV_DIM, MKV_DIM // 2, MKV_DIM // 16), "local": (1, M
                "key": (2, DIM, DIM // 2, DIM // 32)}
 
 
+# (The helpers below ask for a tensor's properties in place, a few tenths of a microsecond less for each than through _arg,
+# and leave it to _arg to say what is wrong: the calls of a decode step cost the host more than the card.)
+_U8, _I32, _I64, _F32, _F64, _BF16 = torch.uint8, torch.int32, torch.int64, torch.float32, torch.float64, torch.bfloat16
+
+
 def _row_format(format, codes, scales) -> tuple:
     """(number, values of a row, address of codes, of scales, rows) of a cache in a format"""
-    if format not in ROW_FORMATS:
+    found = ROW_FORMATS.get(format)
+    if found is None:
         raise ValueError(f"format must be one of {sorted(ROW_FORMATS)}, got {format!r}")
-    number, dim, width, groups = ROW_FORMATS[format]
-    codes_ptr, scales_ptr = _arg(codes, torch.uint8, None, "codes"), _arg(scales, torch.uint8, None, "scales")
-    rows, rest = divmod(codes.numel(), width)
-    if rest or scales.numel() != rows * groups:
+    if codes.dtype is not _U8 or scales.dtype is not _U8 or not codes.is_contiguous() or not scales.is_contiguous():
+        _arg(codes, _U8, None, "codes"), _arg(scales, _U8, None, "scales")
+    number, dim, width, groups = found
+    size = codes.numel()
+    rows = size // width
+    if size != rows * width or scales.numel() != rows * groups:
         raise ValueError(f"codes and scales must hold {width} and {groups} bytes for each cache row")
-    return number, dim, codes_ptr, scales_ptr, rows
+    return number, dim, codes.data_ptr(), scales.data_ptr(), rows
 
 
 def _places(n, max_n, ring, kv_base, pages, page_size, seq) -> tuple:
@@ -538,17 +546,21 @@ def _places(n, max_n, ring, kv_base, pages, page_size, seq) -> tuple:
     base_ptr = pages_ptr = seq_ptr = None
     stride = nseq = 0
     if kv_base is not None:
-        base_ptr = _arg(kv_base, torch.int64, (n,), "kv_base")
+        if kv_base.dtype is not _I64 or kv_base.shape != (n,) or not kv_base.is_contiguous():
+            _arg(kv_base, _I64, (n,), "kv_base")
+        base_ptr = kv_base.data_ptr()
     if pages is not None:
         nseq = pages.shape[0]
-        pages_ptr, stride = _rows_arg(pages, torch.int32, nseq, 0, "pages")
+        pages_ptr, stride = _rows_arg(pages, _I32, nseq, 0, "pages")
         most = min(max_n, ring) if ring else max_n
         if pages.shape[1] * page_size < most:
             raise ValueError(f"pages must cover {most} places: {pages.shape[1]} pages of {page_size}")
         if pages_ptr == 0:  # no column: every place lies outside
             raise ValueError("pages must not be empty")
     if seq is not None:
-        seq_ptr = _arg(seq, torch.int32, (n,), "seq")
+        if seq.dtype is not _I32 or seq.shape != (n,) or not seq.is_contiguous():
+            _arg(seq, _I32, (n,), "seq")
+        seq_ptr = seq.data_ptr()
     return base_ptr, pages_ptr, stride, nseq, page_size, seq_ptr
 
 
@@ -556,22 +568,28 @@ def _turn(pos, freq, n, dim, offset, layout) -> tuple:
     """The arguments pos, freq, rot, offset and layout (freq None: no rotation)"""
     if freq is None:
         return None, None, 0, 0, 0
-    if layout not in ROPE_LAYOUTS:
+    number = ROPE_LAYOUTS.get(layout)
+    if number is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    rot = 2 * freq.numel()
-    freq_ptr = _arg(freq, torch.float64, (rot // 2,), "freq")
-    pos_ptr = None if pos is None else _arg(pos, torch.int64, (n,), "pos")
-    return pos_ptr, freq_ptr, rot, dim - rot if offset is None else offset, ROPE_LAYOUTS[layout]
+    pairs = freq.numel()
+    if freq.dtype is not _F64 or freq.dim() != 1 or not freq.is_contiguous():
+        _arg(freq, _F64, (pairs,), "freq")
+    pos_ptr = None
+    if pos is not None:
+        if pos.dtype is not _I64 or pos.shape != (n,) or not pos.is_contiguous():
+            _arg(pos, _I64, (n,), "pos")
+        pos_ptr = pos.data_ptr()
+    return pos_ptr, freq.data_ptr(), 2 * pairs, dim - 2 * pairs if offset is None else offset, number
 
 
 def _value_rows(x, tokens, dim, name) -> tuple:
     """(address, type, row stride) of rows [tokens, dim] of consecutive values"""
     dtype = x.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if dtype is not _BF16 and dtype is not _F32:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
-    if x.dim() != 2 or x.shape[0] != tokens or x.shape[1] != dim or x.stride(1) != 1:
+    if x.shape != (tokens, dim) or x.stride(1) != 1:
         raise ValueError(f"{name} must be [{tokens}, {dim}] with consecutive values, got {tuple(x.shape)}")
-    return x.data_ptr(), 0 if dtype is torch.bfloat16 else 1, x.stride(0) if tokens > 1 else dim
+    return x.data_ptr(), 0 if dtype is _BF16 else 1, x.stride(0) if tokens > 1 else dim
 
 
 def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, pages=None, page_size: int = 0, seq=None,
@@ -582,18 +600,19 @@ def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, 
     at entries at [tokens] (int64) below max_n: rows kv_base [tokens] + entry, or of pages [nseq, ...] of page_size
     (seq [tokens] names the page row); with ring, entry % ring takes the entry's place."""
     number, dim, codes_ptr, scales_ptr, rows = _row_format(format, codes, scales)
-    tokens = at.shape[0]
+    if at.dtype is not _I64 or at.dim() != 1 or not at.is_contiguous():
+        _arg(at, _I64, (at.numel(),), "at")
+    tokens = at.numel()
     x_ptr, dtype, stride = _value_rows(x, tokens, dim, "x")
-    at_ptr = _arg(at, torch.int64, (tokens,), "at")
     where = _places(tokens, max_n, ring, kv_base, pages, page_size, seq)
     turn = _turn(pos, freq, tokens, dim, offset, layout)
     if gamma is not None and eps is None:
         raise ValueError("gamma needs eps")
-    gamma_ptr = None if gamma is None else _arg(gamma, torch.float32, (dim,), "gamma")
+    gamma_ptr = None if gamma is None else _arg(gamma, _F32, (dim,), "gamma")
     signs_ptr = None if signs is None else _arg(signs, torch.int8, (DIM,), "signs")
     _same_gpu(codes, scales, x, at, kv_base, pages, seq, pos, freq, gamma, signs)
     _call(lib.idx_write_rows, number, x_ptr, dtype, tokens, stride, int(eps is not None), gamma_ptr, eps or 0.0, *turn,
-          mscale, signs_ptr, codes_ptr, scales_ptr, rows, *where, at_ptr, max_n, ring, _stream(stream))
+          mscale, signs_ptr, codes_ptr, scales_ptr, rows, *where, at.data_ptr(), max_n, ring, _stream(stream))
     return codes, scales
 
 
@@ -604,8 +623,9 @@ def idx_read_rows(format: str, codes, scales, at, max_n: int, kv_base=None, page
     turned by pos (default: at) as by idx_rope. The other arguments as for idx_write_rows; entries that are not there
     give zeros."""
     number, dim, codes_ptr, scales_ptr, rows = _row_format(format, codes, scales)
-    tokens = at.shape[0]
-    at_ptr = _arg(at, torch.int64, (tokens,), "at")
+    if at.dtype is not _I64 or at.dim() != 1 or not at.is_contiguous():
+        _arg(at, _I64, (at.numel(),), "at")
+    tokens = at.numel()
     where = _places(tokens, max_n, ring, kv_base, pages, page_size, seq)
     turn = _turn(pos, freq, tokens, dim, offset, layout)
     if out is None:
@@ -614,7 +634,7 @@ def idx_read_rows(format: str, codes, scales, at, max_n: int, kv_base=None, page
     if stride < dim:
         raise ValueError("out's rows may not overlap")
     _same_gpu(codes, scales, at, kv_base, pages, seq, pos, freq, out)
-    _call(lib.idx_read_rows, number, codes_ptr, scales_ptr, rows, *where, at_ptr, max_n, ring, tokens, *turn, mscale,
+    _call(lib.idx_read_rows, number, codes_ptr, scales_ptr, rows, *where, at.data_ptr(), max_n, ring, tokens, *turn, mscale,
           int(inverse), out_ptr, number_out, stride, _stream(stream))
     return out
 
@@ -633,17 +653,22 @@ def idx_attend_local(q, codes, scales, n_vis, max_n: int, scale: float, out, ws,
     nq, heads, _ = shape
     if group < 1 or nq % group:
         raise ValueError(f"group={group} must divide nq={nq}")
-    q_ptr = _arg(q, torch.bfloat16, None, "q")
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        _arg(q, _BF16, None, "q")
+    if n_vis.dtype is not _I32 or n_vis.shape != (nq,) or not n_vis.is_contiguous():
+        _arg(n_vis, _I32, (nq,), "n_vis")
+    if out.dtype is not _BF16 or out.shape != shape or not out.is_contiguous():
+        _arg(out, _BF16, shape, "out")
+    if ws.dtype is not _U8 or not ws.is_contiguous():
+        _arg(ws, _U8, None, "ws")
     _, _, codes_ptr, scales_ptr, rows = _row_format("local", codes, scales)
-    nv_ptr = _arg(n_vis, torch.int32, (nq,), "n_vis")
     where = _places(nq // group, max_n, ring, kv_base, pages, page_size, seq)
-    other_ptr = None if other is None else _arg(other, torch.bfloat16, shape, "other")
-    other_lse_ptr = None if other_lse is None else _arg(other_lse, torch.float32, shape[:2], "other_lse")
+    other_ptr = None if other is None else _arg(other, _BF16, shape, "other")
+    other_lse_ptr = None if other_lse is None else _arg(other_lse, _F32, (nq, heads), "other_lse")
     turn = _turn(pos, freq, nq, MKV_DIM, offset, layout)
-    out_ptr = _arg(out, torch.bfloat16, shape, "out")
-    lse_ptr = None if lse is None else _arg(lse, torch.float32, shape[:2], "lse")
-    ws_ptr = _arg(ws, torch.uint8, None, "ws")
+    lse_ptr = None if lse is None else _arg(lse, _F32, (nq, heads), "lse")
     _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, other, other_lse, pos, freq, out, lse, ws)
-    _call(lib.idx_attend_local, q_ptr, nq, heads, group, codes_ptr, scales_ptr, rows, *where, nv_ptr, max_n, window, ring,
-          scale, other_ptr, other_lse_ptr, *turn, mscale, out_ptr, lse_ptr, ws_ptr, ws.numel(), _stream(stream))
+    _call(lib.idx_attend_local, q.data_ptr(), nq, heads, group, codes_ptr, scales_ptr, rows, *where, n_vis.data_ptr(), max_n,
+          window, ring, scale, other_ptr, other_lse_ptr, *turn, mscale, out.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(),
+          _stream(stream))
     return out, lse
