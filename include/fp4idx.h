@@ -635,6 +635,18 @@ idx_status idx_attend_local(const uint16_t* q, int32_t nq, int32_t heads, int32_
                             int32_t rot, int32_t offset, int32_t layout, double mscale, uint16_t* out, float* lse,
                             void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * idx_attend_local_strided: the same, run i's sequence at seq[i * seq_stride] (seq_stride >= 0; not looked at without
+ * seq): of a step's sequences by query, those of its runs' first queries (seq_stride = group), read where they lie.
+ */
+idx_status idx_attend_local_strided(const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
+                                    const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                                    int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq,
+                                    int64_t seq_stride, const int32_t* n_vis, int64_t max_n, int64_t window, int64_t ring,
+                                    float scale, const uint16_t* other, const float* other_lse, const int64_t* pos,
+                                    const double* freq, int32_t rot, int32_t offset, int32_t layout, double mscale,
+                                    uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -56,18 +56,20 @@ lib.idx_read_rows.argtypes = [_i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, 
                               _i32, _f64, _i32, _P, _i32, _i64, _P]
 lib.idx_attend_local.argtypes = [_P, _i32, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _f32,
                                  _P, _P, _P, _P, _i32, _i32, _i32, _f64, _P, _P, _P, _sz, _P]
+lib.idx_attend_local_strided.argtypes = [*lib.idx_attend_local.argtypes[:13], _i64, *lib.idx_attend_local.argtypes[13:]]
 for _f in ("idx_quantize_q", "idx_score_full", "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks",
            "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope",
            "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows",
-           "idx_attend_local"):
+           "idx_attend_local", "idx_attend_local_strided"):
     getattr(lib, _f).restype = _i32
 
 EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quantize_q", "idx_score_full",
            "idx_build_pool", "idx_build_pool_noalloc", "idx_top_blocks", "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv",
            "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope", "idx_attend",
-           "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows", "idx_attend_local")
+           "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows", "idx_attend_local",
+           "idx_attend_local_strided")
 MKV_DIM = 512
 
 
@@ -541,8 +543,8 @@ def _row_format(format, codes, scales) -> tuple:
     return number, dim, codes.data_ptr(), scales.data_ptr(), rows
 
 
-def _places(n, max_n, ring, kv_base, pages, page_size, seq) -> tuple:
-    """The arguments from kv_base to seq; n: how many kv_base and seq name."""
+def _places(n, max_n, ring, kv_base, pages, page_size, seq, strided: bool = False) -> tuple:
+    """The arguments from kv_base to seq; n: how many kv_base and seq name. strided: seq's numbers may lie apart."""
     base_ptr = pages_ptr = seq_ptr = None
     stride = nseq = 0
     if kv_base is not None:
@@ -558,7 +560,7 @@ def _places(n, max_n, ring, kv_base, pages, page_size, seq) -> tuple:
         if pages_ptr == 0:  # no column: every place lies outside
             raise ValueError("pages must not be empty")
     if seq is not None:
-        if seq.dtype is not _I32 or seq.shape != (n,) or not seq.is_contiguous():
+        if seq.dtype is not _I32 or seq.shape != (n,) or not (strided or seq.is_contiguous()):
             _arg(seq, _I32, (n,), "seq")
         seq_ptr = seq.data_ptr()
     return base_ptr, pages_ptr, stride, nseq, page_size, seq_ptr
@@ -646,7 +648,8 @@ def idx_attend_local(q, codes, scales, n_vis, max_n: int, scale: float, out, ws,
     """Attention of q [nq, heads, 512] over the FP8 cache of local positions (IDX_ROWS_LOCAL rows): the last `window`
     visible entries or all of them, joined with `other` (out and lse of the attention over other entries) and, with freq,
     turned back by pos [nq]. Runs of `group` queries are of one sequence; kv_base or seq [nq / group] names its rows, as for
-    idx_write_rows. ws: workspace(IDX_OP_ATTEND_LOCAL, nq, entries, heads), or another call's."""
+    idx_write_rows; seq may be a view of any stride (seq[::group] of the queries' sequences).
+    ws: workspace(IDX_OP_ATTEND_LOCAL, nq, entries, heads), or another call's."""
     shape = q.shape
     if len(shape) != 3 or shape[2] != MKV_DIM:
         raise ValueError(f"q must be [nq, heads, {MKV_DIM}], got {tuple(shape)}")
@@ -662,13 +665,16 @@ def idx_attend_local(q, codes, scales, n_vis, max_n: int, scale: float, out, ws,
     if ws.dtype is not _U8 or not ws.is_contiguous():
         _arg(ws, _U8, None, "ws")
     _, _, codes_ptr, scales_ptr, rows = _row_format("local", codes, scales)
-    where = _places(nq // group, max_n, ring, kv_base, pages, page_size, seq)
+    where = _places(nq // group, max_n, ring, kv_base, pages, page_size, seq, strided=True)
+    fn = lib.idx_attend_local
+    if seq is not None and nq > group and seq.stride(0) != 1:
+        fn, where = lib.idx_attend_local_strided, (*where, seq.stride(0))
     other_ptr = None if other is None else _arg(other, _BF16, shape, "other")
     other_lse_ptr = None if other_lse is None else _arg(other_lse, _F32, (nq, heads), "other_lse")
     turn = _turn(pos, freq, nq, MKV_DIM, offset, layout)
     lse_ptr = None if lse is None else _arg(lse, _F32, (nq, heads), "lse")
     _same_gpu(q, codes, scales, n_vis, kv_base, pages, seq, other, other_lse, pos, freq, out, lse, ws)
-    _call(lib.idx_attend_local, q.data_ptr(), nq, heads, group, codes_ptr, scales_ptr, rows, *where, n_vis.data_ptr(), max_n,
+    _call(fn, q.data_ptr(), nq, heads, group, codes_ptr, scales_ptr, rows, *where, n_vis.data_ptr(), max_n,
           window, ring, scale, other_ptr, other_lse_ptr, *turn, mscale, out.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(),
           _stream(stream))
     return out, lse

@@ -226,6 +226,53 @@ idx_status rows_args(const char* fn, int32_t format, const void* x, int32_t dtyp
 }
 constexpr int32_t row_dim(int32_t format) { return format == IDX_ROWS_KEY ? kDim : 512; }
 
+// idx_attend_local, run i's sequence seq_stride numbers behind the one before
+idx_status attend_local(const char* fn, const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
+                        const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                        int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, int64_t seq_stride,
+                        const int32_t* n_vis, int64_t max_n, int64_t window, int64_t ring, float scale,
+                        const uint16_t* other, const float* other_lse, const int64_t* pos, const double* freq,
+                        int32_t rot, int32_t offset, int32_t layout, double mscale, uint16_t* out, float* lse,
+                        void* ws, size_t ws_bytes, void* stream) {
+    REQUIRE(nq >= 0 && nq <= kMaxQueries, IDX_EUNSUPPORTED, "%s: nq=%d out of [0, 65535]", fn, nq);
+    REQUIRE(heads >= 1 && heads <= kMaxAttendHeads, IDX_EUNSUPPORTED, "%s: heads=%d out of [1, 128]", fn, heads);
+    REQUIRE(group >= 1 && nq % group == 0, IDX_EINVAL, "%s: group=%d must divide nq=%d", fn, group, nq);
+    LocalArgs a{};
+    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, nq / group, max_n, ring,
+                                a.places);
+    if (st == IDX_OK) st = turn_args(fn, row_dim(IDX_ROWS_LOCAL), pos, freq, rot, offset, layout, mscale, 1, a.turn);
+    if (st != IDX_OK) return st;
+    REQUIRE(rows <= INT32_MAX, IDX_EUNSUPPORTED, "%s: rows=%lld out of [0, 2^31 - 1]", fn, (long long)rows);
+    REQUIRE(window >= 0, IDX_EINVAL, "%s: window=%lld is negative", fn, (long long)window);
+    REQUIRE(!ring || (window >= 1 && window <= ring - (group - 1)), IDX_EINVAL,
+            "%s: ring=%lld must hold window=%lld + group - 1=%d entries", fn, (long long)ring, (long long)window, group - 1);
+    REQUIRE(isfinite(scale), IDX_EINVAL, "%s: scale is not finite", fn);
+    REQUIRE(seq_stride >= 0, IDX_EINVAL, "%s: seq_stride=%lld is negative", fn, (long long)seq_stride);
+    REQUIRE((other != nullptr) == (other_lse != nullptr), IDX_EINVAL, "%s: other and other_lse go together", fn);
+    if (nq == 0) return ok();
+    REQUIRE(q && n_vis && out && (rows == 0 || (codes && scales)) && (!freq || pos), IDX_EINVAL, "%s: null pointer", fn);
+    REQUIRE(kv_base || pages, IDX_EINVAL, "%s: give either kv_base or pages", fn);
+    REQUIRE(ws && ws_bytes >= 16, IDX_EWORKSPACE, "%s: workspace %zu bytes, need at least 16", fn, ws_bytes);
+    REQUIRE(aligned(q, 16) && aligned(codes, 16) && aligned(scales, 4) && aligned(n_vis, 4) && aligned(other, 16) &&
+                aligned(other_lse, 4) && aligned(out, 16) && aligned(lse, 4) && aligned(ws, 16),
+            IDX_EALIGN, "%s: misaligned pointer", fn);
+    a.q = q;
+    a.nq = nq;
+    a.heads = heads;
+    a.group = group;
+    a.codes = codes;
+    a.scales = scales;
+    a.seq_stride = seq_stride;
+    a.n_vis = n_vis;
+    a.window = window;
+    a.scale = scale;
+    a.other = other;
+    a.other_lse = other_lse;
+    a.out = out;
+    a.lse = lse;
+    return hip_status(launch_attend_local(a, ws, ws_bytes, (hipStream_t)stream), fn);
+}
+
 constexpr int kMaxDevices = 64;
 struct DeviceScratch {
     void* ptr;             // device address of this device's `scratch`
@@ -713,42 +760,21 @@ idx_status idx_attend_local(const uint16_t* q, int32_t nq, int32_t heads, int32_
                             const uint16_t* other, const float* other_lse, const int64_t* pos, const double* freq,
                             int32_t rot, int32_t offset, int32_t layout, double mscale, uint16_t* out, float* lse,
                             void* ws, size_t ws_bytes, void* stream) {
-    const char* fn = "idx_attend_local";
-    REQUIRE(nq >= 0 && nq <= kMaxQueries, IDX_EUNSUPPORTED, "%s: nq=%d out of [0, 65535]", fn, nq);
-    REQUIRE(heads >= 1 && heads <= kMaxAttendHeads, IDX_EUNSUPPORTED, "%s: heads=%d out of [1, 128]", fn, heads);
-    REQUIRE(group >= 1 && nq % group == 0, IDX_EINVAL, "%s: group=%d must divide nq=%d", fn, group, nq);
-    LocalArgs a{};
-    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, nq / group, max_n, ring,
-                                a.places);
-    if (st == IDX_OK) st = turn_args(fn, row_dim(IDX_ROWS_LOCAL), pos, freq, rot, offset, layout, mscale, 1, a.turn);
-    if (st != IDX_OK) return st;
-    REQUIRE(rows <= INT32_MAX, IDX_EUNSUPPORTED, "%s: rows=%lld out of [0, 2^31 - 1]", fn, (long long)rows);
-    REQUIRE(window >= 0, IDX_EINVAL, "%s: window=%lld is negative", fn, (long long)window);
-    REQUIRE(!ring || (window >= 1 && window <= ring - (group - 1)), IDX_EINVAL,
-            "%s: ring=%lld must hold window=%lld + group - 1=%d entries", fn, (long long)ring, (long long)window, group - 1);
-    REQUIRE(isfinite(scale), IDX_EINVAL, "%s: scale is not finite", fn);
-    REQUIRE((other != nullptr) == (other_lse != nullptr), IDX_EINVAL, "%s: other and other_lse go together", fn);
-    if (nq == 0) return ok();
-    REQUIRE(q && n_vis && out && (rows == 0 || (codes && scales)) && (!freq || pos), IDX_EINVAL, "%s: null pointer", fn);
-    REQUIRE(kv_base || pages, IDX_EINVAL, "%s: give either kv_base or pages", fn);
-    REQUIRE(ws && ws_bytes >= 16, IDX_EWORKSPACE, "%s: workspace %zu bytes, need at least 16", fn, ws_bytes);
-    REQUIRE(aligned(q, 16) && aligned(codes, 16) && aligned(scales, 4) && aligned(n_vis, 4) && aligned(other, 16) &&
-                aligned(other_lse, 4) && aligned(out, 16) && aligned(lse, 4) && aligned(ws, 16),
-            IDX_EALIGN, "%s: misaligned pointer", fn);
-    a.q = q;
-    a.nq = nq;
-    a.heads = heads;
-    a.group = group;
-    a.codes = codes;
-    a.scales = scales;
-    a.n_vis = n_vis;
-    a.window = window;
-    a.scale = scale;
-    a.other = other;
-    a.other_lse = other_lse;
-    a.out = out;
-    a.lse = lse;
-    return hip_status(launch_attend_local(a, ws, ws_bytes, (hipStream_t)stream), fn);
+    return attend_local("idx_attend_local", q, nq, heads, group, codes, scales, rows, kv_base, pages, pages_stride, nseq,
+                        page_size, seq, 1, n_vis, max_n, window, ring, scale, other, other_lse, pos, freq, rot, offset,
+                        layout, mscale, out, lse, ws, ws_bytes, stream);
+}
+
+idx_status idx_attend_local_strided(const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
+                                    const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                                    int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq,
+                                    int64_t seq_stride, const int32_t* n_vis, int64_t max_n, int64_t window, int64_t ring,
+                                    float scale, const uint16_t* other, const float* other_lse, const int64_t* pos,
+                                    const double* freq, int32_t rot, int32_t offset, int32_t layout, double mscale,
+                                    uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return attend_local("idx_attend_local_strided", q, nq, heads, group, codes, scales, rows, kv_base, pages, pages_stride,
+                        nseq, page_size, seq, seq_stride, n_vis, max_n, window, ring, scale, other, other_lse, pos, freq, rot,
+                        offset, layout, mscale, out, lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -314,7 +314,7 @@ __global__ __launch_bounds__(256, kLocalPair<NH> ? 2 : 1) void attend_local_kern
     int64_t base = 0;
     const int32_t* pages = nullptr;
     if (PAGED) {
-        const int64_t s = a.places.seq ? (int64_t)a.places.seq[run] : run;
+        const int64_t s = a.places.seq ? (int64_t)a.places.seq[run * a.seq_stride] : run;
         if (s < 0 || s >= a.places.nseq)
             sp.count = 0;
         else
@@ -921,7 +921,7 @@ __global__ __launch_bounds__(64 * kWinWaves) void attend_window_kernel(const Loc
     int64_t base = 0, s = 0;
     bool cached = a.places.rows > 0;
     if (a.places.pages) {
-        s = a.places.seq ? (int64_t)a.places.seq[run] : run;
+        s = a.places.seq ? (int64_t)a.places.seq[run * a.seq_stride] : run;
         cached &= s >= 0 && s < a.places.nseq;
     } else if (a.places.base) {
         base = a.places.base[run];
@@ -1229,7 +1229,7 @@ __global__ __launch_bounds__(512) void attend_one_kernel(const LocalArgs a, int 
     const int count = see.y - see.x;
     int32_t row = -1;  // of entry 16 w + c
     if (16 * w + c < count && a.places.rows > 0)
-        row = (int32_t)row_at(a.places, a.places.seq ? (int64_t)a.places.seq[run] : run, a.places.base ? a.places.base[run] : 0,
+        row = (int32_t)row_at(a.places, a.places.seq ? (int64_t)a.places.seq[run * a.seq_stride] : run, a.places.base ? a.places.base[run] : 0,
                               (int64_t)see.x + 16 * w + c);
     // two rows at a time, whole
     uint4 code[8];

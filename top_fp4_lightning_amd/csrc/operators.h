@@ -144,7 +144,8 @@ struct LocalArgs {
     int32_t group;          // consecutive queries of one sequence
     const uint8_t* codes;
     const uint8_t* scales;
-    Places places;          // base and seq by run of `group` queries
+    Places places;          // base and seq by run of `group` queries,
+    int64_t seq_stride;     // run i's sequence at seq[i * seq_stride]
     const int32_t* n_vis;
     int64_t window;         // the last `window` visible entries; 0 is all
     float scale;

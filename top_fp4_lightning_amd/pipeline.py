@@ -475,7 +475,7 @@ class LayerAttention:
         query sees itself) -> out, lse, the values turned back to the query's frame."""
         core = self.core
         core.run(q, pos, seq, n_vis, idx, stream=stream)
-        runs = seq if self.group == 1 else seq.view(-1, self.group)[:, 0].contiguous()
+        runs = seq if self.group == 1 else seq[::self.group]  # (a view: recorded and captured calls read seq itself)
         return idx_attend_local(core.q, self.codes, self.scales, n_local, self.MOST, core.scale, self.out, self.ws,
                                 lse=self.lse, window=self.window, ring=self.ring, group=self.group, pages=self.own,
                                 page_size=self.ring, seq=runs, other=core.out, other_lse=core.lse, pos=pos, freq=core.freq,
