@@ -583,6 +583,17 @@ idx_status idx_write_rows(int32_t format, const void* x, int32_t dtype, int64_t 
                           int64_t max_n, int64_t ring, void* stream);
 
 /*
+ * idx_write_rows_kept: the same for the tokens with keep[i] >= 0 (device int64 [tokens], or NULL: for all). The others are
+ * left out, whatever their at[i]: a batch's idle slots.
+ */
+idx_status idx_write_rows_kept(int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, int32_t norm,
+                               const float* gamma, double eps, const int64_t* pos, const double* freq, int32_t rot,
+                               int32_t offset, int32_t layout, double mscale, const int8_t* signs, uint8_t* codes,
+                               uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                               int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int64_t* at,
+                               int64_t max_n, int64_t ring, const int64_t* keep, void* stream);
+
+/*
  * idx_read_rows: the stored rows of entries at[i], as values: a code times its scale, exact in both output types, and
  * with freq turned as by idx_rope (inverse != 0: back; not for keys, which are stored transformed), in fp32 and rounded
  * once. Arguments as above; codes 8-byte aligned at least, and

@@ -122,3 +122,61 @@ def test_recorded_steps(fx, pl, group):
         out, lse = layer.run(*given)
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+@pytest.mark.parametrize("format, dim, width, groups", [("main", 512, 256, 32), ("local", 512, 512, 16), ("key", 128, 64, 4)])
+@pytest.mark.parametrize("tokens", [1, 9, 700])
+def test_kept_rows(fx, format, dim, width, groups, tokens):
+    """the tokens that are kept are stored as without the others, and no other row is written"""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    x = torch.randn(tokens, dim, device="cuda", generator=g)
+    at = torch.randperm(tokens + 5, device="cuda", generator=g)[:tokens]
+    keep = torch.randint(-(1 << 40), 1 << 40, (tokens,), device="cuda", generator=g)
+    keep[0] = 0
+    if tokens > 1:
+        keep[-1] = -1
+        at[-1] = at[0]  # an idle slot at a real token's entry
+    signs = (torch.randint(0, 2, (128,), device="cuda", generator=g) * 2 - 1).to(torch.int8)
+    some = (keep >= 0).nonzero().flatten()
+    caches = []
+    for rows, places, k in ((x, at, keep), (x[some], at[some], None), (x[some], at[some], at[some])):
+        codes = torch.full((tokens + 5, width), 0xA5, dtype=torch.uint8, device="cuda")
+        scales = torch.full((tokens + 5, groups), 0xA5, dtype=torch.uint8, device="cuda")
+        fx.idx_write_rows(format, rows, codes, scales, places, tokens + 5, eps=1e-6, signs=signs, keep=k)
+        caches.append((codes, scales))
+    for codes, scales in caches[1:]:
+        assert torch.equal(codes, caches[0][0]) and torch.equal(scales, caches[0][1])
+    assert (caches[0][0] != 0xA5).any(1).sum() == len(some)
+
+
+def test_idle_slots_with_positions(pl):
+    """a compressed cache: entries and positions differ, and a padded batch's idle slots name positions that live rows of
+    their sequence's ring have"""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    layer = make_plan(pl, g, 3, 2)
+    core = layer.core
+    before = [t.clone() for t in (core.codes, core.scales, layer.codes, layer.scales, layer.k_codes, layer.k_scales)]
+    seq = torch.tensor([0, 0, 1, 2, 2], dtype=torch.int32, device="cuda")
+    at = torch.tensor([10, -1, -1, 11, -5], device="cuda")
+    pos = torch.tensor([40, 39, 25, 41, 41], device="cuda")
+    x, k = torch.randn(5, 512, device="cuda", generator=g), torch.randn(5, 128, device="cuda", generator=g)
+    layer.write(seq, at, main=x, local=x, key=k, pos=pos)
+    now = (core.codes, core.scales, layer.codes, layer.scales, layer.k_codes, layer.k_scales)
+    local = [0 * layer.ring + 40 % layer.ring, 2 * layer.ring + 41 % layer.ring]
+    main = [int(core.pages[b, e // 16]) * 16 + e % 16 for b, e in ((0, 10), (2, 11))]
+    key = [0 * core.n + 10, 2 * core.n + 11]
+    for i, rows in enumerate((main, main, local, local, key, key)):
+        changed = (now[i] != before[i]).any(1).nonzero().flatten().tolist()
+        assert set(changed) <= set(rows), i  # (a scale may come out as it was)
+        if i % 2 == 0:
+            assert changed == sorted(rows)
+    live = [0, 3]  # and they hold what a call without the idle slots stores
+    for t in now:
+        t.zero_()
+    layer.write(seq, at, main=x, local=x, key=k, pos=pos)
+    padded = [t.clone() for t in now]
+    for t in now:
+        t.zero_()
+    layer.write(seq[live], at[live], main=x[live], local=x[live], key=k[live], pos=pos[live])
+    for a, b in zip(now, padded):
+        assert torch.equal(a, b)

@@ -2,9 +2,10 @@
 import pytest
 import torch
 
-from test_abi import call, fx  # noqa: F401
+import rows_ref
+from test_abi import FAKE, call, fx  # noqa: F401
 from test_operator_args import refuse
-from test_rows_args import L, LOCAL
+from test_rows_args import L, LOCAL, W, WRITE
 
 
 @pytest.fixture
@@ -68,3 +69,41 @@ def test_binding_refuses_other_views(fx):
         with pytest.raises(error):
             fx.idx_attend_local(q, codes, torch.zeros(10, 16, dtype=torch.uint8), torch.zeros(6, dtype=torch.int32), 10, 1.0,
                                 q.clone(), torch.zeros(16, dtype=torch.uint8), group=2, pages=pages, page_size=10, seq=bad)
+
+
+def written(args, kw, max_n, rows):
+    """{token: cache row} of a call, by the definition"""
+    at, keep = kw["at"], kw.get("keep")
+    where = dict(pages=kw["pages"].numpy(), page_size=kw["page_size"], seq=kw["seq"].numpy(), ring=kw.get("ring", 0))
+    found = {t: rows_ref.row_of(t, at, max_n, rows, **where) for t in range(len(at)) if keep is None or keep[t] >= 0}
+    return {t: r for t, r in found.items() if r >= 0}
+
+
+@pytest.mark.parametrize("compressed", [False, True])
+def test_tokens_that_are_left_out(calls, compressed):
+    """a token at an entry below 0 is written to none of the caches, with or without positions of its own"""
+    pl, made = calls
+    layer = plan(pl, 3, 1, signs=torch.ones(128, dtype=torch.int8))
+    for b in range(3):
+        layer.core.reserve(b, 20)
+    at = torch.tensor([5, -1, 7, -1, 0])
+    pos = torch.tensor([20, 20, 29, 0, 3]) if compressed else None  # (an idle slot may name a real token's position)
+    seq = torch.tensor([0, 0, 1, 2, 2], dtype=torch.int32)
+    x = torch.zeros(5, 512)
+    layer.write(seq, at, main=x, local=x, key=x[:, :128], pos=pos)
+    rows = dict(main=len(layer.core.codes), local=len(layer.codes), key=len(layer.k_codes))
+    assert [args[0] for _, args, _ in made] == ["main", "local", "key"]
+    for _, args, kw in made:
+        kw["at"], max_n = args[4], args[5]
+        assert sorted(written(args, kw, max_n, rows[args[0]])) == [0, 2, 4], args[0]
+        assert args[0] != "local" or torch.equal(kw["at"], at if pos is None else pos)
+
+
+def test_kept_refusals(fx):
+    good = [*WRITE[:-1], FAKE, None]
+    refuse(fx, "idx_write_rows_kept", good, [(27, FAKE + 4, fx.IDX_EALIGN), (W["x"], None, fx.IDX_EINVAL),
+                                             (W["eps"], 0.0, fx.IDX_EINVAL), (W["format"], 3, fx.IDX_EUNSUPPORTED)])
+    codes, at = torch.zeros(10, 512, dtype=torch.uint8), torch.zeros(3, dtype=torch.int64)
+    for keep, error in ((at[:2], ValueError), (at.int(), TypeError), (at.repeat(2)[::2], ValueError), (at, ValueError)):
+        with pytest.raises(error):  # (the last: not on a GPU)
+            fx.idx_write_rows("local", torch.zeros(3, 512), codes, codes[:, :16].contiguous(), at, 10, keep=keep)

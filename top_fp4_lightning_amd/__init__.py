@@ -52,6 +52,7 @@ lib.idx_distill.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, 
 lib.idx_distill_bwd.argtypes = [_P, _i64, _P, _i32, _i64, _P, _P, _i64, _i32, _f32, _P, _P, _P, _P, _i64, _P]
 lib.idx_write_rows.argtypes = [_i32, _P, _i32, _i64, _i64, _i32, _P, _f64, _P, _P, _i32, _i32, _i32, _f64, _P, _P, _P, _i64,
                                _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _P]
+lib.idx_write_rows_kept.argtypes = [*lib.idx_write_rows.argtypes[:-1], _P, _P]
 lib.idx_read_rows.argtypes = [_i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _P, _P, _i32, _i32,
                               _i32, _f64, _i32, _P, _i32, _i64, _P]
 lib.idx_attend_local.argtypes = [_P, _i32, _i32, _i32, _P, _P, _i64, _P, _P, _i64, _i32, _i32, _P, _P, _i64, _i64, _i64, _f32,
@@ -61,7 +62,7 @@ for _f in ("idx_quantize_q", "idx_score_full", "idx_build_pool", "idx_build_pool
            "idx_score_pool_gather", "idx_topk",
            "idx_quantize_kv", "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope",
            "idx_attend", "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows",
-           "idx_attend_local", "idx_attend_local_strided"):
+           "idx_attend_local", "idx_attend_local_strided", "idx_write_rows_kept"):
     getattr(lib, _f).restype = _i32
 
 EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quantize_q", "idx_score_full",
@@ -69,7 +70,7 @@ EXPORTS = ("idx_abi_version", "idx_last_error", "idx_workspace_size", "idx_quant
            "idx_quantize_kv",
            "idx_gather_kv", "idx_mask_pool", "idx_topk_pool", "idx_rope_freqs", "idx_rope", "idx_attend",
            "idx_attend_weights", "idx_distill", "idx_distill_bwd", "idx_write_rows", "idx_read_rows", "idx_attend_local",
-           "idx_attend_local_strided")
+           "idx_attend_local_strided", "idx_write_rows_kept")
 MKV_DIM = 512
 
 
@@ -596,11 +597,12 @@ def _value_rows(x, tokens, dim, name) -> tuple:
 
 def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, pages=None, page_size: int = 0, seq=None,
                    ring: int = 0, gamma=None, eps: float | None = None, pos=None, freq=None, offset: int | None = None,
-                   layout: str = "half", mscale: float = 1.0, signs=None, stream=None):
+                   layout: str = "half", mscale: float = 1.0, signs=None, keep=None, stream=None):
     """Rows x [tokens, 512] (keys: 128; bf16 or fp32, any row stride), normalised (with eps; times gamma), turned by
     pos (default: at) * freq, quantised in the cache's format ("main", "local" or "key") and stored in codes and scales
     at entries at [tokens] (int64) below max_n: rows kv_base [tokens] + entry, or of pages [nseq, ...] of page_size
-    (seq [tokens] names the page row); with ring, entry % ring takes the entry's place."""
+    (seq [tokens] names the page row); with ring, entry % ring takes the entry's place. Tokens with keep [tokens] (int64)
+    below 0 are left out."""
     number, dim, codes_ptr, scales_ptr, rows = _row_format(format, codes, scales)
     if at.dtype is not _I64 or at.dim() != 1 or not at.is_contiguous():
         _arg(at, _I64, (at.numel(),), "at")
@@ -612,9 +614,12 @@ def idx_write_rows(format: str, x, codes, scales, at, max_n: int, kv_base=None, 
         raise ValueError("gamma needs eps")
     gamma_ptr = None if gamma is None else _arg(gamma, _F32, (dim,), "gamma")
     signs_ptr = None if signs is None else _arg(signs, torch.int8, (DIM,), "signs")
-    _same_gpu(codes, scales, x, at, kv_base, pages, seq, pos, freq, gamma, signs)
-    _call(lib.idx_write_rows, number, x_ptr, dtype, tokens, stride, int(eps is not None), gamma_ptr, eps or 0.0, *turn,
-          mscale, signs_ptr, codes_ptr, scales_ptr, rows, *where, at.data_ptr(), max_n, ring, _stream(stream))
+    fn, kept = lib.idx_write_rows, ()
+    if keep is not None:
+        fn, kept = lib.idx_write_rows_kept, (_arg(keep, _I64, (tokens,), "keep"),)
+    _same_gpu(codes, scales, x, at, kv_base, pages, seq, pos, freq, gamma, signs, keep)
+    _call(fn, number, x_ptr, dtype, tokens, stride, int(eps is not None), gamma_ptr, eps or 0.0, *turn, mscale, signs_ptr,
+          codes_ptr, scales_ptr, rows, *where, at.data_ptr(), max_n, ring, *kept, _stream(stream))
     return codes, scales
 
 

@@ -226,6 +226,33 @@ idx_status rows_args(const char* fn, int32_t format, const void* x, int32_t dtyp
 }
 constexpr int32_t row_dim(int32_t format) { return format == IDX_ROWS_KEY ? kDim : 512; }
 
+// idx_write_rows, tokens left out where keep is below 0 (null: none)
+idx_status write_rows(const char* fn, int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t x_stride,
+                      int32_t norm, const float* gamma, double eps, const int64_t* pos, const double* freq, int32_t rot,
+                      int32_t offset, int32_t layout, double mscale, const int8_t* signs, uint8_t* codes, uint8_t* scales,
+                      int64_t rows, const int64_t* kv_base, const int32_t* pages, int64_t pages_stride, int32_t nseq,
+                      int32_t page_size, const int32_t* seq, const int64_t* at, int64_t max_n, int64_t ring,
+                      const int64_t* keep, void* stream) {
+    RowsArgs a{};
+    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, tokens, max_n, ring, a.places);
+    if (st == IDX_OK) st = rows_args(fn, format, x, dtype, tokens, x_stride, codes, scales, at, a);
+    if (st == IDX_OK) st = turn_args(fn, row_dim(format), pos, freq, rot, offset, layout, mscale, 0, a.turn);
+    if (st != IDX_OK) return st;
+    REQUIRE(!norm || (isfinite(eps) && eps > 0.0), IDX_EINVAL, "%s: eps must be finite and above 0", fn);
+    REQUIRE(x_stride >= 0, IDX_EINVAL, "%s: x_stride=%lld is negative", fn, (long long)x_stride);
+    if (tokens == 0 || rows == 0) return ok();
+    REQUIRE(format != IDX_ROWS_KEY || signs, IDX_EINVAL, "%s: keys need signs", fn);
+    REQUIRE(aligned(codes, 16) && aligned(gamma, 4) && aligned(keep, 8) && (format != IDX_ROWS_KEY || aligned(signs, 16)),
+            IDX_EALIGN, "%s: codes and signs must be 16-byte aligned, keep 8-byte, gamma 4-byte", fn);
+    a.x = x;
+    a.norm = norm != 0;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.signs = signs;
+    a.keep = keep;
+    return hip_status(launch_write_rows(a, (hipStream_t)stream), fn);
+}
+
 // idx_attend_local, run i's sequence seq_stride numbers behind the one before
 idx_status attend_local(const char* fn, const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
                         const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
@@ -713,24 +740,20 @@ idx_status idx_write_rows(int32_t format, const void* x, int32_t dtype, int64_t 
                           uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
                           int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int64_t* at,
                           int64_t max_n, int64_t ring, void* stream) {
-    const char* fn = "idx_write_rows";
-    RowsArgs a{};
-    idx_status st = places_args(fn, rows, kv_base, pages, pages_stride, nseq, page_size, seq, tokens, max_n, ring, a.places);
-    if (st == IDX_OK) st = rows_args(fn, format, x, dtype, tokens, x_stride, codes, scales, at, a);
-    if (st == IDX_OK) st = turn_args(fn, row_dim(format), pos, freq, rot, offset, layout, mscale, 0, a.turn);
-    if (st != IDX_OK) return st;
-    REQUIRE(!norm || (isfinite(eps) && eps > 0.0), IDX_EINVAL, "%s: eps must be finite and above 0", fn);
-    REQUIRE(x_stride >= 0, IDX_EINVAL, "%s: x_stride=%lld is negative", fn, (long long)x_stride);
-    if (tokens == 0 || rows == 0) return ok();
-    REQUIRE(format != IDX_ROWS_KEY || signs, IDX_EINVAL, "%s: keys need signs", fn);
-    REQUIRE(aligned(codes, 16) && aligned(gamma, 4) && (format != IDX_ROWS_KEY || aligned(signs, 16)), IDX_EALIGN,
-            "%s: codes and signs must be 16-byte aligned, gamma 4-byte", fn);
-    a.x = x;
-    a.norm = norm != 0;
-    a.gamma = gamma;
-    a.eps = eps;
-    a.signs = signs;
-    return hip_status(launch_write_rows(a, (hipStream_t)stream), fn);
+    return write_rows("idx_write_rows", format, x, dtype, tokens, x_stride, norm, gamma, eps, pos, freq, rot, offset, layout,
+                      mscale, signs, codes, scales, rows, kv_base, pages, pages_stride, nseq, page_size, seq, at, max_n, ring,
+                      nullptr, stream);
+}
+
+idx_status idx_write_rows_kept(int32_t format, const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, int32_t norm,
+                               const float* gamma, double eps, const int64_t* pos, const double* freq, int32_t rot,
+                               int32_t offset, int32_t layout, double mscale, const int8_t* signs, uint8_t* codes,
+                               uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
+                               int64_t pages_stride, int32_t nseq, int32_t page_size, const int32_t* seq, const int64_t* at,
+                               int64_t max_n, int64_t ring, const int64_t* keep, void* stream) {
+    return write_rows("idx_write_rows_kept", format, x, dtype, tokens, x_stride, norm, gamma, eps, pos, freq, rot, offset,
+                      layout, mscale, signs, codes, scales, rows, kv_base, pages, pages_stride, nseq, page_size, seq, at,
+                      max_n, ring, keep, stream);
 }
 
 idx_status idx_read_rows(int32_t format, const uint8_t* codes, const uint8_t* scales, int64_t rows,

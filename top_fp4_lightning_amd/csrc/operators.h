@@ -133,6 +133,7 @@ struct RowsArgs {
     const float* gamma;     // may be null
     double eps;
     const int8_t* signs;    // keys
+    const int64_t* keep;    // write: below 0 where a token is left out; may be null
     void* out;              // read
     int64_t stride;         // of x or out
 };

@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void write_rows_kernel(const RowsArgs a) {
     const int rot = a.turn.rot, pairs = a.turn.freq ? rot / 2 : 0, offset = a.turn.offset;
     Raw raw;
     load16<F32>(a, tc, 16 * li, raw);
-    const int64_t at = a.at[tc];
+    const int64_t at = a.at[tc], keep = a.keep ? a.keep[tc] : 0;
     constexpr int kAhead = kKey ? 4 : 1;  // pairs of a lane whose frequencies are read ahead
     double freq[kAhead];
 #pragma unroll
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(256) void write_rows_kernel(const RowsArgs a) {
     uint4 signs{};
     if constexpr (kKey) signs = reinterpret_cast<const uint4*>(a.signs)[li];
     int64_t row = row_at(a.places, a.places.seq ? a.places.seq[tc] : tc, a.places.base ? a.places.base[tc] : 0, at);
-    if (!live) row = -1;
+    if (!live || keep < 0) row = -1;
     // this lane's values among the turned ones: first .. last - 1
     const int first = pairs ? max(offset - 16 * li, 0) : 16, last = pairs ? min(offset + rot - 16 * li, 16) : 16;
     float f[16];

@@ -454,7 +454,8 @@ class LayerAttention:
         None, of sequences seq [tokens] (int32) at entries at [tokens] (int64), turned by pos [tokens] (default: at).
         Entries of one call's main rows and keys are those of a cache compressed along the sequence where pos is given;
         local rows are one a position and go by pos then, of each sequence at most `ring` a call (the last of a prefill).
-        Tokens at entries below 0 are left out."""
+        Tokens at entries below 0 are left out of all of them, whatever their pos (a batch's idle slots; a position that
+        has a local row and ends no compressed entry is written by a call of its own, at = its position)."""
         core = self.core
         norm = dict(gamma=self.gamma, eps=self.eps)
         turn = dict(pos=pos, freq=core.freq, layout=core.layout, mscale=core.mscale)
@@ -463,7 +464,8 @@ class LayerAttention:
                            seq=seq, stream=stream, **norm, **turn)
         if local is not None:
             idx_write_rows("local", local, self.codes, self.scales, at if pos is None else pos, self.MOST, pages=self.own,
-                           page_size=self.ring, seq=seq, ring=self.ring, stream=stream, **norm, **turn)
+                           page_size=self.ring, seq=seq, ring=self.ring, keep=None if pos is None else at, stream=stream,
+                           **norm, **turn)
         if key is not None:
             # (the indexer's keys carry their position, too: the rotated part at the end of the row)
             idx_write_rows("key", key, self.k_codes, self.k_scales, at, core.n, pages=self.own, page_size=core.n, seq=seq,
