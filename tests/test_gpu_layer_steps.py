@@ -180,3 +180,46 @@ def test_idle_slots_with_positions(pl):
     layer.write(seq[live], at[live], main=x[live], local=x[live], key=k[live], pos=pos[live])
     for a, b in zip(now, padded):
         assert torch.equal(a, b)
+
+
+def test_fewer_queries_than_the_plan_has(pl):
+    """single queries of different sequences in a plan for draft positions: as in a plan for single queries"""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    big, one = make_plan(pl, g, 2, 3), make_plan(pl, g, 6, 1)
+    # the same rows of two sequences in both
+    for layer in (big, one):
+        g.manual_seed(6)
+        for b in range(2):
+            x = torch.randn(40, 512, device="cuda", generator=g).bfloat16()
+            at, seq = torch.arange(40, device="cuda"), torch.full((40,), b, dtype=torch.int32, device="cuda")
+            layer.write(seq, at, main=x)
+            layer.write(seq[-layer.ring:], at[-layer.ring:], local=x[-layer.ring:])
+    seq = torch.tensor([0, 1, 1, 1, 0, 1], dtype=torch.int32, device="cuda")
+    pos = torch.full((6,), 39, device="cuda")
+    n_vis = (pos + 1).int()
+    idx = (torch.rand(6, 8, device="cuda", generator=g) * 40).int()
+    q = torch.randn(big.core.q.shape, device="cuda", generator=g).bfloat16()
+    got = big.run(q, pos, seq, n_vis, idx, n_vis, group=1)
+    want = one.run(q, pos, seq, n_vis, idx, n_vis)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.isfinite(got[1]).all()
+
+
+def test_a_padded_run(pl):
+    """a sequence with fewer queries than the step: the padding gives nothing, and what it holds has no effect"""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    layer = make_plan(pl, g, 3, 3)
+    q, pos, seq, n_vis, idx, n_local = a_step(layer, g, [2, 0, 1])
+    idle = [4, 5, 8]
+    n_vis[idle] = 0
+    n_local[idle] = 0
+    rest = [t for t in range(9) if t not in idle]
+    outs = []
+    for _ in range(2):
+        out, lse = layer.run(q, pos, seq, n_vis, idx, n_local)
+        assert (out[idle] == 0).all() and torch.isneginf(lse[idle]).all()
+        outs.append((out[rest].clone(), lse[rest].clone()))
+        q[idle], pos[idle], idx[idle] = torch.nan, 7, 3
+        seq[idle] = -1
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.isfinite(outs[0][1]).all()

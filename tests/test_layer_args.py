@@ -107,3 +107,19 @@ def test_kept_refusals(fx):
     for keep, error in ((at[:2], ValueError), (at.int(), TypeError), (at.repeat(2)[::2], ValueError), (at, ValueError)):
         with pytest.raises(error):  # (the last: not on a GPU)
             fx.idx_write_rows("local", torch.zeros(3, 512), codes, codes[:, :16].contiguous(), at, 10, keep=keep)
+
+
+def test_queries_of_a_step(calls):
+    """a plan for three draft positions takes steps of fewer: every query goes to its own sequence's ring"""
+    pl, made = calls
+    layer = plan(pl, 2, 3)
+    seq = torch.tensor([1, 0, 1, 1, 0, 0], dtype=torch.int32)
+    for group in (1, 2, 3, None):
+        layer.run(*step(layer, seq), group=group)
+        kw = made[-1][2]
+        assert kw["group"] == (group or 3) and kw["seq"].tolist() == seq[::kw["group"]].tolist()
+    made.clear()
+    for group in (0, 4, -1):
+        with pytest.raises(ValueError):
+            layer.run(*step(layer, seq), group=group)
+    assert not made

@@ -423,8 +423,9 @@ class CoreAttention:
 class LayerAttention:
     """A layer's attention over its selection (`core`'s cache) and its last `window` positions, which lie in a ring of FP8
     rows for each sequence, and the layer's caches as a step writes them: main rows, local rows and the indexer's keys.
-    Steps have up to `group` consecutive queries of a sequence (1, or the draft positions). gamma and eps: the norm of the
-    rows before they are turned (none without eps); signs: the indexer's, for its keys.
+    Steps have up to `group` consecutive queries of a sequence (1, or the draft positions), in one step the same number of
+    each: run is told it, and a sequence that has fewer is padded behind them (n_vis and n_local 0). gamma and eps: the
+    norm of the rows before they are turned (none without eps); signs: the indexer's, for its keys.
 
     Everything here can be captured: a step writes its rows at entries that the device names and attends to them. Pages
     of the main cache are reserved ahead (core.reserve)."""
@@ -471,15 +472,20 @@ class LayerAttention:
             idx_write_rows("key", key, self.k_codes, self.k_scales, at, core.n, pages=self.own, page_size=core.n, seq=seq,
                            signs=self.signs, stream=stream, **turn)
 
-    def run(self, q, pos, seq, n_vis, idx, n_local, stream=None):
+    def run(self, q, pos, seq, n_vis, idx, n_local, stream=None, group=None):
         """q [nq, heads, 512] (bf16, not rotated) at positions pos [nq] of sequences seq [nq]: the attention over the
         selected entries idx [nq, k] below n_vis [nq] and over the last positions before n_local [nq] (pos + 1, where a
-        query sees itself) -> out, lse, the values turned back to the query's frame."""
+        query sees itself) -> out, lse, the values turned back to the query's frame. Queries come in runs of `group`
+        (default: the plan's; at most it) of one sequence, the one that seq gives a run's first query; 1 where every query
+        is by itself."""
         core = self.core
+        group = self.group if group is None else group
+        if not 1 <= group <= self.group:
+            raise ValueError(f"group={group} must be 1 .. {self.group}, which the rings are made for")
         core.run(q, pos, seq, n_vis, idx, stream=stream)
-        runs = seq if self.group == 1 else seq[::self.group]  # (a view: recorded and captured calls read seq itself)
+        runs = seq if group == 1 else seq[::group]  # (a view: recorded and captured calls read seq itself)
         return idx_attend_local(core.q, self.codes, self.scales, n_local, self.MOST, core.scale, self.out, self.ws,
-                                lse=self.lse, window=self.window, ring=self.ring, group=self.group, pages=self.own,
+                                lse=self.lse, window=self.window, ring=self.ring, group=group, pages=self.own,
                                 page_size=self.ring, seq=runs, other=core.out, other_lse=core.lse, pos=pos, freq=core.freq,
                                 layout=core.layout, mscale=1.0 / core.mscale, stream=stream)
 
