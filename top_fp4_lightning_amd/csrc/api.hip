@@ -291,7 +291,7 @@ idx_status attend_local(const char* fn, const uint16_t* q, int32_t nq, int32_t h
     a.scales = scales;
     a.seq_stride = seq_stride;
     a.n_vis = n_vis;
-    a.window = window;
+    a.window = window < kMaxN ? window : kMaxN;  // (no range is longer, and the kernel's sums with it fit)
     a.scale = scale;
     a.other = other;
     a.other_lse = other_lse;
