@@ -1309,6 +1309,9 @@ __global__ __launch_bounds__(512) void attend_one_kernel(const LocalArgs a, int 
             *reinterpret_cast<h4*>(&sh.p[w][c][4 * g]) = p;
             if (g == 0) sh.m[c][w] = top > ninf() ? R : kNone, sh.l[c][w] = l;
         }
+        // other_lse may be lse, which the first wavefront writes behind the barrier: every wavefront's read of it ends before
+        // (a barrier waits for LDS alone; the wait that the join has right behind it stands here instead)
+        asm volatile("" : "+v"(l2));
         __syncthreads();
 
         // The wavefronts' references below the largest (none: far enough below). Their probabilities are brought to it in
