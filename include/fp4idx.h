@@ -561,8 +561,11 @@ idx_status idx_distill_bwd(const float* scores, int64_t score_stride, const int3
  *                 448 2^e >= the group's largest magnitude, code = E4M3 of y / 2^e, to nearest, ties to the even
  *                 code, 448 at most; zero is +0, a group of zeros has e = -15;
  * and stored in the row of its entry at[i]. Everything up to the codes is in 64 bits (the keys' transform ends with the
- * two fp32 roundings of idx_quantize_q), so a code is the nearest to the formula's value except within 2^-40 of it at a
- * border. One launch that reads its places on the device: a captured step can make it.
+ * two fp32 roundings of idx_quantize_q), so a code is the nearest to the formula's value but for the error of these 64
+ * bits: none in a row stored as it is; 2^-48 of a normalised value; 2^-47 (|y_0| + |y_1|) |mscale| of a value turned from
+ * y_0 and y_1, of the value itself far more where the products cancel; of a key's transformed values, before the two
+ * roundings, the row's sum of these and 2^-50 of its sum of magnitudes. One launch that reads its places on the device: a
+ * captured step can make it.
  *
  *   x       : device, dtype IDX_BF16 or IDX_F32 [tokens][x_stride], dim (512, 128) consecutive values, finite.
  *   gamma   : device fp32 [dim] or NULL (ones).   eps : above 0 with norm.
