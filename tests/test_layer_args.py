@@ -123,3 +123,12 @@ def test_queries_of_a_step(calls):
         with pytest.raises(ValueError):
             layer.run(*step(layer, seq), group=group)
     assert not made
+
+
+def test_keys_of_a_plan_without_signs(calls):
+    pl, made = calls
+    layer = plan(pl, 2, 1)
+    at, x = torch.zeros(2, dtype=torch.int64), torch.zeros(2, 512)
+    with pytest.raises(ValueError, match="signs"):
+        layer.write(at.int(), at, main=x, local=x, key=x[:, :128])
+    assert not made  # before anything is written

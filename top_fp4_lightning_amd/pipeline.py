@@ -457,6 +457,8 @@ class LayerAttention:
         local rows are one a position and go by pos then, of each sequence at most `ring` a call (the last of a prefill).
         Tokens at entries below 0 are left out of all of them, whatever their pos (a batch's idle slots; a position that
         has a local row and ends no compressed entry is written by a call of its own, at = its position)."""
+        if key is not None and self.signs is None:
+            raise ValueError("a layer without signs keeps no keys")
         core = self.core
         norm = dict(gamma=self.gamma, eps=self.eps)
         turn = dict(pos=pos, freq=core.freq, layout=core.layout, mscale=core.mscale)
