@@ -13,7 +13,7 @@
 // Under the tracer, writing takes 18 us for 32770 fp32 rows of the main KV, turned (76 MB at 4.3 TB/s), 13 for 16384 bf16 rows
 // of local positions, normalised and turned, 18 for 65537 keys: vector instructions fill two thirds to nine tenths of the time,
 // 24, 32 and 58 a value, a third of a key's for its pairs' sines and cosines. A fifth block on a compute unit changes nothing.
-// Reading them takes 12, 7 and 6 us. One row 3.2 and 2.2 us: launch, three loads one behind the other.
+// Reading them takes 12, 7 and 6 us. One row 3.2 and 1.9 us: launch, three loads one behind the other.
 #include "../../include/fp4idx.h"
 #include <type_traits>
 
@@ -560,8 +560,8 @@ hipError_t launch_write_rows(const RowsArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_read_rows(const RowsArgs& a, hipStream_t stream) {
-    // Two rows a lane where the wavefronts fill the card four times: 32768 rows of the main KV, turned, 13.8 -> 11.9 us (four
-    // rows 13.3, eight 14), 65536 23.5 -> 19.7; 8192 rows of local positions in fp32 7.0 us with one and 7.4 with two.
+    // Two rows a lane where the wavefronts fill the card four times: 32768 rows of the main KV, turned, replayed 15.3 us with one,
+    // 13.1 with two, 14.5 with four; 65536 26.5, 21.9, 22.4; 8192 rows of local positions in fp32 7.05, 7.25, 7.35.
     const int64_t lanes = a.tokens * (a.format == IDX_ROWS_KEY ? kDim : 512) / 8;
     if (lanes >= (int64_t)4 * 64 * 4096) {
         const dim3 grid((unsigned)((lanes + 511) / 512));
