@@ -650,8 +650,8 @@ idx_status idx_attend_local(const uint16_t* q, int32_t nq, int32_t heads, int32_
                             void* ws, size_t ws_bytes, void* stream);
 
 /*
- * idx_attend_local_strided: the same, run i's sequence at seq[i * seq_stride] (seq_stride >= 0; not looked at without
- * seq): of a step's sequences by query, those of its runs' first queries (seq_stride = group), read where they lie.
+ * idx_attend_local_strided: the same, run i's sequence at seq[i * seq_stride], seq_stride >= 0: of a step's sequences by
+ * query, those of its runs' first queries (seq_stride = group), read where they lie.
  */
 idx_status idx_attend_local_strided(const uint16_t* q, int32_t nq, int32_t heads, int32_t group, const uint8_t* codes,
                                     const uint8_t* scales, int64_t rows, const int64_t* kv_base, const int32_t* pages,
